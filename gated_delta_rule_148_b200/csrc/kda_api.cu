@@ -78,6 +78,45 @@ size_t spans_bytes(int num_seqs) {
   return (raw + 255) / 256 * 256;
 }
 
+// Sizes shared by the linear-attention calls; KDA_OK, or why they are refused.
+kda_status linear_sizes(int dtype, int B, int N, int H, int Hk, int dk, int dv, int decay) {
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (B < 0 || N < 0 || H < 1 || Hk < 1 || H % Hk != 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID_ARG;
+  if (decay != KDA_DECAY_TOKEN && decay != KDA_DECAY_HEAD) return KDA_ERR_INVALID_ARG;
+  if (!head_dim_ok(dk) || !head_dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+template <class A>
+LinearParams linear_params(const A *a) {
+  LinearParams p{};
+  p.num_seqs = a->num_seqs;
+  p.N = a->total_tokens;
+  p.H = a->H;
+  p.Hk = a->Hk;
+  p.dk = a->dk;
+  p.dv = a->dv;
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.log_alpha = a->log_alpha;
+  p.cu = a->cu_seqlens;
+  p.mask = a->pad_mask;
+  p.init_state = a->init_state;
+  p.decay_head = a->decay == KDA_DECAY_HEAD ? 1 : 0;
+  p.ws = a->workspace;
+  p.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
+  return p;
+}
+
+// Sizes shared by the norm and its backward pass.
+kda_status norm_sizes(int dtype, int64_t rows, int D, float eps) {
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (rows < 0 || D < 8 || D % 8 != 0 || !(eps >= 0.f) || !(eps <= 3.4e38f)) return KDA_ERR_INVALID_ARG;
+  if (D > 16384 || rows > 0x7FFFFFFF) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -85,7 +124,7 @@ using namespace kda;
 
 extern "C" {
 
-int kda_version(void) { return (1 << 16) | 1; }
+int kda_version(void) { return (1 << 16) | 2; }
 
 const char *kda_status_string(kda_status s) {
   switch (s) {
@@ -378,6 +417,217 @@ kda_status kda_prefill_backward(const kda_backward_args *a, void *stream) {
   p.err = err;
   p.gate_head = gate_head ? 1 : 0;
   return launch_backward(p, a->dtype == KDA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_linear_prefill_workspace_size(const kda_linear_args *a) {
+  if (!a || linear_sizes(a->dtype, a->num_seqs, a->total_tokens, a->H, a->Hk, a->dk, a->dv, a->decay) != KDA_OK)
+    return 0;
+  return linear_prefill_workspace(linear_params(a), a->dtype == KDA_BF16);
+}
+
+kda_status kda_linear_prefill(const kda_linear_args *a, void *stream) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  const kda_status ok =
+      linear_sizes(a->dtype, a->num_seqs, a->total_tokens, a->H, a->Hk, a->dk, a->dv, a->decay);
+  if (ok != KDA_OK) return ok;
+  if (a->num_seqs == 0) return a->total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+  const size_t N = (size_t)a->total_tokens, B = (size_t)a->num_seqs, H = (size_t)a->H, es = elem_bytes(a->dtype);
+  if (!a->cu_seqlens || !a->workspace) return KDA_ERR_INVALID_ARG;
+  if (N > 0 && (!a->log_alpha || !a->q || !a->k || !a->v || !a->o)) return KDA_ERR_INVALID_ARG;
+  LinearParams p = linear_params(a);
+  const bool bf16 = a->dtype == KDA_BF16;
+  if (a->workspace_bytes < linear_prefill_workspace(p, bf16)) return KDA_ERR_INVALID_ARG;
+  const void *need16[] = {a->q, a->k, a->v, a->o, a->init_state, a->final_state};
+  for (const void *x : need16)
+    if (x && !aligned(x, 16)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->log_alpha, 4) || !aligned(a->cu_seqlens, 4) || !aligned(a->workspace, 256))
+    return KDA_ERR_INVALID_ARG;
+  const size_t sbytes = B * H * a->dk * a->dv * 4;
+  const Range o{a->o, N * H * a->dv * es}, s1{a->final_state, sbytes}, ws{a->workspace, a->workspace_bytes};
+  const Range inputs[] = {{a->q, N * a->Hk * a->dk * es}, {a->k, N * a->Hk * a->dk * es}, {a->v, N * H * a->dv * es},
+                          {a->log_alpha, (p.decay_head ? H : N * H) * 4}, {a->cu_seqlens, 4 * (B + 1)},
+                          {a->pad_mask, N}, {a->init_state, sbytes}};
+  for (const Range &r : inputs) {
+    if (overlap(o, r) || overlap(ws, r)) return KDA_ERR_INVALID_ARG;
+    if (overlap(s1, r) && !(r.p == (const void *)a->init_state && r.p == (const void *)a->final_state))
+      return KDA_ERR_INVALID_ARG;
+  }
+  if (overlap(o, s1) || overlap(o, ws) || overlap(s1, ws)) return KDA_ERR_INVALID_ARG;
+  p.o = a->o;
+  p.final_state = a->final_state;
+  if (error_word(&p.err) != KDA_OK || timeout_site_word(&p.site) != KDA_OK) return KDA_ERR_CUDA;
+  return launch_linear_prefill(p, bf16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_linear_decode(const kda_linear_decode_args *a, void *stream) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  const kda_status ok = linear_sizes(a->dtype, a->B, 0, a->H, a->Hk, a->dk, a->dv, a->decay);
+  if (ok != KDA_OK) return ok;
+  if (a->B == 0) return KDA_OK;
+  if (!a->q || !a->k || !a->v || !a->log_alpha || !a->state || !a->o) return KDA_ERR_INVALID_ARG;
+  const size_t B = (size_t)a->B, H = (size_t)a->H, es = elem_bytes(a->dtype);
+  if (B * H > 0x7FFFFFFFull / 4) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->state, 16) || !aligned(a->log_alpha, 4)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->q, es) || !aligned(a->k, es) || !aligned(a->v, es) || !aligned(a->o, es))
+    return KDA_ERR_INVALID_ARG;
+  const bool head = a->decay == KDA_DECAY_HEAD;
+  const Range st{a->state, B * H * a->dk * a->dv * 4}, o{a->o, B * H * a->dv * es};
+  const Range others[] = {{a->q, B * a->Hk * a->dk * es}, {a->k, B * a->Hk * a->dk * es}, {a->v, B * H * a->dv * es},
+                          {a->log_alpha, (head ? H : B * H) * 4}, {a->mask, B}};
+  for (const Range &r : others)
+    if (overlap(o, r) || overlap(st, r)) return KDA_ERR_INVALID_ARG;
+  if (overlap(o, st)) return KDA_ERR_INVALID_ARG;
+  LinearDecodeParams p;
+  if (error_word(&p.err) != KDA_OK) return KDA_ERR_CUDA;
+  p.B = a->B;
+  p.H = a->H;
+  p.Hk = a->Hk;
+  p.dk = a->dk;
+  p.dv = a->dv;
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.log_alpha = a->log_alpha;
+  p.mask = a->mask;
+  p.state = a->state;
+  p.o = a->o;
+  p.decay_head = head ? 1 : 0;
+  return launch_linear_decode(p, a->dtype == KDA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_linear_prefill_backward_workspace_size(const kda_linear_backward_args *a) {
+  if (!a || linear_sizes(a->dtype, a->num_seqs, a->total_tokens, a->H, a->Hk, a->dk, a->dv, a->decay) != KDA_OK)
+    return 0;
+  return linear_backward_workspace(linear_params(a), a->dtype == KDA_BF16);
+}
+
+kda_status kda_linear_prefill_backward(const kda_linear_backward_args *a, void *stream) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  const kda_status ok =
+      linear_sizes(a->dtype, a->num_seqs, a->total_tokens, a->H, a->Hk, a->dk, a->dv, a->decay);
+  if (ok != KDA_OK) return ok;
+  if (a->num_seqs == 0 && a->total_tokens != 0) return KDA_ERR_INVALID_ARG;
+  const size_t N = (size_t)a->total_tokens, B = (size_t)a->num_seqs, H = (size_t)a->H, es = elem_bytes(a->dtype);
+  const bool head = a->decay == KDA_DECAY_HEAD;
+  if (a->num_seqs == 0 && !head) return KDA_OK;
+  if (!a->grad_log_alpha && (N > 0 || head)) return KDA_ERR_INVALID_ARG;
+  if (a->num_seqs > 0 && (!a->cu_seqlens || !a->workspace)) return KDA_ERR_INVALID_ARG;
+  if (N > 0 && (!a->log_alpha || !a->q || !a->k || !a->v || !a->grad_o || !a->grad_q || !a->grad_k || !a->grad_v))
+    return KDA_ERR_INVALID_ARG;
+  LinearParams p = linear_params(a);
+  const bool bf16 = a->dtype == KDA_BF16;
+  if (a->num_seqs > 0 && a->workspace_bytes < linear_backward_workspace(p, bf16)) return KDA_ERR_INVALID_ARG;
+  const void *need16[] = {a->q, a->k, a->v, a->grad_o, a->grad_q, a->grad_k, a->grad_v, a->init_state,
+                          a->grad_final_state, a->grad_init_state};
+  for (const void *x : need16)
+    if (x && !aligned(x, 16)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->log_alpha, 4) || !aligned(a->grad_log_alpha, 4) || !aligned(a->cu_seqlens, 4) ||
+      !aligned(a->workspace, 256))
+    return KDA_ERR_INVALID_ARG;
+  const size_t sbytes = B * H * a->dk * a->dv * 4, qb = N * a->Hk * a->dk * es, vb = N * H * a->dv * es;
+  const size_t lb = (head ? H : N * H) * 4;
+  const Range ins[] = {{a->q, qb}, {a->k, qb}, {a->v, vb}, {a->log_alpha, lb}, {a->cu_seqlens, 4 * (B + 1)},
+                       {a->pad_mask, N}, {a->init_state, sbytes}, {a->grad_o, vb}, {a->grad_final_state, sbytes}};
+  const Range outs[] = {{a->grad_q, qb}, {a->grad_k, qb}, {a->grad_v, vb}, {a->grad_log_alpha, lb},
+                        {a->grad_init_state, sbytes}, {a->workspace, a->workspace_bytes}};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range &r : ins)
+      if (overlap(outs[i], r)) return KDA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
+  }
+  p.d_o = a->grad_o;
+  p.d_final = a->grad_final_state;
+  p.gq = a->grad_q;
+  p.gk = a->grad_k;
+  p.gv = a->grad_v;
+  p.gla = a->grad_log_alpha;
+  p.g_init = a->grad_init_state;
+  if (error_word(&p.err) != KDA_OK || timeout_site_word(&p.site) != KDA_OK) return KDA_ERR_CUDA;
+  return launch_linear_backward(p, bf16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  const kda_status ok = norm_sizes(a->dtype, a->rows, a->D, a->eps);
+  if (ok != KDA_OK) return ok;
+  const bool bytes = a->out_dtype == KDA_E4M3 || a->out_dtype == KDA_I8;
+  if (!bytes && a->out_dtype != a->dtype) return KDA_ERR_INVALID_ARG;
+  if (bytes && a->group != 0 && a->group != 32 && a->group != 64 && a->group != 128) return KDA_ERR_UNSUPPORTED;
+  if (!bytes && (a->group != 0 || a->scale)) return KDA_ERR_INVALID_ARG;
+  if (a->residual_out && !a->residual) return KDA_ERR_INVALID_ARG;
+  if (a->rows == 0) return KDA_OK;
+  if (!a->x || !a->y || (bytes && !a->scale)) return KDA_ERR_INVALID_ARG;
+  const void *need16[] = {a->x, a->residual, a->weight, a->residual_out};
+  for (const void *x : need16)
+    if (x && !aligned(x, 16)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->y, bytes ? 8 : 16) || !aligned(a->scale, 4)) return KDA_ERR_INVALID_ARG;
+  const size_t n = (size_t)a->rows * a->D, es = elem_bytes(a->dtype);
+  const size_t scales = (size_t)a->rows * (a->group ? (a->D + a->group - 1) / a->group : 1);
+  const Range y{a->y, n * (bytes ? 1 : es)}, sc{a->scale, a->scale ? scales * 4 : 0};
+  const Range r{a->residual_out, n * es};
+  const Range inputs[] = {{a->x, n * es}, {a->residual, n * es}, {a->weight, (size_t)a->D * 4}};
+  for (const Range &in : inputs) {
+    if (overlap(y, in) || overlap(sc, in)) return KDA_ERR_INVALID_ARG;
+    if (overlap(r, in) && !(in.p == a->residual && r.p == a->residual)) return KDA_ERR_INVALID_ARG;
+  }
+  if (overlap(y, sc) || overlap(y, r) || overlap(sc, r)) return KDA_ERR_INVALID_ARG;
+  NormParams p;
+  if (error_word(&p.err) != KDA_OK) return KDA_ERR_CUDA;
+  p.rows = a->rows;
+  p.D = a->D;
+  p.group = a->group;
+  p.x = a->x;
+  p.residual = a->residual;
+  p.weight = a->weight;
+  p.eps = a->eps;
+  p.y = a->y;
+  p.scale = a->scale;
+  p.residual_out = a->residual_out;
+  const int out = a->out_dtype == KDA_E4M3 ? 1 : a->out_dtype == KDA_I8 ? 2 : 0;
+  return launch_norm(p, a->dtype == KDA_BF16, out, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                        : KDA_ERR_CUDA;
+}
+
+size_t kda_rms_norm_backward_workspace_size(const kda_rms_norm_backward_args *a) {
+  if (!a || norm_sizes(a->dtype, a->rows, a->D, a->eps) != KDA_OK) return 0;
+  return norm_backward_workspace(a->rows, a->D);
+}
+
+kda_status kda_rms_norm_backward(const kda_rms_norm_backward_args *a, void *stream) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  const kda_status ok = norm_sizes(a->dtype, a->rows, a->D, a->eps);
+  if (ok != KDA_OK) return ok;
+  if (a->rows > 0 && (!a->x || !a->grad_y || !a->grad_x)) return KDA_ERR_INVALID_ARG;
+  if (a->rows > 0 && a->grad_weight && (!a->workspace || a->workspace_bytes < norm_backward_workspace(a->rows, a->D)))
+    return KDA_ERR_INVALID_ARG;
+  const void *need16[] = {a->x, a->weight, a->grad_y, a->grad_residual, a->grad_x};
+  for (const void *x : need16)
+    if (x && !aligned(x, 16)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->grad_weight, 4) || !aligned(a->workspace, 256)) return KDA_ERR_INVALID_ARG;
+  const size_t n = (size_t)a->rows * a->D * elem_bytes(a->dtype), d = (size_t)a->D * 4;
+  const Range dx{a->grad_x, n}, dw{a->grad_weight, d}, ws{a->workspace, a->workspace ? a->workspace_bytes : 0};
+  const Range inputs[] = {{a->x, n}, {a->weight, d}, {a->grad_y, n}, {a->grad_residual, n}};
+  for (const Range &in : inputs) {
+    if (overlap(dw, in) || overlap(ws, in)) return KDA_ERR_INVALID_ARG;
+    if (overlap(dx, in) && !(in.p == a->grad_residual && dx.p == a->grad_residual)) return KDA_ERR_INVALID_ARG;
+  }
+  if (overlap(dx, dw) || overlap(dx, ws) || overlap(dw, ws)) return KDA_ERR_INVALID_ARG;
+  NormBackwardParams p;
+  if (error_word(&p.err) != KDA_OK) return KDA_ERR_CUDA;
+  p.rows = a->rows;
+  p.D = a->D;
+  p.x = a->x;
+  p.dy = a->grad_y;
+  p.dr = a->grad_residual;
+  p.weight = a->weight;
+  p.eps = a->eps;
+  p.dx = a->grad_x;
+  p.dw = a->grad_weight;
+  p.part = a->grad_weight ? static_cast<float *>(a->workspace) : nullptr;
+  return launch_norm_backward(p, a->dtype == KDA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -85,6 +85,61 @@ struct BackwardParams {
   int gate_head;
 };
 
+// Linear attention with a decay for each head: prefill and (d_o ..) its backward pass.
+struct LinearParams {
+  int num_seqs, N, H, Hk, dk, dv;
+  const void *q, *k, *v;
+  const float *log_alpha;
+  const int32_t *cu;
+  const uint8_t *mask;
+  const float *init_state;
+  void *o;
+  float *final_state;
+  int decay_head;         // 1: log_alpha is [H] (a constant of the head)
+  void *ws;               // segment table, states at segment starts, ...
+  unsigned *err;
+  long long wait_cycles;  // limit of every bounded device wait
+  unsigned *site;         // device word: code of the first bounded wait that ran out
+  const void *d_o;
+  const float *d_final;
+  void *gq, *gk, *gv;
+  float *gla, *g_init;
+};
+
+struct LinearDecodeParams {
+  int B, H, Hk, dk, dv;
+  const void *q, *k, *v;
+  const float *log_alpha;
+  const uint8_t *mask;
+  float *state;
+  void *o;
+  unsigned *err;
+  int decay_head;         // 1: log_alpha is [H]
+};
+
+struct NormParams {
+  long long rows;
+  int D, group;
+  const void *x, *residual;
+  const float *weight;
+  float eps;
+  void *y;
+  float *scale;
+  void *residual_out;
+  unsigned *err;
+};
+
+struct NormBackwardParams {
+  long long rows;
+  int D;
+  const void *x, *dy, *dr;
+  const float *weight;
+  float eps;
+  void *dx;
+  float *dw, *part;       // part: one row of partial sums per block
+  unsigned *err;
+};
+
 // Launchers (return a CUDA error code; argument checks happen before).
 cudaError_t launch_prefill_prepass(const PrefillParams &p, bool bf16, SeqSpan *spans,
                                    cudaStream_t s);
@@ -106,6 +161,19 @@ cudaError_t launch_decode(const DecodeParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_short_conv(const ConvParams &p, bool bf16, cudaStream_t s);
 size_t backward_workspace(int N, int B, int H, int dk, int dv);
 cudaError_t launch_backward(const BackwardParams &p, bool bf16, cudaStream_t s);
+size_t linear_prefill_workspace(const LinearParams &p, bool bf16);
+cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t s);
+size_t linear_backward_workspace(const LinearParams &p, bool bf16);
+cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_linear_decode(const LinearDecodeParams &p, bool bf16, cudaStream_t s);
+// cu_seqlens check and segment table; states at segment starts (and gradients at their ends).
+cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int tokens, cudaStream_t s);
+cudaError_t launch_linear_chain(const LinearParams &p, const int *sbase, float *part, float *rpart,
+                                const float *whole, cudaStream_t s);
+// out: 0 the type of x, 1 e4m3, 2 int8.
+cudaError_t launch_norm(const NormParams &p, bool bf16, int out, cudaStream_t s);
+size_t norm_backward_workspace(long long rows, int D);
+cudaError_t launch_norm_backward(const NormBackwardParams &p, bool bf16, cudaStream_t s);
 
 // ---------------------------------------------------------------- helpers
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {

@@ -1,0 +1,672 @@
+// Linear attention with a decay for each head: prefill and its backward pass at fp32
+// accuracy, for any element type and head dimensions (formulas in kda_linear.cuh).
+//
+// Three steps, all parallel over segments and heads except the short middle one:
+//   parts    each segment's own contribution to the state,  sum_s 2^{b_end - b_s} k_s v_s^T
+//            (and for the backward pass to the gradient of the state at its start,
+//            sum_t 2^{b_t} q_t do_t^T, the same product over the same rows in reverse)
+//   chain    S <- a S + part over a sequence's segments, one thread per 4 state elements: the
+//            parts are replaced by the states at the segments' starts (gradients at their ends)
+//   rows     outputs (or gradients) of each segment from the state at its start
+// The products run on the tensor cores as 3xTF32: x = hi + lo with tf32 hi, lo, and
+// a b = a_h b_l + a_l b_h + a_h b_h, where the dropped term is below 2^-21 of the product.
+// Chunks of 64 rows, so that the fp32 tiles of a chunk fit in shared memory.
+#include "kda_linear.cuh"
+
+namespace kda {
+namespace lin {
+
+constexpr int C = 64;
+constexpr int kThreads = 256;
+constexpr int kSlice = 64;          // d_v columns of a block in the parts and prefill rows kernels
+
+// ------------------------------------------------------------------ 3xTF32 products
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc[m][n] += A B for a warp's 16 MT x 8 NT tile over K; a(r, k) and b(k, n) read the operands.
+// Entry acc[m][n][e] is row 16 m + lane / 4 + 8 (e / 2), column 8 n + 2 (lane % 4) + e % 2.
+template <int MT, int NT, int K, class FA, class FB>
+__device__ __forceinline__ void gemm3(float (&acc)[MT][NT][4], FA a, FB b) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll 2
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    uint32_t ah[MT][4], al[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      split_tf32(a(16 * m + g, k0 + t), ah[m][0], al[m][0]);
+      split_tf32(a(16 * m + g + 8, k0 + t), ah[m][1], al[m][1]);
+      split_tf32(a(16 * m + g, k0 + t + 4), ah[m][2], al[m][2]);
+      split_tf32(a(16 * m + g + 8, k0 + t + 4), ah[m][3], al[m][3]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t bh[2], bl[2];
+      split_tf32(b(k0 + t, 8 * n + g), bh[0], bl[0]);
+      split_tf32(b(k0 + t + 4, 8 * n + g), bh[1], bl[1]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma_tf32(acc[m][n], ah[m], bl);
+        mma_tf32(acc[m][n], al[m], bh);
+        mma_tf32(acc[m][n], ah[m], bh);
+      }
+    }
+  }
+}
+template <int MT, int NT>
+__device__ __forceinline__ void zero(float (&acc)[MT][NT][4]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+}
+// f(row, column, value) over a thread's accumulator entries.
+template <int MT, int NT, class F>
+__device__ __forceinline__ void each(float (&acc)[MT][NT][4], F f) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(16 * m + g + 8 * (e >> 1), 8 * n + 2 * t + (e & 1), acc[m][n][e]);
+}
+
+// ------------------------------------------------------------------ tiles
+// Rows [pos0, pos0 + C) of x [N, heads, d], columns [c0, c0 + W) of head `hd`, as fp32 with row
+// stride LD.  Rows past `end` and pads are zeros and are not read.
+template <int W, int LD, bool BF16>
+__device__ __forceinline__ void load_rows(float *dst, const void *x, int heads, int d, int hd, int c0, int pos0,
+                                          int end, const uint8_t *mask) {
+  constexpr int E = BF16 ? 8 : 4, V = W / E;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < C * V; i += kThreads) {
+    const int r = i / V, c = (i % V) * E, pos = pos0 + r;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (pos < end && (mask == nullptr || mask[pos] != 0)) {
+      const size_t at = ((size_t)pos * heads + hd) * d + c0 + c;
+      u = BF16 ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(x) + at)
+               : *reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(x) + at);
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float *o = dst + r * LD + c;
+    if (BF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[2 * e] = __uint_as_float(w[e] << 16);
+        o[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    } else {
+      *reinterpret_cast<uint4 *>(o) = u;
+    }
+  }
+}
+
+// A chunk's decays.  Filled by the first warp; the block synchronises after it.
+struct Decays {
+  float hi[C], lo[C];      // b, log2
+  float from[C];           // 2^b: from the chunk's start to the row
+  float to[C];             // 2^{b_C - b}: from the row to the chunk's end
+  float whole;             // 2^{b_C}
+};
+__device__ __forceinline__ void chunk_decays(Decays &d, const LinearParams &p, int pos0, int end, int h) {
+  const int lane = threadIdx.x & 31;
+  double x[2], s;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) x[e] = log2_decay(p.log_alpha, p.decay_head, p.mask, pos0 + 2 * lane + e, end, h, p.H);
+  s = x[0] + x[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = shfl_up_f64(s, o);
+    if (lane >= o) s += y;
+  }
+  const double total = shfl_f64(s, 31);
+  const double b[2] = {s - x[1], s};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * lane + e;
+    d.hi[r] = (float)b[e];
+    d.lo[r] = (float)(b[e] - (double)d.hi[r]);
+    d.from[r] = exp2f((float)b[e]);
+    d.to[r] = exp2f((float)(total - b[e]));
+  }
+  if (lane == 0) d.whole = exp2f((float)total);
+}
+__device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
+  return exp2f((d.hi[t] - d.hi[s]) + (d.lo[t] - d.lo[s]));
+}
+
+// ------------------------------------------------------------------ plan
+// Checks cu_seqlens (nothing else runs if it is invalid) and fills the segment table.
+__global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int tokens) {
+  __shared__ int tot[32], carry, bad;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (tid == 0) { carry = 0; bad = 0; }
+  __syncthreads();
+  if (device_error_latched(p.err)) return;
+  int wrong = 0;
+  for (int i = tid; i <= p.num_seqs; i += 1024) {
+    const int c = p.cu[i];
+    if (c < 0 || c > p.N || (i == 0 && c != 0) || (i == p.num_seqs && c != p.N) || (i > 0 && p.cu[i - 1] > c)) wrong = 1;
+  }
+  if (wrong) atomicOr(&bad, 1);
+  __syncthreads();
+  if (bad) {
+    if (tid == 0) atomicOr(p.err, ERR_BIT_CHECK);
+    return;
+  }
+  for (int b0 = 0; b0 <= p.num_seqs; b0 += 1024) {
+    const int b = b0 + tid;
+    const int n = b < p.num_seqs ? (p.cu[b + 1] - p.cu[b] + tokens - 1) / tokens : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) tot[w] = x;
+    __syncthreads();
+    int before = carry;
+    for (int i = 0; i < w; ++i) before += tot[i];
+    if (b <= p.num_seqs) sbase[b] = before + x - n;
+    __syncthreads();
+    if (tid == 1023) carry = before + x;
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ parts
+// Block: segment x head x 64 columns of d_v.  REVERSE: q, do and the rows in reverse.
+template <int DK, bool BF16, bool REVERSE>
+__device__ __forceinline__ void parts_block(const LinearParams &p, const Segment &sg, int seg, int h, int c0,
+                                            float *part, float *whole, float *sm, Decays &dec, int tokens) {
+  constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
+  float *sk = sm, *sv = sm + C * LK;
+  const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16 * MT, n0 = (warp >> 2) * 32;
+  const int hk = h / (p.H / p.Hk);
+  float acc[MT][4][4], keep = 1.f;
+  zero(acc);
+  const int chunks = (sg.end - sg.begin + C - 1) / C;
+  for (int j = 0; j < chunks; ++j) {
+    const int pos0 = sg.begin + (REVERSE ? chunks - 1 - j : j) * C;
+    __syncthreads();
+    load_rows<DK, LK, BF16>(sk, REVERSE ? p.q : p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV, BF16>(sv, REVERSE ? p.d_o : p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
+    __syncthreads();
+    const float a = dec.whole, *wgt = REVERSE ? dec.from : dec.to;
+    keep *= a;
+    each(acc, [&](int, int, float &x) { x *= a; });
+    gemm3<MT, 4, C>(acc, [&](int r, int k) { return sk[k * LK + m0 + r] * wgt[k]; },
+                    [&](int k, int n) { return sv[k * LV + n0 + n]; });
+  }
+  float *out = part + ((size_t)seg * p.H + h) * DK * p.dv + c0;
+  each(acc, [&](int r, int n, float &x) { out[(size_t)(m0 + r) * p.dv + n0 + n] = x; });
+  if (!REVERSE && c0 == 0 && threadIdx.x == 0) whole[(size_t)seg * p.H + h] = keep;
+}
+
+template <int DK, bool BF16>
+__global__ void __launch_bounds__(kThreads) parts_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
+                                                         float *whole, int tokens) {
+  extern __shared__ float sm[];
+  __shared__ Decays dec;
+  if (device_error_latched(p.err)) return;
+  const int slices = p.dv / kSlice;
+  const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
+  if (seg >= sbase[p.num_seqs]) return;
+  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, tokens);
+  if (blockIdx.y == 0) parts_block<DK, BF16, false>(p, sg, seg, h, c0, part, whole, sm, dec, tokens);
+  else parts_block<DK, BF16, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec, tokens);
+}
+template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + kSlice + 4) * 4; }
+
+// ------------------------------------------------------------------ chain
+// grid: (B H, d_k d_v / 1024, 1 or 2); thread: 4 elements of a sequence's and head's state.
+// z = 0 forwards from init_state, 1 backwards from the final state's gradient.
+__global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
+                                                    const float *whole) {
+  if (device_error_latched(p.err)) return;
+  const bool back = blockIdx.z != 0;
+  const size_t bh = blockIdx.x, per = (size_t)p.dk * p.dv;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  const size_t e = (size_t)blockIdx.y * 256 + threadIdx.x;
+  const int s0 = sbase[b], s1 = sbase[b + 1];
+  const float *in = back ? p.d_final : p.init_state;
+  float *out = back ? p.g_init : p.final_state;
+  float4 S = in ? reinterpret_cast<const float4 *>(in + bh * per)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+  float *x = back ? rpart : part;
+  const int n = s1 - s0;
+  constexpr int AHEAD = 8;             // loads in flight ahead of the chain
+  for (int i0 = 0; i0 < n; i0 += AHEAD) {
+    float4 v[AHEAD];
+    float a[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (i0 + i < n) {
+        const size_t at = (size_t)(back ? s1 - 1 - i0 - i : s0 + i0 + i) * p.H + h;
+        v[i] = reinterpret_cast<const float4 *>(x + at * per)[e];
+        a[i] = whole[at];
+      }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (i0 + i < n) {
+        const size_t at = (size_t)(back ? s1 - 1 - i0 - i : s0 + i0 + i) * p.H + h;
+        reinterpret_cast<float4 *>(x + at * per)[e] = S;
+        S.x = fmaf(a[i], S.x, v[i].x);
+        S.y = fmaf(a[i], S.y, v[i].y);
+        S.z = fmaf(a[i], S.z, v[i].z);
+        S.w = fmaf(a[i], S.w, v[i].w);
+      }
+  }
+  if (out) reinterpret_cast<float4 *>(out + bh * per)[e] = S;
+}
+
+// ------------------------------------------------------------------ prefill rows
+template <int DK, bool BF16>
+__global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const int *sbase, const float *start, int tokens) {
+  constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
+  extern __shared__ float sm[];
+  __shared__ Decays dec;
+  float *sq = sm, *sk = sq + C * LK, *sv = sk + C * LK, *sS = sv + C * LV, *sP = sS + DK * LV;
+  if (device_error_latched(p.err)) return;
+  const int slices = p.dv / kSlice;
+  const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
+  if (seg >= sbase[p.num_seqs]) return;
+  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, tokens);
+  const int hk = h / (p.H / p.Hk);
+  const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16, n0 = (warp >> 2) * 32;
+  float S[MT][4][4];                 // rows MT m0 .., columns n0 .. of the state
+  const float *in = start + ((size_t)seg * p.H + h) * DK * p.dv + c0;
+  each(S, [&](int r, int n, float &x) { x = in[(size_t)(m0 * MT + r) * p.dv + n0 + n]; });
+  const int chunks = (sg.end - sg.begin + C - 1) / C;
+  for (int j = 0; j < chunks; ++j) {
+    const int pos0 = sg.begin + j * C;
+    __syncthreads();
+    load_rows<DK, LK, BF16>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<DK, LK, BF16>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV, BF16>(sv, p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    each(S, [&](int r, int n, float &x) { sS[(m0 * MT + r) * LV + n0 + n] = x; });
+    if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
+    __syncthreads();
+    float o[1][4][4], A[1][4][4];
+    zero(A);
+    if (n0 <= m0 + 15)               // else above the diagonal
+      gemm3<1, 4, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+                      [&](int k, int n) { return sk[(n0 + n) * LK + k]; });
+    each(A, [&](int r, int n, float &x) {
+      const int t = m0 + r, s = n0 + n;
+      sP[t * LV + s] = s <= t ? x * pair_decay(dec, t, s) : 0.f;
+    });
+    zero(o);
+    gemm3<1, 4, DK>(o, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+                    [&](int k, int n) { return sS[k * LV + n0 + n]; });
+    each(o, [&](int r, int, float &x) { x *= dec.from[m0 + r]; });
+    __syncthreads();
+    gemm3<1, 4, C>(o, [&](int r, int k) { return sP[(m0 + r) * LV + k]; },
+                   [&](int k, int n) { return sv[k * LV + n0 + n]; });
+    each(o, [&](int r, int n, float &x) {
+      const int pos = pos0 + m0 + r;
+      if (pos < sg.end) store_elem<BF16>(p.o, ((size_t)pos * p.H + h) * p.dv + c0 + n0 + n, x);
+    });
+    if (j + 1 < chunks) {
+      each(S, [&](int, int, float &x) { x *= dec.whole; });
+      gemm3<MT, 4, C>(S, [&](int r, int k) { return sk[k * LK + m0 * MT + r] * dec.to[k]; },
+                      [&](int k, int n) { return sv[k * LV + n0 + n]; });
+    }
+  }
+}
+template <int DK> constexpr size_t rows_smem() {
+  return (size_t)(2 * C * (DK + 4) + (2 * C + DK) * (kSlice + 4)) * 4;
+}
+
+// ------------------------------------------------------------------ gradients of a chunk
+// Block: chunk (a segment of one chunk) x head, with the state S at its start and the state's
+// gradient D at its end.  With M = tril(dO V^T o 2^{b_t - b_s}), P = tril(Q K^T o 2^{b_t - b_s}):
+//   dQ = M K + Diag(2^b) dO S^T,  dK = M^T Q + Diag(2^{b_C-b}) V D^T,  dV = P^T dO + Diag(2^{b_C-b}) K D
+//   dlog_alpha_u = sum_{t>=u} 2^{b_t} q_t.S do_t + sum_{s<u} 2^{b_C-b_s} k_s.D v_s + 2^{b_C} <S, D>
+//                + sum_{t>=u>s} (q_t.k_s)(do_t.v_s) 2^{b_t-b_s}
+// (what passes over row u: to later rows, from earlier rows, through the chunk, inside it).
+// S and D are taken in halves of 64 rows, one after the other through the same tile.
+template <int DK, int DV, bool BF16>
+struct GradSmem {
+  static constexpr int LK = DK + 4, LV = DV + 4, LP = C + 4;
+  static constexpr int Q = 0, K = Q + C * LK, V = K + C * LK, O = V + C * LV;
+  static constexpr int P = O + C * LV, M = P + C * LP, S = M + C * LP, END = S + C * (LV > LP ? LV : LP);
+};
+
+// x[row] += sum of f's values over the warp's columns of the row, kept per warp column in part[2][C].
+template <int NT, class F>
+__device__ __forceinline__ void row_sums(float (&acc)[1][NT][4], float *part, int m0, int wn, F f) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e >> 1] += f(g + 8 * (e >> 1), 8 * n + 2 * t + (e & 1), acc[0][n][e]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], 1);
+    s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], 2);
+    if (t == 0) part[wn * C + m0 + g + 8 * i] += s[i];
+  }
+}
+
+template <int DK, int DV, bool BF16>
+__global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const int *sbase, const float *start,
+                                                        const float *dend, float *gq32, float *gk32, float *gla) {
+  using L = GradSmem<DK, DV, BF16>;
+  constexpr int LK = L::LK, LV = L::LV, LP = L::LP, HALVES = DK / 64, NV = DV / 16;
+  extern __shared__ float sm[];
+  __shared__ Decays dec;
+  __shared__ float r_part[2 * C], k_part[2 * C], pair_sum[C], red[kThreads / 32];
+  if (device_error_latched(p.err)) return;
+  const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  if (seg >= sbase[p.num_seqs]) return;
+  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, C);
+  const int hk = h / (p.H / p.Hk), pos0 = sg.begin, tid = threadIdx.x;
+  const int warp = tid >> 5, m0 = (warp & 3) * 16, wn = warp >> 2, n0 = wn * 32;
+  float *sq = sm + L::Q, *sk = sm + L::K, *sv = sm + L::V, *so = sm + L::O, *sP = sm + L::P, *sM = sm + L::M,
+        *sS = sm + L::S;
+  load_rows<DK, LK, BF16>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+  load_rows<DK, LK, BF16>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+  load_rows<DV, LV, BF16>(sv, p.v, p.H, DV, h, 0, pos0, sg.end, p.mask);
+  load_rows<DV, LV, BF16>(so, p.d_o, p.H, DV, h, 0, pos0, sg.end, p.mask);
+  if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
+  if (tid < 2 * C) r_part[tid] = k_part[tid] = 0.f;
+  __syncthreads();
+  {
+    float A[1][4][4], G[1][4][4];
+    zero(A);
+    zero(G);
+    if (n0 <= m0 + 15) {
+      gemm3<1, 4, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+                      [&](int k, int n) { return sk[(n0 + n) * LK + k]; });
+      gemm3<1, 4, DV>(G, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
+                      [&](int k, int n) { return sv[(n0 + n) * LV + k]; });
+    }
+    each(G, [&](int r, int n, float &x) {
+      const int t = m0 + r, s = n0 + n;
+      sM[t * LP + s] = s <= t ? x * pair_decay(dec, t, s) : 0.f;
+    });
+    each(A, [&](int r, int n, float &x) {
+      const int t = m0 + r, s = n0 + n;
+      sS[t * LP + s] = s < t ? x * sM[t * LP + s] : 0.f;      // the pairs' shares (own entries)
+      sP[t * LP + s] = s <= t ? x * pair_decay(dec, t, s) : 0.f;
+    });
+  }
+  __syncthreads();
+  if (tid < C) {                     // column tid: sums over t >= u, in place
+    float a = 0.f;
+    for (int t = C - 1; t > tid; --t) {
+      a += sS[t * LP + tid];
+      sS[t * LP + tid] = a;
+    }
+  }
+  __syncthreads();
+  if (tid < C) {
+    float a = 0.f;
+    for (int s = 0; s < tid; ++s) a += sS[tid * LP + s];
+    pair_sum[tid] = a;
+  }
+  const float *gS = start + ((size_t)seg * p.H + h) * DK * DV, *gD = dend + ((size_t)seg * p.H + h) * DK * DV;
+  float through = 0.f;
+  float av[1][NV][4];
+  zero(av);
+#pragma unroll 1
+  for (int half = 0; half < HALVES; ++half) {
+    const int k0 = half * 64;
+    __syncthreads();
+    for (int i = tid; i < 64 * DV / 4; i += kThreads) {
+      const int r = i / (DV / 4), c = i % (DV / 4) * 4;
+      const float4 x = *reinterpret_cast<const float4 *>(gS + (size_t)(k0 + r) * DV + c);
+      const float4 y = *reinterpret_cast<const float4 *>(gD + (size_t)(k0 + r) * DV + c);
+      through += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+      *reinterpret_cast<float4 *>(sS + r * LV + c) = x;
+    }
+    __syncthreads();
+    float acc[1][4][4];
+    zero(acc);
+    gemm3<1, 4, DV>(acc, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
+                    [&](int k, int n) { return sS[(n0 + n) * LV + k]; });
+    each(acc, [&](int r, int, float &x) { x *= dec.from[m0 + r]; });
+    row_sums(acc, r_part, m0, wn, [&](int r, int n, float x) { return x * sq[(m0 + r) * LK + k0 + n0 + n]; });
+    gemm3<1, 4, C>(acc, [&](int r, int k) { return sM[(m0 + r) * LP + k]; },
+                   [&](int k, int n) { return sk[k * LK + k0 + n0 + n]; });
+    each(acc, [&](int r, int n, float &x) {
+      const int pos = pos0 + m0 + r;
+      if (pos >= sg.end) return;
+      if (gq32) gq32[((size_t)pos * p.H + h) * DK + k0 + n0 + n] = x;
+      else store_elem<BF16>(p.gq, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
+    });
+    __syncthreads();
+    for (int i = tid; i < 64 * DV / 4; i += kThreads) {
+      const int r = i / (DV / 4), c = i % (DV / 4) * 4;
+      *reinterpret_cast<float4 *>(sS + r * LV + c) = *reinterpret_cast<const float4 *>(gD + (size_t)(k0 + r) * DV + c);
+    }
+    __syncthreads();
+    zero(acc);
+    gemm3<1, 4, DV>(acc, [&](int r, int k) { return sv[(m0 + r) * LV + k]; },
+                    [&](int k, int n) { return sS[(n0 + n) * LV + k]; });
+    each(acc, [&](int r, int, float &x) { x *= dec.to[m0 + r]; });
+    row_sums(acc, k_part, m0, wn, [&](int r, int n, float x) { return x * sk[(m0 + r) * LK + k0 + n0 + n]; });
+    gemm3<1, 4, C>(acc, [&](int r, int k) { return sM[k * LP + m0 + r]; },
+                   [&](int k, int n) { return sq[k * LK + k0 + n0 + n]; });
+    each(acc, [&](int r, int n, float &x) {
+      const int pos = pos0 + m0 + r;
+      if (pos >= sg.end) return;
+      if (gk32) gk32[((size_t)pos * p.H + h) * DK + k0 + n0 + n] = x;
+      else store_elem<BF16>(p.gk, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
+    });
+    gemm3<1, NV, 64>(av, [&](int r, int k) { return sk[(m0 + r) * LK + k0 + k]; },
+                     [&](int k, int n) { return sS[k * LV + wn * (DV / 2) + n]; });
+  }
+  each(av, [&](int r, int, float &x) { x *= dec.to[m0 + r]; });
+  gemm3<1, NV, C>(av, [&](int r, int k) { return sP[k * LP + m0 + r]; },
+                  [&](int k, int n) { return so[k * LV + wn * (DV / 2) + n]; });
+  each(av, [&](int r, int n, float &x) {
+    const int pos = pos0 + m0 + r;
+    if (pos < sg.end) store_elem<BF16>(p.gv, ((size_t)pos * p.H + h) * DV + wn * (DV / 2) + n, x);
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(0xFFFFFFFFu, through, o);
+  if ((tid & 31) == 0) red[warp] = through;
+  __syncthreads();
+  if (tid < C && pos0 + tid < sg.end) {
+    float x = 0.f, r = 0.f, k = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) x += red[i];
+    for (int t = C - 1; t >= tid; --t) r += r_part[t] + r_part[C + t];
+    for (int s = 0; s < tid; ++s) k += k_part[s] + k_part[C + s];
+    const bool pad = p.mask != nullptr && p.mask[pos0 + tid] == 0;
+    const float g = pad ? 0.f : pair_sum[tid] + r + k + dec.whole * x;
+    // one decay per head: [H, N] for the sum that follows
+    gla[p.decay_head ? (size_t)h * p.N + pos0 + tid : (size_t)(pos0 + tid) * p.H + h] = g;
+  }
+}
+
+// ------------------------------------------------------------------ sums over shared inputs
+// dq, dk of a key head: the value heads' fp32 gradients added in order.  Thread: 4 columns.
+template <bool BF16>
+__global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float *gq32, const float *gk32) {
+  if (device_error_latched(p.err)) return;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = p.dk / 4;
+  if (i >= (size_t)p.N * p.Hk * per) return;
+  const int G = p.H / p.Hk, c = (int)(i % per);
+  const size_t row = i / per;          // pos Hk + hk
+  const float4 *x = reinterpret_cast<const float4 *>(blockIdx.y ? gk32 : gq32) + row * G * per + c;
+  float4 s = x[0];
+  for (int g = 1; g < G; ++g) {
+    const float4 y = x[g * per];
+    s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+  }
+  void *out = blockIdx.y ? p.gk : p.gq;
+  const size_t at = row * p.dk + 4 * c;
+  store_elem<BF16>(out, at, s.x);
+  store_elem<BF16>(out, at + 1, s.y);
+  store_elem<BF16>(out, at + 2, s.z);
+  store_elem<BF16>(out, at + 3, s.w);
+}
+
+// The gradient of a head's constant log_alpha: the sum over the tokens, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(1024) head_decay_kernel(LinearParams p, const float *gla) {
+  __shared__ double s[32];
+  if (device_error_latched(p.err)) return;
+  const int h = blockIdx.x;
+  double a = 0.0;
+  for (int i = threadIdx.x; i < p.N; i += 1024) a += (double)gla[(size_t)h * p.N + i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a += __hiloint2double(__shfl_xor_sync(0xFFFFFFFFu, __double2hiint(a), o),
+                          __shfl_xor_sync(0xFFFFFFFFu, __double2loint(a), o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a = 0.0;
+    for (int i = 0; i < 32; ++i) a += s[i];
+    p.gla[h] = (float)a;
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Chunks in a segment of the prefill: as many as leave about six blocks per SM, since the
+// chain and its states (written and read once per segment) shrink with longer segments.
+int segment_chunks(int N, int B, int blocks_per_chunk, int chunk) {
+  int per = 1;
+  while (per < 64 && ((size_t)N / (chunk * 2 * per) + B) * (size_t)blocks_per_chunk >= 6 * 148) per *= 2;
+  return per;
+}
+size_t state_bytes(const LinearParams &p, size_t segs) { return align256(segs * p.H * (size_t)p.dk * p.dv * 4); }
+
+cudaError_t launch_parts_chain(const LinearParams &p, bool bf16, const int *sbase, float *part, float *rpart,
+                               float *whole, size_t segs, int tokens, cudaStream_t s) {
+  const size_t blocks = segs * p.H * (p.dv / kSlice);
+  if (blocks > 0x7FFFFFFFull || (size_t)p.num_seqs * p.H > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  auto kern = p.dk == 128 ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
+                          : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
+  const size_t smem = p.dk == 128 ? parts_smem<128>() : parts_smem<64>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (blocks) kern<<<dim3((unsigned)blocks, rpart ? 2 : 1), kThreads, smem, s>>>(p, sbase, part, rpart, whole, tokens);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_linear_chain(p, sbase, part, rpart, whole, s);
+}
+
+template <int DK, int DV, bool BF16>
+cudaError_t launch_grad(const LinearParams &p, const int *sbase, const float *start, const float *dend, float *gq32,
+                        float *gk32, float *gla, size_t segs, cudaStream_t s) {
+  auto kern = grad_kernel<DK, DV, BF16>;
+  const size_t smem = (size_t)GradSmem<DK, DV, BF16>::END * 4;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(segs * p.H), kThreads, smem, s>>>(p, sbase, start, dend, gq32, gk32, gla);
+  return cudaGetLastError();
+}
+template <bool BF16>
+cudaError_t launch_grad_dims(const LinearParams &p, const int *sbase, const float *start, const float *dend,
+                             float *gq32, float *gk32, float *gla, size_t segs, cudaStream_t s) {
+  if (p.dk == 128)
+    return p.dv == 128 ? launch_grad<128, 128, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
+                       : launch_grad<128, 64, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
+  return p.dv == 128 ? launch_grad<64, 128, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
+                     : launch_grad<64, 64, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
+}
+
+}  // namespace lin
+
+cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int tokens, cudaStream_t s) {
+  lin::plan_kernel<<<1, 1024, 0, s>>>(p, sbase, tokens);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_chain(const LinearParams &p, const int *sbase, float *part, float *rpart, const float *whole,
+                                cudaStream_t s) {
+  const unsigned nx = (unsigned)(p.dk * p.dv / 1024);
+  lin::chain_kernel<<<dim3((unsigned)(p.num_seqs * p.H), nx, rpart ? 2 : 1), 256, 0, s>>>(p, sbase, part, rpart, whole);
+  return cudaGetLastError();
+}
+
+size_t linear_prefill_workspace(const LinearParams &p, bool bf16) {
+  using namespace lin;
+  const int per = segment_chunks(p.N, p.num_seqs, p.H * (p.dv / kSlice), C);
+  const size_t segs = max_segments(p.N, p.num_seqs, C * per);
+  return table_bytes(p.num_seqs) + align256(segs * p.H * 4) + state_bytes(p, segs);
+}
+
+cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t s) {
+  using namespace lin;
+  if (p.num_seqs == 0) return cudaSuccess;
+  const int per = segment_chunks(p.N, p.num_seqs, p.H * (p.dv / kSlice), C), tokens = C * per;
+  const size_t segs = max_segments(p.N, p.num_seqs, tokens);
+  unsigned char *w = static_cast<unsigned char *>(p.ws);
+  int *sbase = reinterpret_cast<int *>(w);
+  float *whole = reinterpret_cast<float *>(w + table_bytes(p.num_seqs));
+  float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs) + align256(segs * p.H * 4));
+  cudaError_t e = launch_linear_plan(p, sbase, tokens, s);
+  if (e != cudaSuccess) return e;
+  e = launch_parts_chain(p, bf16, sbase, part, nullptr, whole, segs, tokens, s);
+  if (e != cudaSuccess || p.N == 0) return e;
+  auto kern = p.dk == 128 ? (bf16 ? rows_kernel<128, true> : rows_kernel<128, false>)
+                          : (bf16 ? rows_kernel<64, true> : rows_kernel<64, false>);
+  const size_t smem = p.dk == 128 ? rows_smem<128>() : rows_smem<64>();
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, smem, s>>>(p, sbase, part, tokens);
+  return cudaGetLastError();
+}
+
+size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
+  using namespace lin;
+  const size_t segs = max_segments(p.N, p.num_seqs, C);
+  size_t n = table_bytes(p.num_seqs) + align256(segs * p.H * 4) + 2 * state_bytes(p, segs);
+  if (p.H != p.Hk) n += 2 * align256((size_t)p.N * p.H * p.dk * 4);
+  if (p.decay_head) n += align256((size_t)p.N * p.H * 4);
+  return n;
+}
+
+cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_t s) {
+  using namespace lin;
+  if (p.num_seqs == 0) return p.decay_head ? cudaMemsetAsync(p.gla, 0, (size_t)p.H * 4, s) : cudaSuccess;
+  const size_t segs = max_segments(p.N, p.num_seqs, C);
+  unsigned char *w = static_cast<unsigned char *>(p.ws);
+  auto take = [&](size_t n) {
+    unsigned char *at = w;
+    w += align256(n);
+    return reinterpret_cast<float *>(at);
+  };
+  int *sbase = reinterpret_cast<int *>(take(table_bytes(p.num_seqs)));
+  float *whole = take(segs * p.H * 4), *part = take(state_bytes(p, segs)), *rpart = take(state_bytes(p, segs));
+  const bool shared = p.H != p.Hk;
+  float *gq32 = shared ? take((size_t)p.N * p.H * p.dk * 4) : nullptr;
+  float *gk32 = shared ? take((size_t)p.N * p.H * p.dk * 4) : nullptr;
+  float *gla = p.decay_head ? take((size_t)p.N * p.H * 4) : p.gla;
+  cudaError_t e = launch_linear_plan(p, sbase, C, s);
+  if (e != cudaSuccess) return e;
+  e = launch_parts_chain(p, bf16, sbase, part, rpart, whole, segs, C, s);
+  if (e != cudaSuccess) return e;
+  if (p.N > 0) {
+    e = bf16 ? launch_grad_dims<true>(p, sbase, part, rpart, gq32, gk32, gla, segs, s)
+             : launch_grad_dims<false>(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
+    if (e != cudaSuccess) return e;
+    if (shared) {
+      const size_t n = ((size_t)p.N * p.Hk * (p.dk / 4) + 255) / 256;
+      if (n > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+      if (bf16) share_kernel<true><<<dim3((unsigned)n, 2), 256, 0, s>>>(p, gq32, gk32);
+      else share_kernel<false><<<dim3((unsigned)n, 2), 256, 0, s>>>(p, gq32, gk32);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
+  if (p.decay_head) head_decay_kernel<<<(unsigned)p.H, 1024, 0, s>>>(p, gla);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

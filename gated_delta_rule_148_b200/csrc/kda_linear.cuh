@@ -1,0 +1,63 @@
+// Linear attention with a decay for each head: what its kernels share.
+//
+//   S_t = a_t S_{t-1} + k_t v_t^T,  o_t = S_t^T q_t,  a_t = exp(log_alpha_t)
+// A sequence is cut into chunks of C tokens and segments of `per` chunks.  With b the running
+// sum of log2 a inside a chunk (inclusive) and S the state at the chunk's start,
+//   O = tril(Q K^T o 2^{b_t - b_s}) V + Diag(2^b) Q S,   S' = 2^{b_C} S + (Diag(2^{b_C - b}) K)^T V.
+// Every exponent is <= 0, so nothing overflows for any log_alpha <= 0.  b is summed in 64 bits
+// and kept as hi + lo floats: after a strong decay b is large against the differences
+// that still matter, and a float's step there would show in the fp32 outputs.  A step below
+// 2^-400 counts as 2^-400: both are 0 against any fp32 value, and the sum keeps its digits.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace lin {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs).
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+__host__ __device__ inline size_t table_bytes(int B) { return align256((size_t)(B + 1) * 4); }
+__host__ __device__ inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
+
+// A segment's sequence, rows [begin, end) and first row of the sequence's next segment.
+struct Segment {
+  int b, begin, end;
+  bool last;         // the sequence's last segment
+};
+__device__ __forceinline__ Segment locate(const int32_t *cu, const int *sbase, int num_seqs, int seg, int tokens) {
+  int lo = 0, hi = num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sbase[mid] <= seg) lo = mid; else hi = mid - 1;
+  }
+  Segment s;
+  s.b = lo;
+  const int e = cu[lo + 1];
+  s.begin = cu[lo] + (seg - sbase[lo]) * tokens;
+  s.end = min(e, s.begin + tokens);
+  s.last = s.begin + tokens >= e;
+  return s;
+}
+
+__device__ __forceinline__ double shfl_up_f64(double x, int o) {
+  return __hiloint2double(__shfl_up_sync(0xFFFFFFFFu, __double2hiint(x), o),
+                          __shfl_up_sync(0xFFFFFFFFu, __double2loint(x), o));
+}
+__device__ __forceinline__ double shfl_f64(double x, int lane) {
+  return __hiloint2double(__shfl_sync(0xFFFFFFFFu, __double2hiint(x), lane),
+                          __shfl_sync(0xFFFFFFFFu, __double2loint(x), lane));
+}
+
+// log2 of token `pos`'s decay for head h; 0 past the end and at pads.
+__device__ __forceinline__ double log2_decay(const float *la, int decay_head, const uint8_t *mask, int pos, int end,
+                                             int h, int H) {
+  if (pos >= end || (mask != nullptr && mask[pos] == 0)) return 0.0;
+  const float x = la[decay_head ? (size_t)h : (size_t)pos * H + h];
+  return fmax((double)x * 1.4426950408889634074, -400.0);
+}
+
+}  // namespace lin
+}  // namespace kda

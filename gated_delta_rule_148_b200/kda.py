@@ -30,11 +30,18 @@ KDA_F32 = 0
 KDA_BF16 = 1
 KDA_GATE_CHANNEL = 0
 KDA_GATE_HEAD = 1
+KDA_E4M3 = 2
+KDA_I8 = 3
+KDA_DECAY_TOKEN = 0
+KDA_DECAY_HEAD = 1
 
 EXPORTED = ("kda_prefill", "kda_prefill_workspace_size", "kda_decode", "kda_get_device_status",
             "kda_status_string", "kda_version", "kda_prefill_noalloc", "kda_short_conv",
             "kda_prefill_backward", "kda_prefill_backward_workspace_size", "kda_debug_set_fault",
-            "kda_debug_timeout_site")
+            "kda_debug_timeout_site", "kda_linear_prefill", "kda_linear_prefill_workspace_size",
+            "kda_linear_decode", "kda_linear_prefill_backward",
+            "kda_linear_prefill_backward_workspace_size", "kda_rms_norm", "kda_rms_norm_backward",
+            "kda_rms_norm_backward_workspace_size")
 KDA_FAULT_STARVE_STATE_LOADS = 1
 
 
@@ -89,6 +96,54 @@ class BackwardArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("num_seqs", ctypes.c_int),
+                ("total_tokens", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("log_alpha", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("pad_mask", ctypes.c_void_p),
+                ("init_state", ctypes.c_void_p), ("o", ctypes.c_void_p),
+                ("final_state", ctypes.c_void_p), ("decay", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class LinearDecodeArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_alpha", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("o", ctypes.c_void_p), ("decay", ctypes.c_int)]
+
+
+class LinearBackwardArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("num_seqs", ctypes.c_int),
+                ("total_tokens", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("log_alpha", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("pad_mask", ctypes.c_void_p),
+                ("init_state", ctypes.c_void_p), ("decay", ctypes.c_int),
+                ("grad_o", ctypes.c_void_p), ("grad_final_state", ctypes.c_void_p),
+                ("grad_q", ctypes.c_void_p), ("grad_k", ctypes.c_void_p),
+                ("grad_v", ctypes.c_void_p), ("grad_log_alpha", ctypes.c_void_p),
+                ("grad_init_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("D", ctypes.c_int), ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("group", ctypes.c_int),
+                ("y", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("residual_out", ctypes.c_void_p)]
+
+
+class RmsNormBackwardArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_int64), ("D", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("grad_y", ctypes.c_void_p), ("grad_residual", ctypes.c_void_p),
+                ("grad_x", ctypes.c_void_p), ("grad_weight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -127,6 +182,14 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
             lib.kda_debug_set_fault.restype = ctypes.c_int
             lib.kda_debug_timeout_site.argtypes = [ctypes.c_void_p]
             lib.kda_debug_timeout_site.restype = ctypes.c_int
+            for name, args in (("kda_linear_prefill", LinearArgs), ("kda_linear_decode", LinearDecodeArgs),
+                               ("kda_linear_prefill_backward", LinearBackwardArgs),
+                               ("kda_rms_norm", RmsNormArgs), ("kda_rms_norm_backward", RmsNormBackwardArgs)):
+                getattr(lib, name).argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+                getattr(lib, name).restype = ctypes.c_int
+                if hasattr(lib, name + "_workspace_size"):
+                    getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args)]
+                    getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -415,3 +478,247 @@ def prefill_noalloc(q, k, v, log_alpha, beta, cu_seqlens, o, final_state=None,
     if st != KDA_OK:
         raise KdaError(st, "kda_prefill_noalloc")
     return o, final_state
+
+
+def decay_layout(log_alpha) -> int:
+    """KDA_DECAY_HEAD for a [H] log_alpha (a constant of the head), else KDA_DECAY_TOKEN ([rows, H])."""
+    return KDA_DECAY_HEAD if log_alpha.dim() == 1 else KDA_DECAY_TOKEN
+
+
+def _linear_common(a, q, k, v, log_alpha, rows: int, same_device=()):
+    """Checks what the linear-attention calls share and fills those fields of ``a``."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must be [rows, heads, dim]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    if Hk == 0 or H == 0 or H % Hk:
+        raise ValueError(f"the value heads ({H}) must be a multiple of the query/key heads ({Hk})")
+    _check_cuda("q", q, shape=(rows, Hk, dk))
+    _check_cuda("k", k, q.dtype, (rows, Hk, dk))
+    _check_cuda("v", v, q.dtype, (rows, H, dv))
+    head = decay_layout(log_alpha) == KDA_DECAY_HEAD
+    _check_cuda("log_alpha", log_alpha, torch.float32, (H,) if head else (rows, H))
+    a.dtype = _dtype_code(q)
+    a.H, a.Hk, a.dk, a.dv = H, Hk, dk, dv
+    a.q, a.k, a.v, a.log_alpha = _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha)
+    a.decay = decay_layout(log_alpha)
+    _check_device(q, k, v, log_alpha, *same_device)
+    return H, Hk, dk, dv
+
+
+def _check_device(first, *others):
+    """All tensors on one device, and that device current: a launch goes to the current one."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _workspace(a, name: str, workspace, device):
+    """The call's workspace: the caller's, or one of the size that the library states."""
+    nbytes = int(getattr(load(), name + "_workspace_size")(ctypes.byref(a)))
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    a.workspace = _ptr(workspace)
+    a.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor,
+                   cu_seqlens: torch.Tensor, pad_mask: Optional[torch.Tensor] = None,
+                   init_state: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                   final_state: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, want_final_state: bool = True,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head over a packed batch (kda_linear_prefill):
+    S_t = exp(log_alpha_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.  Returns (o, final_state).
+
+    q, k [N,Hk,dk] and v [N,H,dv] bf16 or fp32, H a multiple of Hk (value head h reads
+    query/key head h // (H // Hk)); log_alpha fp32 [N,H] (per token) or [H] (a constant of
+    the head); cu_seqlens [B+1] int32; pad_mask [N] uint8 or None; init_state [B,H,dk,dv]
+    fp32 or None.  Outputs are allocated here when not given."""
+    a = LinearArgs()
+    N, B = q.shape[0], cu_seqlens.numel() - 1
+    H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, N,
+                                   (cu_seqlens, pad_mask, init_state, o, final_state, workspace))
+    _check_cuda("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _check_cuda("pad_mask", pad_mask, torch.uint8, (N,))
+    _check_cuda("init_state", init_state, torch.float32, (B, H, dk, dv))
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    _check_cuda("o", o, q.dtype, (N, H, dv))
+    if final_state is None and want_final_state:
+        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    _check_cuda("final_state", final_state, torch.float32, (B, H, dk, dv))
+    a.num_seqs, a.total_tokens = B, N
+    a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
+    a.o, a.final_state = _ptr(o), _ptr(final_state)
+    workspace = _workspace(a, "kda_linear_prefill", workspace, q.device)
+    st = load().kda_linear_prefill(ctypes.byref(a), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_prefill")
+    return o, final_state
+
+
+def linear_prefill_workspace(N: int, B: int, H: int, Hk: int, dk: int, dv: int,
+                             dtype: torch.dtype = torch.bfloat16, device="cuda") -> torch.Tensor:
+    """A workspace for linear_prefill calls of these sizes (to be allocated once, e.g. before
+    a CUDA graph capture); calls that may overlap on the GPU need one each."""
+    a = LinearArgs()
+    a.dtype = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    a.num_seqs, a.total_tokens, a.H, a.Hk, a.dk, a.dv = B, N, H, Hk, dk, dv
+    nbytes = int(load().kda_linear_prefill_workspace_size(ctypes.byref(a)))
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+def linear_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor,
+                  state: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                  o: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One linear-attention step for each row (kda_linear_decode); ``state`` [B,H,dk,dv] fp32
+    is updated in place.  q, k [B,Hk,dk], v [B,H,dv], log_alpha [B,H] or [H], mask [B] uint8."""
+    a = LinearDecodeArgs()
+    B = q.shape[0]
+    H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, B, (state, mask, o))
+    _check_cuda("mask", mask, torch.uint8, (B,))
+    _check_cuda("state", state, torch.float32, (B, H, dk, dv))
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    _check_cuda("o", o, q.dtype, (B, H, dv))
+    a.B = B
+    a.mask, a.state, a.o = _ptr(mask), _ptr(state), _ptr(o)
+    st = load().kda_linear_decode(ctypes.byref(a), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_decode")
+    return o
+
+
+def linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_state=None, pad_mask=None,
+                            init_state=None, want_grad_init_state: bool = True, workspace=None, stream=None):
+    """Backward of linear_prefill (kda_linear_prefill_backward).  grad_o [N,H,dv] has the type
+    of q; grad_final_state [B,H,dk,dv] is fp32 or None.  Returns a dict: dq, dk, dv in the type
+    of q (summed over the value heads of a shared query/key head), dlog_alpha fp32 in
+    log_alpha's layout, dS0 fp32 (None unless wanted)."""
+    a = LinearBackwardArgs()
+    N, B = q.shape[0], cu_seqlens.numel() - 1
+    H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, N,
+                                   (cu_seqlens, grad_o, grad_final_state, pad_mask, init_state, workspace))
+    _check_cuda("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _check_cuda("pad_mask", pad_mask, torch.uint8, (N,))
+    _check_cuda("init_state", init_state, torch.float32, (B, H, dk, dv))
+    _check_cuda("grad_o", grad_o, q.dtype, (N, H, dv))
+    _check_cuda("grad_final_state", grad_final_state, torch.float32, (B, H, dk, dv))
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dlog_alpha": torch.empty_like(log_alpha),
+         "dS0": torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device) if want_grad_init_state else None}
+    a.num_seqs, a.total_tokens = B, N
+    a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
+    a.grad_o, a.grad_final_state = _ptr(grad_o), _ptr(grad_final_state)
+    a.grad_q, a.grad_k, a.grad_v = _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"])
+    a.grad_log_alpha, a.grad_init_state = _ptr(g["dlog_alpha"]), _ptr(g["dS0"])
+    workspace = _workspace(a, "kda_linear_prefill_backward", workspace, q.device)
+    st = load().kda_linear_prefill_backward(ctypes.byref(a), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_prefill_backward")
+    return g
+
+
+def _norm_rows(x: torch.Tensor) -> Tuple[int, int]:
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    D = x.shape[-1]
+    return (x.numel() // D if D else 0), D
+
+
+def _rms_norm(x, weight, residual, eps, out_dtype, group, y, scale, residual_out, stream):
+    rows, D = _norm_rows(x)
+    _check_cuda("x", x)
+    _check_cuda("weight", weight, torch.float32, (D,))
+    _check_cuda("residual", residual, x.dtype, x.shape)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    _check_cuda("residual_out", residual_out, x.dtype, x.shape)
+    _check_device(x, weight, residual, y, scale, residual_out)
+    a = RmsNormArgs()
+    a.dtype, a.out_dtype = _dtype_code(x), out_dtype
+    a.rows, a.D, a.eps, a.group = rows, D, float(eps), int(group)
+    a.x, a.residual, a.weight = _ptr(x), _ptr(residual), _ptr(weight)
+    a.y, a.scale, a.residual_out = _ptr(y), _ptr(scale), _ptr(residual_out)
+    st = load().kda_rms_norm(ctypes.byref(a), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rms_norm")
+    return residual_out
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, y: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Root-mean-square norm over the last dimension (kda_rms_norm), of r = x + residual if a
+    residual is given.  x [.., D] bf16 or fp32, D a multiple of 8 up to 16384; weight [D] fp32
+    or None (ones).  Returns (y, r), r None without a residual; residual_out may be the
+    residual itself."""
+    if y is None:
+        y = torch.empty_like(x)
+    _check_cuda("y", y, x.dtype, x.shape)
+    return y, _rms_norm(x, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out, stream)
+
+
+_BYTE_TYPES = {"e4m3": (KDA_E4M3, torch.float8_e4m3fn), "int8": (KDA_I8, torch.int8)}
+
+
+def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, eps: float = 1e-6, quant: str = "e4m3",
+                   group: int = 128, y: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                   residual_out: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """rms_norm with an 8-bit output: quant "e4m3" or "int8", one fp32 scale per group of 32,
+    64 or 128 columns, or per row (group 0).  Returns (y8 [.., D], scale [.., ceil(D / group)],
+    r); y is approximately y8 * scale."""
+    if quant not in _BYTE_TYPES:
+        raise ValueError(f"quant must be one of {sorted(_BYTE_TYPES)}, got {quant!r}")
+    code, tdt = _BYTE_TYPES[quant]
+    _, D = _norm_rows(x)
+    if group < 0:
+        raise ValueError("group must be 0, 32, 64 or 128")
+    n = -(-D // group) if group else 1
+    if y is None:
+        y = torch.empty(x.shape, dtype=tdt, device=x.device)
+    if scale is None:
+        scale = torch.empty((*x.shape[:-1], n), dtype=torch.float32, device=x.device)
+    _check_cuda("y", y, tdt, x.shape)
+    _check_cuda("scale", scale, torch.float32, (*x.shape[:-1], n))
+    r = _rms_norm(x, weight, residual, eps, code, group, y, scale, residual_out, stream)
+    return y, scale, r
+
+
+def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: torch.Tensor,
+                      grad_residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      grad_x: Optional[torch.Tensor] = None, want_grad_weight: bool = True,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Backward of rms_norm (kda_rms_norm_backward).  x is the normalised input (r, or x without
+    a residual); grad_residual is the gradient that reaches r along the residual stream.
+    Returns (grad_x, grad_weight): the gradient of r, which is that of x and of the residual, in
+    the type of x (grad_x may be grad_residual itself), and of weight [D] fp32."""
+    rows, D = _norm_rows(x)
+    _check_cuda("x", x)
+    _check_cuda("weight", weight, torch.float32, (D,))
+    _check_cuda("grad_y", grad_y, x.dtype, x.shape)
+    _check_cuda("grad_residual", grad_residual, x.dtype, x.shape)
+    if grad_x is None:
+        grad_x = torch.empty_like(x)
+    _check_cuda("grad_x", grad_x, x.dtype, x.shape)
+    _check_device(x, weight, grad_y, grad_residual, grad_x, workspace)
+    grad_weight = torch.empty(D, dtype=torch.float32, device=x.device) if want_grad_weight else None
+    a = RmsNormBackwardArgs()
+    a.dtype, a.rows, a.D, a.eps = _dtype_code(x), rows, D, float(eps)
+    a.x, a.weight, a.grad_y, a.grad_residual = _ptr(x), _ptr(weight), _ptr(grad_y), _ptr(grad_residual)
+    a.grad_x, a.grad_weight = _ptr(grad_x), _ptr(grad_weight)
+    if want_grad_weight:
+        workspace = _workspace(a, "kda_rms_norm_backward", workspace, x.device)
+    st = load().kda_rms_norm_backward(ctypes.byref(a), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rms_norm_backward")
+    return grad_x, grad_weight

@@ -60,7 +60,8 @@ typedef enum {
   KDA_ERR_DEVICE_CHECK = 5    /* a device-side argument check failed */
 } kda_status;
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* KDA_E4M3 and KDA_I8 are output types of kda_rms_norm() only. */
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_E4M3 = 2, KDA_I8 = 3 } kda_dtype;
 
 /*
  * Layout of log_alpha.  KDA_GATE_CHANNEL: one decay per key channel, [.., H, dk]
@@ -316,6 +317,206 @@ typedef struct {
 
 size_t kda_prefill_backward_workspace_size(const kda_backward_args *args);
 kda_status kda_prefill_backward(const kda_backward_args *args, void *stream);
+
+/*
+ * Linear attention with a decay for each head (the additive recurrence, without
+ * KDA's removal of the old projection onto the key):
+ *   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_t = exp(log_alpha_t)
+ * per sequence b and value head h, with the state S d_k x d_v in fp32.  The same
+ * conventions as kda_prefill: packed variable-length batch, pads are identity
+ * steps with o = 0 whatever they hold (nothing at a pad is read but its mask),
+ * optional initial and final state.  Any result is independent of how the
+ * library cuts sequences beyond rounding, and the same call gives the same bits.
+ *
+ * Fields (device pointers, caller-owned):
+ *   dtype        type of q, k, v and o (KDA_BF16 or KDA_F32); everything else fp32.
+ *   num_seqs     B >= 0; total_tokens N >= 0; H >= 1 value heads; Hk >= 1 query/key
+ *                heads, a divisor of H: value head h reads query/key head
+ *                h / (H / Hk).  dk, dv: each 64 or 128.
+ *   q, k         [N, Hk, dk]; v, o [N, H, dv]; 16-byte aligned.
+ *   log_alpha    decay = KDA_DECAY_TOKEN: [N, H], one decay per token and head;
+ *                decay = KDA_DECAY_HEAD: [H], a constant of the head.  Natural
+ *                log, finite and <= 0 (not checked; other values give unspecified
+ *                results).  A step below 2^-400 counts as 2^-400.
+ *   cu_seqlens   [B+1] int32 as for kda_prefill (checked on the device).
+ *   pad_mask     [N] uint8, 1 = valid; NULL = all valid.
+ *   init_state   [B, H, dk, dv] fp32, 16-byte aligned; NULL = 0.
+ *   final_state  [B, H, dk, dv] fp32, 16-byte aligned, or NULL (not written); may be
+ *                the same pointer as init_state, may not otherwise overlap an input.
+ *   o            must not overlap any input.
+ *   workspace    kda_linear_prefill_workspace_size() bytes, 256-byte aligned: the
+ *                state at the start of every segment of a sequence.  Calls that may
+ *                overlap on the GPU need workspaces of their own.
+ * Numerics: products of bf16 inputs are accumulated in fp32; for o the weights
+ * q.k a..a and the state are rounded to bf16 once as operands; final_state keeps fp32
+ * accuracy.  fp32 inputs keep fp32 accuracy throughout.
+ */
+typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1 } kda_decay;
+
+typedef struct {
+  kda_dtype dtype;
+  int num_seqs;
+  int total_tokens;
+  int H;
+  int Hk;
+  int dk;
+  int dv;
+  const void *q;
+  const void *k;
+  const void *v;
+  const float *log_alpha;
+  const int32_t *cu_seqlens;
+  const uint8_t *pad_mask;
+  const float *init_state;
+  void *o;
+  float *final_state;
+  kda_decay decay;
+  void *workspace;
+  size_t workspace_bytes;
+} kda_linear_args;
+
+/* Bytes of workspace (reads dtype, sizes and decay).  0 if args is NULL or invalid. */
+size_t kda_linear_prefill_workspace_size(const kda_linear_args *args);
+kda_status kda_linear_prefill(const kda_linear_args *args, void *stream);
+
+/*
+ * One step of the same recurrence for each of B independent rows, all heads.
+ *   q, k [B, Hk, dk]; v, o [B, H, dv] of dtype; log_alpha [B, H] or [H] fp32
+ *   (decay); mask [B] uint8 (1 = active, NULL = all active); state [B, H, dk, dv]
+ *   fp32, updated in place, 16-byte aligned; o must not overlap any other argument.
+ * A masked row's state is neither read nor written and its o is written as 0.
+ */
+typedef struct {
+  kda_dtype dtype;
+  int B;
+  int H;
+  int Hk;
+  int dk;
+  int dv;
+  const void *q;
+  const void *k;
+  const void *v;
+  const float *log_alpha;
+  const uint8_t *mask;
+  float *state;
+  void *o;
+  kda_decay decay;
+} kda_linear_decode_args;
+
+kda_status kda_linear_decode(const kda_linear_decode_args *args, void *stream);
+
+/*
+ * Backward pass of kda_linear_prefill (training): the gradients of <o, grad_o> +
+ * <final_state, grad_final_state> with respect to q, k, v, log_alpha and
+ * init_state.  dtype .. init_state and decay as for kda_linear_prefill.
+ *   grad_o           [N, H, dv] of dtype, 16-byte aligned.
+ *   grad_final_state [B, H, dk, dv] fp32 or NULL (zero).
+ *   grad_q, grad_k   [N, Hk, dk], grad_v [N, H, dv] of dtype (the types in which
+ *                    training hands them on); of a shared query/key head the sum
+ *                    over its value heads, taken in fp32.
+ *   grad_log_alpha   fp32, the layout of log_alpha ([H]: the sum over the tokens).
+ *   grad_init_state  [B, H, dk, dv] fp32 or NULL (not written).
+ *                    Outputs 16-byte aligned (grad_log_alpha 4), not overlapping any
+ *                    input or each other; pads get zero gradients.
+ *   workspace        kda_linear_prefill_backward_workspace_size() bytes, 256-byte aligned.
+ * Sums over shared heads and tokens are taken in a fixed order: the same call gives
+ * the same bits.
+ */
+typedef struct {
+  kda_dtype dtype;
+  int num_seqs;
+  int total_tokens;
+  int H;
+  int Hk;
+  int dk;
+  int dv;
+  const void *q;
+  const void *k;
+  const void *v;
+  const float *log_alpha;
+  const int32_t *cu_seqlens;
+  const uint8_t *pad_mask;
+  const float *init_state;
+  kda_decay decay;
+  const void *grad_o;
+  const float *grad_final_state;
+  void *grad_q;
+  void *grad_k;
+  void *grad_v;
+  float *grad_log_alpha;
+  float *grad_init_state;
+  void *workspace;
+  size_t workspace_bytes;
+} kda_linear_backward_args;
+
+size_t kda_linear_prefill_backward_workspace_size(const kda_linear_backward_args *args);
+kda_status kda_linear_prefill_backward(const kda_linear_backward_args *args, void *stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition and an optional
+ * 8-bit output with scales:
+ *   r = x + residual (rounded to dtype; r = x without a residual)
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ * Fields (device pointers, caller-owned):
+ *   dtype        type of x, residual, residual_out (KDA_BF16 or KDA_F32).
+ *   out_dtype    type of y: dtype, KDA_E4M3 or KDA_I8 (8 bits, with scale).
+ *   rows >= 0; D columns: a multiple of 8, 8 .. 16384.
+ *   x            [rows, D]; residual [rows, D] or NULL; y [rows, D]; 16-byte aligned
+ *                (an 8-bit y: 8-byte).
+ *   weight       [D] fp32, 16-byte aligned, or NULL (ones).  eps >= 0, finite.
+ *   group        8-bit output: 0 = one scale per row, or 32, 64 or 128 = one scale per
+ *                group of that many columns (the last may be short).
+ *   scale        8-bit output: fp32 [rows, 1] or [rows, ceil(D / group)]:
+ *                max(max|y|, 2^-100) / 448 (e4m3) or / 127 (int8), and the stored value is
+ *                y / scale rounded to nearest even.  A NaN in a group makes its scale NaN.
+ *   residual_out [rows, D] r, or NULL; needs residual; may be the same pointer as residual.
+ * Outputs may not otherwise overlap an input or each other.  Allocates nothing.
+ */
+typedef struct {
+  kda_dtype dtype;
+  kda_dtype out_dtype;
+  int64_t rows;
+  int D;
+  const void *x;
+  const void *residual;
+  const float *weight;
+  float eps;
+  int group;
+  void *y;
+  float *scale;
+  void *residual_out;
+} kda_rms_norm_args;
+
+kda_status kda_rms_norm(const kda_rms_norm_args *args, void *stream);
+
+/*
+ * Backward pass of kda_rms_norm (the output before any 8-bit rounding).
+ *   x             [rows, D] of dtype: the normalised input (residual_out, or x).
+ *   grad_y        [rows, D] of dtype; grad_residual [rows, D] of dtype or NULL: the
+ *                 gradient that reaches r along the residual stream, added to grad_x.
+ *   grad_x        [rows, D] of dtype: the gradient of r, which is that of x and of the
+ *                 residual; may be the same pointer as grad_residual.
+ *   grad_weight   [D] fp32 or NULL (not computed); the sum over rows in fp32, in a fixed order.
+ *   workspace     kda_rms_norm_backward_workspace_size() bytes, 256-byte aligned; NULL
+ *                 without grad_weight.
+ */
+typedef struct {
+  kda_dtype dtype;
+  int64_t rows;
+  int D;
+  const void *x;
+  const float *weight;
+  float eps;
+  const void *grad_y;
+  const void *grad_residual;
+  void *grad_x;
+  float *grad_weight;
+  void *workspace;
+  size_t workspace_bytes;
+} kda_rms_norm_backward_args;
+
+size_t kda_rms_norm_backward_workspace_size(const kda_rms_norm_backward_args *args);
+kda_status kda_rms_norm_backward(const kda_rms_norm_backward_args *args, void *stream);
 
 /* Synchronise `stream`, then return and clear the error latched on the
  * current device by earlier kernels (KDA_OK if none). */
