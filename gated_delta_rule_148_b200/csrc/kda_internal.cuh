@@ -163,6 +163,9 @@ size_t backward_workspace(int N, int B, int H, int dk, int dv);
 cudaError_t launch_backward(const BackwardParams &p, bool bf16, cudaStream_t s);
 size_t linear_prefill_workspace(const LinearParams &p, bool bf16);
 cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t s);
+// bf16 inputs: tensor-core kernels (kda_linear_tc.cu).
+size_t linear_prefill_tc_workspace(const LinearParams &p);
+cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s);
 size_t linear_backward_workspace(const LinearParams &p, bool bf16);
 cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_linear_decode(const LinearDecodeParams &p, bool bf16, cudaStream_t s);

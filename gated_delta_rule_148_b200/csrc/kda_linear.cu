@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *s
 }
 
 // ------------------------------------------------------------------ prefill rows
-template <int DK, bool BF16>
+template <int DK>
 __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const int *sbase, const float *start, int tokens) {
   constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
   extern __shared__ float sm[];
@@ -292,9 +292,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
   for (int j = 0; j < chunks; ++j) {
     const int pos0 = sg.begin + j * C;
     __syncthreads();
-    load_rows<DK, LK, BF16>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<DK, LK, BF16>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<kSlice, LV, BF16>(sv, p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    load_rows<DK, LK, false>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<DK, LK, false>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV, false>(sv, p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
     each(S, [&](int r, int n, float &x) { sS[(m0 * MT + r) * LV + n0 + n] = x; });
     if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
     __syncthreads();
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
                    [&](int k, int n) { return sv[k * LV + n0 + n]; });
     each(o, [&](int r, int n, float &x) {
       const int pos = pos0 + m0 + r;
-      if (pos < sg.end) store_elem<BF16>(p.o, ((size_t)pos * p.H + h) * p.dv + c0 + n0 + n, x);
+      if (pos < sg.end) store_elem<false>(p.o, ((size_t)pos * p.H + h) * p.dv + c0 + n0 + n, x);
     });
     if (j + 1 < chunks) {
       each(S, [&](int, int, float &x) { x *= dec.whole; });
@@ -597,6 +597,7 @@ cudaError_t launch_linear_chain(const LinearParams &p, const int *sbase, float *
 
 size_t linear_prefill_workspace(const LinearParams &p, bool bf16) {
   using namespace lin;
+  if (bf16) return linear_prefill_tc_workspace(p);
   const int per = segment_chunks(p.N, p.num_seqs, p.H * (p.dv / kSlice), C);
   const size_t segs = max_segments(p.N, p.num_seqs, C * per);
   return table_bytes(p.num_seqs) + align256(segs * p.H * 4) + state_bytes(p, segs);
@@ -605,6 +606,7 @@ size_t linear_prefill_workspace(const LinearParams &p, bool bf16) {
 cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t s) {
   using namespace lin;
   if (p.num_seqs == 0) return cudaSuccess;
+  if (bf16) return launch_linear_prefill_tc(p, s);
   const int per = segment_chunks(p.N, p.num_seqs, p.H * (p.dv / kSlice), C), tokens = C * per;
   const size_t segs = max_segments(p.N, p.num_seqs, tokens);
   unsigned char *w = static_cast<unsigned char *>(p.ws);
@@ -615,8 +617,7 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   if (e != cudaSuccess) return e;
   e = launch_parts_chain(p, bf16, sbase, part, nullptr, whole, segs, tokens, s);
   if (e != cudaSuccess || p.N == 0) return e;
-  auto kern = p.dk == 128 ? (bf16 ? rows_kernel<128, true> : rows_kernel<128, false>)
-                          : (bf16 ? rows_kernel<64, true> : rows_kernel<64, false>);
+  auto kern = p.dk == 128 ? rows_kernel<128> : rows_kernel<64>;
   const size_t smem = p.dk == 128 ? rows_smem<128>() : rows_smem<64>();
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
