@@ -37,7 +37,6 @@ enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" :: "r"(id) : "memory"); }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
                :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
@@ -55,19 +54,63 @@ struct Maps {
   CUtensorMap q, k, v, o;
 };
 
+// 2^x with results below 2^-126 taken as 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 32 fp32 columns of this thread's TMEM lane: issue, and wait for all loads issued before.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The registers pass through the wait, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
 // Bounded waits of one block.  After one has run out every role leaves its loop; the waits of the
-// others then run out too.
+// others then end too.
 struct Waits {
   long long limit;
   unsigned *err, *site;
   volatile int *failed;
-  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity, unsigned code) const {
-    if (*failed) return false;
-    if (mbar_wait(bar, parity & 1, limit)) return true;
-    note_timeout(site, code);
-    atomicOr(err, ERR_BIT_TIMEOUT);
-    *failed = 1;
-    return false;
+  static __device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+  }
+  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t phase, unsigned code) const {
+    const uint32_t parity = phase & 1;
+    if (test(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!test(bar, parity)) {
+      if (*failed) return false;
+      if (clock64() - t0 > limit) {
+        note_timeout(site, code);
+        atomicOr(err, ERR_BIT_TIMEOUT);
+        *failed = 1;
+        return false;
+      }
+    }
+    return true;
   }
 };
 
@@ -75,26 +118,42 @@ struct Waits {
 template <int D>
 __device__ __forceinline__ void clear_rows(unsigned char *tile, const uint32_t *valid) {
   const int lane = threadIdx.x & 31;
-  for (int i = lane; i < C * (D / 8); i += 32) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    if (!((valid[r >> 5] >> (r & 31)) & 1))
-      *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
-  }
+  for (int w = 0; w < C / 32; ++w)
+    for (uint32_t pads = ~valid[w]; pads != 0; pads &= pads - 1) {
+      const int r = 32 * w + __ffs((int)pads) - 1;
+      if (lane < D / 8) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, lane >> 3, lane & 7, C)) = make_uint4(0, 0, 0, 0);
+    }
 }
 
-// log2 decays of a chunk by one warp: lane's rows 4 lane .. 4 lane + 3, inclusive sums b and the total.
-// word: lanes 0, 8, 16 and 24 get the bits of rows 32 (lane / 8) .. + 31 that are real tokens; returns
-// whether all 128 are.
-__device__ __forceinline__ bool scan_chunk(const LinearParams &p, int pos0, int end, int h, double (&b)[4],
-                                           double &total, uint32_t &word) {
-  const int lane = threadIdx.x & 31;
-  double s = 0.0;
-  uint32_t bits = 0;
+// A chunk's decays, one warp: lane's rows 4 lane .. 4 lane + 3.  Loading is apart from summing, so that the
+// next chunk's values are on their way while this one's are used.
+struct RawDecays {
+  float x[4];
+  uint32_t bits;        // bit e: row 4 lane + e is a real token
+};
+__device__ __forceinline__ RawDecays load_decays(const LinearParams &p, int pos0, int end, int h) {
+  RawDecays d;
+  const int pos = pos0 + 4 * (threadIdx.x & 31);
+  uint8_t m[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int pos = pos0 + 4 * lane + e;
-    if (pos < end && (p.mask == nullptr || p.mask[pos] != 0)) bits |= 1u << e;
-    s += lin::log2_decay(p.log_alpha, p.decay_head, p.mask, pos, end, h, p.H);
+    const bool in = pos + e < end;
+    m[e] = in ? (p.mask != nullptr ? p.mask[pos + e] : (uint8_t)1) : (uint8_t)0;
+    d.x[e] = in ? p.log_alpha[p.decay_head ? (size_t)h : (size_t)(pos + e) * p.H + h] : 0.f;
+  }
+  d.bits = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d.bits |= (uint32_t)(m[e] != 0) << e;
+  return d;
+}
+// Inclusive sums b of log2 a, the total; word: lanes 0, 8, 16, 24 get the bits of rows 32 (lane / 8) .. + 31.
+// Returns whether all 128 rows are real tokens.
+__device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], double &total, uint32_t &word) {
+  const int lane = threadIdx.x & 31;
+  double s = 0.0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((d.bits >> e) & 1) s += fmax((double)d.x[e] * 1.4426950408889634074, -400.0);
     b[e] = s;
   }
   double x = s;
@@ -106,11 +165,11 @@ __device__ __forceinline__ bool scan_chunk(const LinearParams &p, int pos0, int 
   total = lin::shfl_f64(x, 31);
 #pragma unroll
   for (int e = 0; e < 4; ++e) b[e] += x - s;
-  word = bits << (4 * (lane & 7));
+  word = d.bits << (4 * (lane & 7));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  return __all_sync(0xFFFFFFFFu, bits == 0xFu);
+  return __all_sync(0xFFFFFFFFu, d.bits == 0xFu);
 }
 
 // 8 bf16 of a 16-byte word as floats.
@@ -135,14 +194,27 @@ __device__ __forceinline__ uint4 take_bf16(float (&f)[8]) {
 }
 
 // ============================================================ parts
+// A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
+// weights; the others follow.  It goes from a segment's last chunk to its first and stops once every
+// weight that is left is 0 in fp32 (decays of 2^-151 and less): those rows are not read, their share is 0.
 constexpr int kPartsThreads = 8 * 32 + 64;      // two warpgroups, a TMA + MMA warp, a preparing warp
+constexpr int kRing = 4;
+
+struct PartsStep {
+  int item;           // segment x H + h; -1: no more
+  int pos;            // first row of the chunk
+  int h;
+  int first, last;    // of the item's chunks, in the order taken
+};
 
 template <int DK, int DV>
 struct PartsSmem {
   static constexpr uint32_t KT = C * DK * 2, VT = C * DV * 2;
-  static constexpr uint32_t STAGE = KT + VT, W = 2 * STAGE, TAB = W + 3 * VT;
+  static constexpr uint32_t STAGE = KT + VT, W = 2 * STAGE;          // W: the three parts of w V
   // DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and are not used
-  static constexpr uint32_t WGT = TAB, VALID = WGT + 2 * C * 4, BARS = VALID + 32, END = BARS + 128;
+  static constexpr uint32_t WGT = W + 3 * VT, VALID = WGT + kRing * C * 4, STEPS = VALID + kRing * 16;
+  static constexpr uint32_t BARS = STEPS + kRing * 32, END = BARS + 20 * 8;
+  static_assert(END <= 232448, "shared memory of a block");
 };
 
 template <int DK, int DV>
@@ -153,20 +225,25 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nitems = sbase[p.num_seqs] * p.H;
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4,
-           *w_ready = full + 6, *w_free = full + 7, *s_done = full + 8, *s_free = full + 10, *drain = full + 12;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 13);
+  uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
+  volatile PartsStep *steps = reinterpret_cast<volatile PartsStep *>(sm + L::STEPS);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + 2, *planned = full + 4,
+           *done = planned + kRing, *w_ready = done + kRing, *w_free = w_ready + 1, *s_done = w_ready + 2,
+           *s_free = s_done + 2, *drain = s_free + 2;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
-  if (warp == 8) tmem_alloc(tmem_sh, 256);
+  if (warp == 8) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(ready + i, 1);
       mbar_init(empty + i, 1);
       mbar_init(s_done + i, 1);
       mbar_init(s_free + i, 256);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(planned + i, 1);
+      mbar_init(done + i, 1);
     }
     mbar_init(w_ready, 256);
     mbar_init(w_free, 1);
@@ -179,155 +256,180 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   const uint32_t tm = *tmem_sh;
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int G = p.H / p.Hk;
-  int step = 0, n = 0;      // chunks and items that this role has begun
-
-  // the last segment of a sequence matters to the final state only
-  auto skip = [&](const Segment &sg) { return sg.last && p.final_state == nullptr; };
+  constexpr int kCols = 256;      // TMEM columns of an item's accumulators: DV of w V's first part, DV of the others
 
   if (warp == 8) {
     // ---------------- loads and MMAs (one thread)
     if (lane == 0) {
-      auto load = [&](const Segment &sg, int h, int c, int st) {
+      int loaded = 0, n = 0;
+      bool ok = true, more = true;
+      auto load_next = [&]() {
+        if (!more || !ok) return;
+        const int rs = loaded % kRing, st = loaded & 1;
+        ok = wait(planned + rs, loaded / kRing, SITE_PARTS);
+        if (!ok) return;
+        const int pos = steps[rs].pos, h = steps[rs].h;
+        if (steps[rs].item < 0) { more = false; return; }
+        if (loaded >= 2) ok = wait(empty + st, (loaded >> 1) - 1, SITE_PARTS + 1);
+        if (!ok) return;
         mbar_arrive_expect_tx(full + st, L::STAGE);
         const uint32_t dst = smem_u32(sm + st * L::STAGE);
-        const int pos = sg.begin + c * C;
 #pragma unroll
         for (int kb = 0; kb < DK / 64; ++kb) tma_load_3d(dst + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
 #pragma unroll
         for (int kb = 0; kb < DV / 64; ++kb)
           tma_load_3d(dst + L::KT + kb * C * 128, &maps.v, kb * 64, h, pos, full + st);
-      };
-      // loads run one chunk ahead of the MMAs, over the items' borders
-      int li = blockIdx.x, lc = -1, lstep = 0;
-      Segment ls{};
-      auto advance = [&]() {            // next (item, chunk) to load
-        while (true) {
-          if (lc > 0) { --lc; return true; }
-          if (lc == 0) li += gridDim.x;
-          lc = -1;
-          if (li >= nitems) return false;
-          ls = lin::locate(p.cu, sbase, p.num_seqs, li / p.H, per * C);
-          if (!skip(ls)) { lc = (ls.end - ls.begin + C - 1) / C; }
-          else li += gridDim.x;
-        }
-      };
-      bool more = advance();
-      bool ok = true;
-      auto load_next = [&]() {
-        if (!more) return;
-        const int st = lstep & 1;
-        if (lstep >= 2) ok = ok && wait(empty + st, (lstep >> 1) - 1, SITE_PARTS);
-        if (!ok) return;
-        load(ls, li % p.H, lc, st);
-        ++lstep;
-        more = advance();
+        ++loaded;
       };
       load_next();
-      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
-        if (skip(sg)) continue;
-        const int chunks = (sg.end - sg.begin + C - 1) / C, acc = n & 1;
-        if (n >= 2) ok = wait(s_free + acc, (n >> 1) - 1, SITE_PARTS + 1);
-        for (int j = 0; j < chunks && ok; ++j, ++step) {
-          load_next();
-          const int st = step & 1;
-          ok = ok && wait(ready + st, step >> 1, SITE_PARTS + 2) && wait(w_ready, step, SITE_PARTS + 3);
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t sk = smem_u32(sm + st * L::STAGE), sw = smem_u32(sm + L::W);
-          const uint32_t id = idesc_bf16(128, DV, 1, 1);
+      for (int step = 0; ok && step < loaded; ++step) {
+        load_next();
+        const int st = step & 1, rs = step % kRing, acc = n & 1;
+        const bool first = steps[rs].first != 0, last = steps[rs].last != 0;
+        if (first && n >= 2) ok = ok && wait(s_free + acc, (n >> 1) - 1, SITE_PARTS + 2);
+        ok = ok && wait(w_ready, step, SITE_PARTS + 3);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t sk = smem_u32(sm + st * L::STAGE), sw = smem_u32(sm + L::W), d = tm + acc * kCols;
+        if constexpr (DV == 128) {      // first two parts side by side (N = 256), the third into the second's sum
 #pragma unroll
-          for (int x = 0; x < 3; ++x)
+          for (int s = 0; s < C / 16; ++s)
+            mma_bf16(d, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 256, 1, 1), !first || s > 0);
 #pragma unroll
-            for (int s = 0; s < C / 16; ++s)
-              mma_bf16(tm + acc * 128, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw + x * L::VT, C, 0, s), id,
-                       j > 0 || x > 0 || s > 0);
-          mma_commit(w_free);
-          mma_commit(empty + st);
-          if (j == chunks - 1) mma_commit(s_done + acc);
+          for (int s = 0; s < C / 16; ++s)
+            mma_bf16(d + DV, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw + 2 * L::VT, C, 0, s), idesc_bf16(128, DV, 1, 1), 1);
+        } else {
+#pragma unroll
+          for (int s = 0; s < C / 16; ++s)
+            mma_bf16(d, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 3 * DV, 1, 1), !first || s > 0);
         }
-        ++n;
+        mma_commit(w_free);
+        mma_commit(empty + st);
+        mma_commit(done + rs);
+        if (last) {
+          mma_commit(s_done + acc);
+          ++n;
+        }
       }
       if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i < lstep; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+        for (int i = 0; i < loaded; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
   } else if (warp == 9) {
-    // ---------------- weights and rows to clear, from a segment's last chunk to its first
-    uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
+    // ---------------- the plan
+    const int nitems = sbase[p.num_seqs] * p.H;
+    int step = 0;
     bool ok = true;
+    auto publish = [&](int item, int pos, int h, bool first, bool last) {      // entry reserved by the caller
+      if (lane == 0) {
+        volatile PartsStep &e = steps[step % kRing];
+        e.item = item;
+        e.pos = pos;
+        e.h = h;
+        e.first = first;
+        e.last = last;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(planned + step % kRing);
+      ++step;
+    };
+    auto reserve = [&]() {
+      if (step >= kRing) ok = wait(done + step % kRing, step / kRing - 1, SITE_PARTS + 4);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      return ok;
+    };
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
       const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
-      if (skip(sg)) continue;
+      // the last segment of a sequence matters to the final state only
+      if (sg.last && p.final_state == nullptr) continue;
       const int chunks = (sg.end - sg.begin + C - 1) / C, h = i % p.H;
       double after = 0.0;
-      for (int j = chunks - 1; j >= 0 && ok; --j, ++step) {
-        const int st = step & 1;
+      RawDecays raw = load_decays(p, sg.begin + (chunks - 1) * C, sg.end, h);
+      for (int j = chunks - 1; j >= 0; --j) {
+        const RawDecays now = raw;
+        if (j > 0) raw = load_decays(p, sg.begin + (j - 1) * C, sg.end, h);
         double b[4], total;
         uint32_t word;
-        const bool clean = scan_chunk(p, sg.begin + j * C, sg.end, h, b, total, word);
-        if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_PARTS + 4);
-        if ((lane & 7) == 0) valid[4 * st + (lane >> 3)] = word;
-        __syncwarp();
+        scan_decays(now, b, total, word);
+        if (!reserve()) break;
+        const int rs = step % kRing;
         float4 w;
-        w.x = exp2f((float)(after + (total - b[0])));
-        w.y = exp2f((float)(after + (total - b[1])));
-        w.z = exp2f((float)(after + (total - b[2])));
-        w.w = exp2f((float)(after + (total - b[3])));
-        reinterpret_cast<float4 *>(wgt + st * C)[lane] = w;
+        w.x = ex2((float)(after + (total - b[0])));
+        w.y = ex2((float)(after + (total - b[1])));
+        w.z = ex2((float)(after + (total - b[2])));
+        w.w = ex2((float)(after + (total - b[3])));
+        reinterpret_cast<float4 *>(wgt + rs * C)[lane] = w;
+        if ((lane & 7) == 0) valid[4 * rs + (lane >> 3)] = word;
         after += total;
-        ok = ok && wait(full + st, step >> 1, SITE_PARTS + 5);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!clean && ok) {
-          clear_rows<DK>(sm + st * L::STAGE, valid + 4 * st);
-          clear_rows<DV>(sm + st * L::STAGE + L::KT, valid + 4 * st);
-          fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(ready + st);
+        const bool last = j == 0 || after < -151.0;
+        publish(i, sg.begin + j * C, h, j == chunks - 1, last);
+        if (last) break;
       }
-      if (lane == 0) whole[i] = exp2f((float)after);
+      if (lane == 0) whole[i] = ex2((float)after);
     }
+    if (ok && reserve()) publish(-1, 0, 0, false, false);
   } else {
     // ---------------- w V in three parts; at a segment's end the state to global memory
     const int r = tid & 127, half = tid >> 7;          // row of the chunk (of the state), column half
     constexpr int NC = DV / 16;                        // 16-byte words of the half
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    bool ok = true;
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
-      if (skip(sg)) continue;
-      const int chunks = (sg.end - sg.begin + C - 1) / C, acc = n & 1;
-      for (int j = 0; j < chunks && ok; ++j, ++step) {
-        const int st = step & 1;
-        ok = wait(ready + st, step >> 1, SITE_PARTS + 6);
-        if (step >= 1) ok = ok && wait(w_free, step - 1, SITE_PARTS + 7);
-        if (!ok) break;
-        const float w = wgt[st * C + r];
-        const unsigned char *sv = sm + st * L::STAGE + L::KT;
+    int n = 0;
+    for (int step = 0;; ++step) {
+      const int st = step & 1, rs = step % kRing, acc = n & 1;
+      if (!wait(planned + rs, step / kRing, SITE_PARTS + 5)) break;
+      const int item = steps[rs].item;
+      if (item < 0) break;
+      const bool last = steps[rs].last != 0, real = (valid[4 * rs + (r >> 5)] >> (r & 31)) & 1;
+      const float w = wgt[rs * C + r];
+      if (!wait(full + st, step >> 1, SITE_PARTS + 6)) break;
+      unsigned char *sk = sm + st * L::STAGE, *sv = sk + L::KT;
+      uint4 u[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int cc = half * NC + c;
-          const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
-          float f[8];
-          unpack8(*reinterpret_cast<const uint4 *>(sv + at), f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= w;
-#pragma unroll
-          for (int x = 0; x < 3; ++x) *reinterpret_cast<uint4 *>(sm + L::W + x * L::VT + at) = take_bf16(f);
-        }
-        fence_async_smem();
-        mbar_arrive(w_ready);
+      for (int c = 0; c < NC; ++c) {
+        const int cc = half * NC + c;
+        u[c] = real ? *reinterpret_cast<const uint4 *>(sv + row_tile_chunk(r, cc >> 3, cc & 7, C)) : make_uint4(0, 0, 0, 0);
       }
-      ok = ok && wait(s_done + acc, n >> 1, SITE_PARTS + 8);
-      if (!ok) break;
+      if (!real)
+        for (int c = 0; c < DK / 16; ++c) {
+          const int cc = half * (DK / 16) + c;
+          *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
+        }
+      if (step > 0 && !wait(w_free, step - 1, SITE_PARTS + 7)) break;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int cc = half * NC + c;
+        const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
+        float f[8];
+        unpack8(u[c], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= w;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint4 *>(sm + L::W + x * L::VT + at) = take_bf16(f);
+      }
+      fence_async_smem();
+      mbar_arrive(w_ready);
+      if (!last) continue;
+      if (!wait(s_done + acc, n >> 1, SITE_PARTS + 8)) break;
       fence_after_sync();
-      float *out = part + ((size_t)i * DK + r) * DV + half * (DV / 2);
+      float *out = part + ((size_t)item * DK + r) * DV + half * (DV / 2);
 #pragma unroll
       for (int c = 0; c < DV / 64; ++c) {
+        const uint32_t col = tm + lanes + acc * kCols + half * (DV / 2) + c * 32;
+        uint32_t x[32], y[32];
         float v[32];
-        tmem_ld32(tm + lanes + acc * 128 + half * (DV / 2) + c * 32, v);
+        tmem_ld32_issue(col, x);
+        tmem_ld32_issue(col + DV, y);
+        tmem_ld32_wait(x);
+        tmem_ld32_wait(y);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
+        if constexpr (DV == 64) {
+          tmem_ld32_issue(col + 2 * DV, x);
+          tmem_ld32_wait(x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(x[e]);
+        }
         if (r < DK)
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -342,7 +444,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   __syncthreads();
   if (warp == 8) {
     fence_after_sync();
-    tmem_dealloc(tm, 256);
+    tmem_dealloc(tm, 512);
   }
 }
 
@@ -355,7 +457,7 @@ struct RowsSmem {
   static constexpr uint32_t STAGE = 2 * QT + VT, W = 2 * STAGE;      // W: S, then w V, as bf16
   static constexpr uint32_t WB = (DK > C ? DK : C) * DV * 2;
   static constexpr uint32_t HL = W + WB, COLF = HL + 2 * C * 8, VALID = COLF + 192 * 4, WHOLE = VALID + 32;
-  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 15 * 8 + 8;
+  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 16 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -372,7 +474,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4,
            *a_done = full + 6, *p_ready = full + 7, *w_ready = full + 8, *w_free = full + 9, *o_done = full + 10,
-           *o_free = full + 11, *drain = full + 12;
+           *o_free = full + 11, *drain = full + 12, *o_staged = full + 14;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 13);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 8) tmem_alloc(tmem_sh, 512);
@@ -380,7 +482,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
     for (int i = 0; i < 2; ++i) {
       mbar_init(full + i, 1);
       mbar_init(ready + i, 1);
-      mbar_init(empty + i, 2);        // the chunk's MMAs, and its output out of the tile
+      mbar_init(empty + i, 1);
+      mbar_init(o_staged + i, 128);
     }
     mbar_init(a_done, 1);
     mbar_init(p_ready, 128);
@@ -402,30 +505,54 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   uint32_t wn = 0;           // fills of W
 
   if (warp == 9) {
-    // ---------------- loads
+    // ---------------- loads, and stores of whole chunks (from the q tile, and k's where o is wider)
     if (lane == 0) {
       bool ok = true;
+      int done_pos[2], done_h[2];            // the chunk in each stage; pos < 0: its rows were stored directly
+      auto retire = [&](int x) {             // chunk number x: its output leaves the stage
+        const int st = x & 1;
+        ok = ok && wait(o_staged + st, x >> 1, SITE_ROWS);
+        if (!ok || done_pos[st] < 0) return;
+#pragma unroll
+        for (int kb = 0; kb < DV / 64; ++kb)
+          tma_store_3d(&maps.o, smem_u32(sm + st * L::STAGE) + kb * C * 128, kb * 64, done_h[st], done_pos[st]);
+        bulk_commit();
+        bulk_wait_read();
+      };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
         const int h = i % p.H;
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
-          if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS);
+          const uint32_t dst = smem_u32(sm + st * L::STAGE);
+          if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 14);
           if (!ok) break;
           mbar_arrive_expect_tx(full + st, L::STAGE);
-          const uint32_t dst = smem_u32(sm + st * L::STAGE);
-#pragma unroll
-          for (int kb = 0; kb < DK / 64; ++kb) {
-            tma_load_3d(dst + kb * C * 128, &maps.q, kb * 64, h / G, pos, full + st);
-            tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
-          }
 #pragma unroll
           for (int kb = 0; kb < DV / 64; ++kb)
             tma_load_3d(dst + 2 * L::QT + kb * C * 128, &maps.v, kb * 64, h, pos, full + st);
+          if constexpr (DV <= DK)
+#pragma unroll
+            for (int kb = 0; kb < DK / 64; ++kb)
+              tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
+          if (step >= 2) retire(step - 2);
+          // (a failed wait leaves q's bytes missing: the chunk is never used)
+          if (!ok) break;
+          if constexpr (DV > DK)
+#pragma unroll
+            for (int kb = 0; kb < DK / 64; ++kb)
+              tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
+#pragma unroll
+          for (int kb = 0; kb < DK / 64; ++kb)
+            tma_load_3d(dst + kb * C * 128, &maps.q, kb * 64, h / G, pos, full + st);
+          done_pos[st] = pos + C <= sg.end ? pos : -1;
+          done_h[st] = h;
         }
       }
-      if (!ok)
-        for (int i = 0; i < step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+      for (int x = step > 2 ? step - 2 : 0; x < step; ++x) retire(x);
+      bulk_wait_all();
+      if (!ok)      // loads in flight land before the block ends
+        for (int i = 0; i <= step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
     }
   } else if (warp == 8) {
     // ---------------- MMAs
@@ -477,17 +604,38 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       mbar_wait(drain, 0, p.wait_cycles);
     }
   } else if (warp == 10) {
-    // ---------------- decays and rows to clear
+    // ---------------- decays and rows to clear; the next chunk's decays are loaded a chunk ahead
     bool ok = true;
+    int ni = blockIdx.x, npos = 0;           // the chunk whose decays are on their way
+    Segment ns{};
+    auto next = [&]() {
+      RawDecays d{};
+      if (ni >= nitems) return d;
+      d = load_decays(p, npos, ns.end, ni % p.H);
+      npos += C;
+      if (npos >= ns.end && (ni += gridDim.x) < nitems) {
+        ns = lin::locate(p.cu, sbase, p.num_seqs, ni / p.H, per * C);
+        npos = ns.begin;
+      }
+      return d;
+    };
+    if (ni < nitems) {
+      ns = lin::locate(p.cu, sbase, p.num_seqs, ni / p.H, per * C);
+      npos = ns.begin;
+    }
+    RawDecays raw = next();
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
       const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
-      const int h = i % p.H;
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
         double b[4], total;
         uint32_t word;
-        const bool clean = scan_chunk(p, pos, sg.end, h, b, total, word);
-        if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 6);
+        const RawDecays now = raw;
+        raw = next();
+        const bool clean = scan_decays(now, b, total, word);
+        // the stage's MMAs are done, and its output (which reads the tables) is staged
+        if (step >= 2)
+          ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 6) && wait(o_staged + st, (step >> 1) - 1, SITE_ROWS + 15);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         if ((lane & 7) == 0) valid[4 * st + (lane >> 3)] = word;
@@ -496,7 +644,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           const float hi = (float)b[e];
           hl[st * C + 4 * lane + e] = make_float2(hi, (float)(b[e] - (double)hi));
         }
-        if (lane == 0) whole[st] = exp2f((float)total);
+        if (lane == 0) whole[st] = ex2((float)total);
         __syncwarp();
         ok = wait(full + st, step >> 1, SITE_ROWS + 7);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -524,43 +672,54 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         if (!ok) break;
         const float2 *d = hl + st * C;
         const float2 bt = d[t], ref = d[warp > 0 ? 32 * warp - 1 : 0];
-        const float rowf = exp2f((bt.x - ref.x) + (bt.y - ref.y)), from = exp2f(bt.x + bt.y);
+        const float rowf = ex2((bt.x - ref.x) + (bt.y - ref.y)), from = ex2(bt.x + bt.y);
         for (int x = 0; x < warp; ++x) {
           const float2 bs = d[32 * x + lane];
-          colf[32 * x + lane] = exp2f((ref.x - bs.x) + (ref.y - bs.y));
+          colf[32 * x + lane] = ex2((ref.x - bs.x) + (ref.y - bs.y));
         }
         __syncwarp();
         const bool real = (valid[4 * st + warp] >> lane) & 1;
         ok = wait(a_done, step, SITE_ROWS + 9);
         if (!ok) break;
         fence_after_sync();
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          float a[32], w[16];
-          if (x <= warp) tmem_ld32(tm + lanes + T_A + 32 * x, a);
-          if (x < warp) {
+        const uint32_t acol = tm + lanes + T_A;
+        {
+          // the diagonal's 32 columns: each pair by itself
+          uint32_t a[32];
+          float w[16];
+          tmem_ld32_issue(acol + 32 * warp, a);
+          float f[32];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4 *>(colf + 32 * x + e);
-              a[e] *= rowf * f.x;
-              a[e + 1] *= rowf * f.y;
-              a[e + 2] *= rowf * f.z;
-              a[e + 3] *= rowf * f.w;
-            }
-          } else if (x == warp) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 bs = d[32 * x + e];
-              const float f = exp2f((bt.x - bs.x) + (bt.y - bs.y));
-              a[e] = e <= lane ? a[e] * f : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] = 0.f;
+          for (int e = 0; e < 32; ++e) {
+            const float2 bs = d[32 * warp + e];
+            f[e] = ex2(fminf((bt.x - bs.x) + (bt.y - bs.y), 0.f));
           }
+          tmem_ld32_wait(a);
+          // P's columns 16 x .. lie under A's 16 x .., which A's first pieces must have left
+          uint32_t o[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(pack_bf16x2(a[2 * e], a[2 * e + 1]));
-          tmem_st16(tm + lanes + T_A + 16 * x, w);
+          for (int e = 0; e < 32; ++e) f[e] = e <= lane ? __uint_as_float(a[e]) * f[e] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(pack_bf16x2(f[2 * e], f[2 * e + 1]));
+#pragma unroll
+          for (int x = 0; x < 3; ++x) {
+            if (x < warp) {
+              tmem_ld32_issue(acol + 32 * x, o);
+              float g[16];
+              tmem_ld32_wait(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(colf + 32 * x + e);
+                g[e / 2] = __uint_as_float(pack_bf16x2(__uint_as_float(o[e]) * (rowf * c.x), __uint_as_float(o[e + 1]) * (rowf * c.y)));
+                g[e / 2 + 1] = __uint_as_float(pack_bf16x2(__uint_as_float(o[e + 2]) * (rowf * c.z), __uint_as_float(o[e + 3]) * (rowf * c.w)));
+              }
+              tmem_st16(acol + 16 * x, g);
+            }
+          }
+          tmem_st16(acol + 16 * warp, w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0.f;
+          for (int x = warp + 1; x < 4; ++x) tmem_st16(acol + 16 * x, w);
         }
         tmem_st_wait();
         fence_before_sync();
@@ -571,17 +730,25 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         unsigned char *tile = sm + st * L::STAGE;           // q's (and k's) tile: no longer read
         const bool whole_chunk = pos + C <= sg.end;
         uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + t) * p.H + h) * DV;
-#pragma unroll 1
-        for (int x = 0; x < DV / 32; ++x) {
-          float a[32], b[32];
-          tmem_ld32(tm + lanes + T_O1 + 32 * x, a);
-          tmem_ld32(tm + lanes + T_O2 + 32 * x, b);
+        uint32_t a[2][32], b[2][32];
+        tmem_ld32_issue(tm + lanes + T_O1, a[0]);
+        tmem_ld32_issue(tm + lanes + T_O2, b[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] = real ? fmaf(from, a[e], b[e]) : 0.f;
+        for (int x = 0; x < DV / 32; ++x) {
+          tmem_ld32_wait(a[x & 1]);
+          tmem_ld32_wait(b[x & 1]);
+          if (x + 1 < DV / 32) {
+            tmem_ld32_issue(tm + lanes + T_O1 + 32 * (x + 1), a[(x + 1) & 1]);
+            tmem_ld32_issue(tm + lanes + T_O2 + 32 * (x + 1), b[(x + 1) & 1]);
+          }
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            f[e] = real ? fmaf(from, __uint_as_float(a[x & 1][e]), __uint_as_float(b[x & 1][e])) : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint4 u = make_uint4(pack_bf16x2(a[8 * e], a[8 * e + 1]), pack_bf16x2(a[8 * e + 2], a[8 * e + 3]),
-                                       pack_bf16x2(a[8 * e + 4], a[8 * e + 5]), pack_bf16x2(a[8 * e + 6], a[8 * e + 7]));
+            const uint4 u = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                       pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
             const int cc = 4 * x + e;
             if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(t, cc >> 3, cc & 7, C)) = u;
             else if (pos + t < sg.end) *reinterpret_cast<uint4 *>(orow + 8 * cc) = u;
@@ -590,19 +757,9 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         fence_before_sync();
         mbar_arrive(o_free);
         if (whole_chunk) fence_async_smem();
-        group_sync(1);
-        if (tid == 0) {
-          if (whole_chunk) {
-#pragma unroll
-            for (int kb = 0; kb < DV / 64; ++kb) tma_store_3d(&maps.o, smem_u32(tile) + kb * C * 128, kb * 64, h, pos);
-            bulk_commit();
-            bulk_wait_read();
-          }
-          mbar_arrive(empty + st);
-        }
+        mbar_arrive(o_staged + st);
       }
     }
-    if (tid == 0) bulk_wait_all();
   } else {
     // ---------------- S as an operand, S <- 2^{b_C} S, w V (thread: row of the state, then of the chunk)
     const int r = tid & 127;
@@ -619,30 +776,39 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         fence_after_sync();
         const float keep = whole[st];
         const float *in = start + ((size_t)i * DK + r) * DV;
-        if (r < DK || DK == 128) {
-#pragma unroll 1
-          for (int x = 0; x < DV / 32; ++x) {
-            float v[32];
+        if (r < DK) {
+#pragma unroll
+          for (int x = 0; x < DV / 32; x += 2) {       // 64 columns at a time
+            uint32_t v[2][32];
             if (first) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 f = __ldcs(reinterpret_cast<const float4 *>(in + 32 * x + e));
-                v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
-              }
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<uint4 *>(&v[y][e]) = __ldcs(reinterpret_cast<const uint4 *>(in + 32 * (x + y) + e));
             } else {
-              tmem_ld32(tm + lanes + T_S + 32 * x, v);
+              tmem_ld32_issue(tm + lanes + T_S + 32 * x, v[0]);
+              tmem_ld32_issue(tm + lanes + T_S + 32 * (x + 1), v[1]);
+              tmem_ld32_wait(v[0]);
+              tmem_ld32_wait(v[1]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int cc = 4 * x + e;
-              *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, cc >> 3, cc & 7, DK)) =
-                  make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                             pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-            }
-            if (!last) {
+            for (int y = 0; y < 2; ++y) {
+              float f[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= keep;
-              tmem_st32(tm + lanes + T_S + 32 * x, v);
+              for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[y][e]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int cc = 4 * (x + y) + e;
+                *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, cc >> 3, cc & 7, DK)) =
+                    make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                               pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+              }
+              if (!last) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] *= keep;
+                tmem_st32(tm + lanes + T_S + 32 * (x + y), f);
+              }
             }
           }
           tmem_st_wait();
@@ -652,27 +818,33 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         mbar_arrive(w_ready);
         ++wn;
         if (last) continue;
+        // both parts of w V while Q S runs; each goes to W as the product before it is done
         const float2 bs = hl[st * C + r], be = hl[st * C + C - 1];
-        const float w = exp2f((be.x - bs.x) + (be.y - bs.y));
+        const float w = ex2((be.x - bs.x) + (be.y - bs.y));
         const unsigned char *sv = sm + st * L::STAGE + 2 * L::QT;
-#pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
-          ok = wait(w_free, wn - 1, SITE_ROWS + 13);
-          if (!ok) break;
+        uint4 hi[DV / 8], lo[DV / 8];
 #pragma unroll
-          for (int c = 0; c < DV / 8; ++c) {
-            const uint32_t at = row_tile_chunk(r, c >> 3, c & 7, C);
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4 *>(sv + at), f);
+        for (int c = 0; c < DV / 8; ++c) hi[c] = *reinterpret_cast<const uint4 *>(sv + row_tile_chunk(r, c >> 3, c & 7, C));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= w;
-            uint4 u = take_bf16(f);
-            if (x) u = take_bf16(f);
-            *reinterpret_cast<uint4 *>(sm + L::W + at) = u;
+        for (int c = 0; c < DV / 8; ++c) {
+          float f[8];
+          unpack8(hi[c], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= w;
+          hi[c] = take_bf16(f);
+          lo[c] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && wait(w_free, wn - 1, SITE_ROWS + 13);
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < DV / 8; ++c)
+              *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, c >> 3, c & 7, C)) = x ? lo[c] : hi[c];
+            fence_async_smem();
+            mbar_arrive(w_ready);
+            ++wn;
           }
-          fence_async_smem();
-          mbar_arrive(w_ready);
-          ++wn;
         }
       }
     }
