@@ -12,9 +12,10 @@ LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cu", "kda_decode.cu", "kda_prefill_simt.cu", "kda_prefill_tc.cu",
            "kda_noalloc.cu", "kda_prefill_split.cu", "kda_conv.cu",
            "kda_backward.cu", "kda_prefill_bigchunk.cu",
-           "kda_linear.cu", "kda_linear_tc.cu", "kda_linear_decode.cu", "kda_norm.cu"]
+           "kda_linear.cu", "kda_linear_tc.cu", "kda_linear_backward_tc.cu",
+           "kda_linear_decode.cu", "kda_norm.cu"]
 HEADERS = ["kda_internal.cuh", "kda_tc.cuh", "kda_tril_inv.cuh", "kda_chunk_prep.cuh",
-           "kda_linear.cuh"]
+           "kda_linear.cuh", "kda_linear_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

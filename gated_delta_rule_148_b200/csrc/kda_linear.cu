@@ -627,6 +627,7 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
 
 size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
   using namespace lin;
+  if (bf16) return linear_backward_tc_workspace(p);
   const size_t segs = max_segments(p.N, p.num_seqs, C);
   size_t n = table_bytes(p.num_seqs) + align256(segs * p.H * 4) + 2 * state_bytes(p, segs);
   if (p.H != p.Hk) n += 2 * align256((size_t)p.N * p.H * p.dk * 4);
@@ -637,27 +638,34 @@ size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
 cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_t s) {
   using namespace lin;
   if (p.num_seqs == 0) return p.decay_head ? cudaMemsetAsync(p.gla, 0, (size_t)p.H * 4, s) : cudaSuccess;
-  const size_t segs = max_segments(p.N, p.num_seqs, C);
-  unsigned char *w = static_cast<unsigned char *>(p.ws);
-  auto take = [&](size_t n) {
-    unsigned char *at = w;
-    w += align256(n);
-    return reinterpret_cast<float *>(at);
-  };
-  int *sbase = reinterpret_cast<int *>(take(table_bytes(p.num_seqs)));
-  float *whole = take(segs * p.H * 4), *part = take(state_bytes(p, segs)), *rpart = take(state_bytes(p, segs));
   const bool shared = p.H != p.Hk;
-  float *gq32 = shared ? take((size_t)p.N * p.H * p.dk * 4) : nullptr;
-  float *gk32 = shared ? take((size_t)p.N * p.H * p.dk * 4) : nullptr;
-  float *gla = p.decay_head ? take((size_t)p.N * p.H * 4) : p.gla;
-  cudaError_t e = launch_linear_plan(p, sbase, C, s);
-  if (e != cudaSuccess) return e;
-  e = launch_parts_chain(p, bf16, sbase, part, rpart, whole, segs, C, s);
-  if (e != cudaSuccess) return e;
-  if (p.N > 0) {
-    e = bf16 ? launch_grad_dims<true>(p, sbase, part, rpart, gq32, gk32, gla, segs, s)
-             : launch_grad_dims<false>(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
+  float *gq32 = nullptr, *gk32 = nullptr, *gla = p.gla;      // per value head; per head and token
+  cudaError_t e;
+  if (bf16) {
+    e = launch_linear_backward_tc(p, &gq32, &gk32, &gla, s);
     if (e != cudaSuccess) return e;
+  } else {
+    const size_t segs = max_segments(p.N, p.num_seqs, C);
+    unsigned char *w = static_cast<unsigned char *>(p.ws);
+    auto take = [&](size_t n) {
+      unsigned char *at = w;
+      w += align256(n);
+      return reinterpret_cast<float *>(at);
+    };
+    int *sbase = reinterpret_cast<int *>(take(table_bytes(p.num_seqs)));
+    float *whole = take(segs * p.H * 4), *part = take(state_bytes(p, segs)), *rpart = take(state_bytes(p, segs));
+    if (shared) {
+      gq32 = take((size_t)p.N * p.H * p.dk * 4);
+      gk32 = take((size_t)p.N * p.H * p.dk * 4);
+    }
+    if (p.decay_head) gla = take((size_t)p.N * p.H * 4);
+    if ((e = launch_linear_plan(p, sbase, C, s)) != cudaSuccess) return e;
+    e = launch_parts_chain(p, bf16, sbase, part, rpart, whole, segs, C, s);
+    if (e != cudaSuccess) return e;
+    if (p.N > 0) e = launch_grad_dims<false>(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.N > 0) {
     if (shared) {
       const size_t n = ((size_t)p.N * p.Hk * (p.dk / 4) + 255) / 256;
       if (n > 0x7FFFFFFFull) return cudaErrorInvalidValue;

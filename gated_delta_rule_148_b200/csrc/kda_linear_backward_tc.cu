@@ -1,0 +1,894 @@
+// Linear attention with a decay for each head on the tensor cores (bf16 inputs): gradients.
+// Formulas in kda_linear.cuh and kda_linear.cu (grad_kernel); chunks of 128 rows.
+//
+//   sweep   the states at the chunks' starts, S, and their gradients at the chunks' ends, D.
+//           A state's columns never mix, so a block takes 32 columns of d_v of one sequence and
+//           head through all chunks:  S <- 2^{b_C} S + K^T (w V), w_s = 2^{b_C - b_s}, with
+//           S in registers (fp32), w V split into three bf16 parts (24 bits).  The products do not
+//           depend on S, so the chain from chunk to chunk is one multiply-add per element, and four
+//           blocks of a head keep it parallel for few heads.  D: the same from the last chunk to
+//           the first over q, grad_o with w_t = 2^{b_t}; it also takes <S, D> of each chunk.
+//           Both are stored as two bf16 parts (16 bits), the form in which the next step's
+//           products read them.
+//   grad    per chunk and head, everything else (all chunks in parallel).  With rows s and columns t,
+//             A = K Q^T, G = V dO^T, f_st = 2^{b_t - b_s} (t >= s), P = A o f, M = G o f
+//             E = dO S^T, F = V D^T (two parts each), U = K D
+//             dQ = 2^{b_t} E + M^T K,  dK = 2^{b_C - b_s} F + M Q,  dV = 2^{b_C - b_s} U + P dO
+//           M lies in shared memory once and is read K-major (M Q) and MN-major (M^T K); P stays in
+//           TMEM over A.  E, F and U are scaled in TMEM, where the second products add to them; on
+//           the way the row sums q.E and k.F give the decays' gradients, in fp32.
+// The grad kernel is a persistent block per SM: a load/store warp, an MMA thread, a warp that
+// prepares decays and clears rows that are pads or belong to the next sequence, and two warpgroups.
+#include "kda_linear_tc.cuh"
+
+namespace kda {
+namespace lintc {
+
+// Wait sites reported with a timeout.
+enum : unsigned { SITE_SWEEP = 71, SITE_GRAD = 81 };
+
+// State tiles: [chunk x H + h][2 parts][DK][DV] bf16.
+__device__ __forceinline__ size_t tile_at(int chunk, int H, int h, int dk, int dv) {
+  return ((size_t)chunk * H + h) * 2 * dk * dv;
+}
+
+// ============================================================ sweep
+constexpr int kSweepThreads = 4 * 32 + 96;      // a warpgroup; MMA, preparing and load warps
+constexpr int kSweepStages = 3;
+constexpr int kSlice = 32;                      // d_v columns of a block
+
+template <int DK>
+struct SweepSmem {
+  static constexpr uint32_t KT = C * DK * 2, WT = C * 64 * 2;
+  // w V of a step: 64-column tile with parts 0 and 1, and one with part 2 in its first half.
+  // DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and are not used
+  static constexpr uint32_t W = kSweepStages * KT, WGT = W + 2 * 2 * WT, VALID = WGT + 2 * C * 4, WHOLE = VALID + 32;
+  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 16 * 8;
+  static_assert(END <= 232448, "shared memory of a block");
+};
+
+template <int DK, int DV, bool REVERSE>
+__global__ void __launch_bounds__(kSweepThreads, 1)
+sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int *sbase, uint16_t *tiles,
+             const uint16_t *stiles, float *through) {
+  using L = SweepSmem<DK>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if (device_error_latched(p.err)) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int SL = DV / kSlice;
+  const int c0 = (int)(blockIdx.x % SL) * kSlice, h = (int)(blockIdx.x / SL % p.H), b = (int)(blockIdx.x / SL / p.H);
+  const int begin = p.cu[b], end = p.cu[b + 1], n = (end - begin + C - 1) / C, chunk0 = sbase[b];
+  // the last chunk's product matters to the gradient of the initial state only
+  const int n_mma = REVERSE && p.g_init != nullptr ? n : n - 1;
+  auto at = [&](int j) { return REVERSE ? n - 1 - j : j; };      // chunk of step j
+  float *wgt = reinterpret_cast<float *>(sm + L::WGT);
+  uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
+  float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages,
+           *planned = empty + kSweepStages, *w_ready = planned + 2, *done = w_ready + 2, *drain = done + 2;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
+  if (warp == 4) tmem_alloc(tmem_sh, 256);
+  if (tid == 0) {
+    for (int i = 0; i < kSweepStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(planned + i, 1);
+      mbar_init(w_ready + i, 128);
+      mbar_init(done + i, 1);
+    }
+    mbar_init(drain, 1);
+    *failed = 0;
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = *tmem_sh;
+  const Waits wait{p.wait_cycles, p.err, p.site, failed};
+  const int hk = h / (p.H / p.Hk);
+
+  if (warp == 6) {
+    if (lane == 0) {
+      bool ok = true;
+      int j = 0;
+      for (; j < n_mma && ok; ++j) {
+        const int st = j % kSweepStages;
+        if (j >= kSweepStages) ok = wait(empty + st, j / kSweepStages - 1, SITE_SWEEP);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full + st, L::KT);
+#pragma unroll
+        for (int kb = 0; kb < DK / 64; ++kb)
+          tma_load_3d(smem_u32(sm + st * L::KT) + kb * C * 128, &kmap, kb * 64, hk, begin + at(j) * C, full + st);
+      }
+      if (!ok)      // loads in flight land before the block ends
+        for (int i = 0; i < j; ++i) mbar_wait(full + i % kSweepStages, (i / kSweepStages) & 1, 2000000);
+    }
+  } else if (warp == 4) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int j = 0; j < n_mma && ok; ++j) {
+        const int st = j % kSweepStages, sl = j & 1;
+        ok = wait(full + st, j / kSweepStages, SITE_SWEEP + 1) && wait(w_ready + sl, j >> 1, SITE_SWEEP + 2);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t sk = smem_u32(sm + st * L::KT), sw = smem_u32(sm + L::W + sl * 2 * L::WT);
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s)
+          mma_bf16(tm + sl * 128, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 3 * kSlice, 1, 1),
+                   s > 0);
+        mma_commit(empty + st);
+        mma_commit(done + sl);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, p.wait_cycles);
+    }
+  } else if (warp == 5) {
+    bool ok = true;
+    RawDecays raw{};
+    if (n_mma > 0) raw = load_decays(p, begin + at(0) * C, end, h);
+    for (int j = 0; j < n_mma && ok; ++j) {
+      const int sl = j & 1;
+      const RawDecays now = raw;
+      if (j + 1 < n_mma) raw = load_decays(p, begin + at(j + 1) * C, end, h);
+      double d[4], total;
+      uint32_t word;
+      scan_decays(now, d, total, word);
+      if (j >= 2) ok = wait.warp(w_ready + sl, (j >> 1) - 1, SITE_SWEEP + 3);      // the step before has read the slot
+      if (!ok) break;
+      float4 w;
+      w.x = ex2((float)(REVERSE ? d[0] : total - d[0]));
+      w.y = ex2((float)(REVERSE ? d[1] : total - d[1]));
+      w.z = ex2((float)(REVERSE ? d[2] : total - d[2]));
+      w.w = ex2((float)(REVERSE ? d[3] : total - d[3]));
+      reinterpret_cast<float4 *>(wgt + sl * C)[lane] = w;
+      if ((lane & 7) == 0) valid[4 * sl + (lane >> 3)] = word;
+      if (lane == 0) whole[sl] = ex2((float)total);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(planned + sl);
+    }
+  } else {
+    // thread: row of the chunk (w V), then row of the state
+    const int r = tid;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint16_t *vals = reinterpret_cast<const uint16_t *>(REVERSE ? p.d_o : p.v);
+    const float *in = REVERSE ? p.d_final : p.init_state;
+    const size_t own = (((size_t)b * p.H + h) * DK + r) * DV + c0;
+    float S[kSlice], keep = 0.f, keep_next = 0.f;
+#pragma unroll
+    for (int e = 0; e < kSlice; ++e) S[e] = 0.f;
+    if (in != nullptr && r < DK)
+#pragma unroll
+      for (int e = 0; e < kSlice; e += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(in + own + e);
+        S[e] = f.x; S[e + 1] = f.y; S[e + 2] = f.z; S[e + 3] = f.w;
+      }
+    uint4 u[4];
+    auto fetch = [&](int j) {
+      const int pos = begin + at(j) * C + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        u[c] = pos < end ? __ldcs(reinterpret_cast<const uint4 *>(vals + ((size_t)pos * p.H + h) * DV + c0) + c)
+                         : make_uint4(0, 0, 0, 0);
+    };
+    if (n_mma > 0) fetch(0);
+    bool ok = true;
+    for (int j = 0; j <= n && ok; ++j) {
+      keep = keep_next;
+      if (j < n_mma) {
+        const int sl = j & 1, st = j % kSweepStages;
+        ok = wait.warp(planned + sl, j >> 1, SITE_SWEEP + 4);
+        if (!ok) break;
+        const bool real = (valid[4 * sl + warp] >> lane) & 1;
+        const float w = wgt[sl * C + r];
+        keep_next = whole[sl];
+        if (!__all_sync(0xFFFFFFFFu, real)) {
+          ok = wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 5);
+          if (!ok) break;
+          if (!real) {
+#pragma unroll
+            for (int c = 0; c < DK / 8; ++c)
+              *reinterpret_cast<uint4 *>(sm + st * L::KT + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) u[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        unsigned char *sw = sm + L::W + sl * 2 * L::WT;      // its MMA (two steps ago) is done
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float f[8];
+          unpack8(u[c], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= w;
+          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 0, c, C)) = take_bf16(f);
+          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 0, 4 + c, C)) = take_bf16(f);
+          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 1, c, C)) = take_bf16(f);
+        }
+        fence_async_smem();
+        fence_before_sync();
+        mbar_arrive(w_ready + sl);
+        if (j + 1 < n_mma) fetch(j + 1);
+      }
+      if (j == 0) continue;
+      // step j - 1: the state before it goes out, then takes the chunk in
+      const int x = j - 1, sl = x & 1;
+      const size_t tile = tile_at(chunk0 + at(x), p.H, h, DK, DV) + (size_t)r * DV + c0;
+      float dot = 0.f;
+      if (r < DK) {
+        if constexpr (REVERSE) {
+          const uint4 *s0 = reinterpret_cast<const uint4 *>(stiles + tile), *s1 = reinterpret_cast<const uint4 *>(stiles + tile + (size_t)DK * DV);
+          uint4 hi[4], lo[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            hi[c] = __ldg(s0 + c);
+            lo[c] = __ldg(s1 + c);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float f[8], g[8];
+            unpack8(hi[c], f);
+            unpack8(lo[c], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(f[e] + g[e], S[8 * c + e], dot);
+          }
+        }
+        uint4 *d0 = reinterpret_cast<uint4 *>(tiles + tile), *d1 = reinterpret_cast<uint4 *>(tiles + tile + (size_t)DK * DV);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = S[8 * c + e];
+          d0[c] = take_bf16(f);
+          d1[c] = take_bf16(f);
+        }
+      }
+      if constexpr (REVERSE) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        if (lane == 0) through[(((size_t)(chunk0 + at(x)) * p.H + h) * SL + c0 / kSlice) * 4 + warp] = dot;
+      }
+      if (x >= n_mma) continue;
+      ok = wait.warp(done + sl, x >> 1, SITE_SWEEP + 6);
+      if (!ok) break;
+      fence_after_sync();
+      const float a = keep;
+      uint32_t y[32], z[32];
+      tmem_ld32_issue(tm + lanes + sl * 128, y);
+      tmem_ld32_issue(tm + lanes + sl * 128 + 32, z);
+      tmem_ld32_wait(y);
+      tmem_ld32_wait(z);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S[e] = fmaf(a, S[e], __uint_as_float(y[e]) + __uint_as_float(z[e]));
+      tmem_ld32_issue(tm + lanes + sl * 128 + 64, y);
+      tmem_ld32_wait(y);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S[e] += __uint_as_float(y[e]);
+    }
+    if (REVERSE && p.g_init != nullptr && ok && r < DK)
+#pragma unroll
+      for (int e = 0; e < kSlice; e += 4)
+        *reinterpret_cast<float4 *>(p.g_init + own + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 4) {
+    fence_after_sync();
+    tmem_dealloc(tm, 256);
+  }
+}
+
+// ============================================================ grad
+constexpr int kGradThreads = 8 * 32 + 96;
+
+struct GradMaps {
+  CUtensorMap q, k, v, d_o, s, d, gq, gk, gv;
+};
+
+template <int DK, int DV>
+struct GradSmem {
+  static constexpr uint32_t QT = C * DK * 2, VT = C * DV * 2, XT = DK * DV * 2;
+  // X: the two parts of S, then of D, then the gradients of q and k on their way out; M's tile: also grad_v
+  static constexpr uint32_t X1 = XT > QT ? XT : QT;
+  static constexpr uint32_t Q = 0, K = QT, V = 2 * QT, O = V + VT, X = O + VT, M = X + 2 * X1, HL = M + C * C * 2;
+  // column factors of the blocks (w, x) of 32 x 32 pairs, then the blocks' pair sums; the rest of the decays' sums
+  static constexpr uint32_t PAIRS = HL + C * 8, EXTRA = PAIRS + 10 * 32 * 4, SUMS = EXTRA + 2 * 32 * 4;
+  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 24 * 8;
+  static_assert(END <= 232448, "shared memory of a block");
+};
+
+// Sums of 32 columns over the warp's lanes: lane e gets column e's.
+__device__ __forceinline__ float column_sums(float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? x[i] : x[i + o], stay = up ? x[i + o] : x[i];
+      x[i] = stay + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
+  }
+  return x[0];
+}
+// Sums over the lanes before (below) this one.
+__device__ __forceinline__ float exclusive_sum(float x) {
+  const int lane = threadIdx.x & 31;
+  float s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += y;
+  }
+  s = __shfl_up_sync(0xFFFFFFFFu, s, 1);
+  return lane ? s : 0.f;
+}
+// Sums over this lane and those after it.
+__device__ __forceinline__ float suffix_sum(float s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_down_sync(0xFFFFFFFFu, s, o);
+    if (lane + o < 32) s += y;
+  }
+  return s;
+}
+__device__ __forceinline__ uint4 pack8(const float *f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kGradThreads, 1)
+grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sbase, const float *through, float *gq32,
+            float *gk32, float *gla) {
+  using L = GradSmem<DK, DV>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if (device_error_latched(p.err)) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nitems = sbase[p.num_seqs] * p.H;
+  float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
+  float *ksum = reinterpret_cast<float *>(sm + L::HL);      // after the pairs' decays are done with
+  float *pairs = reinterpret_cast<float *>(sm + L::PAIRS), *extra = reinterpret_cast<float *>(sm + L::EXTRA);
+  float *sums = reinterpret_cast<float *>(sm + L::SUMS);    // warps' totals: q.E, k.F
+  uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 1, *s_full = full + 2, *d_full = full + 3,
+           *ag_done = full + 4, *e_done = full + 5, *f_done = full + 6, *u_done = full + 7, *conv = full + 8,
+           *e_scaled = full + 9, *f_scaled = full + 10, *u_scaled = full + 11, *dq_done = full + 12, *dk_done = full + 13,
+           *dv_done = full + 14, *staged = full + 15, *out_free = full + 16, *acc_free = full + 17, *tab_free = full + 18,
+           *drain = full + 19;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 20);
+  volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
+  if (warp == 8) tmem_alloc(tmem_sh, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 20; ++i) {
+      const bool both = i == 8 || i == 11 || i == 15 || i == 17, one = i == 9 || i == 10 || i == 18;
+      mbar_init(full + i, both ? 256 : one ? 128 : 1);
+    }
+    *failed = 0;
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = *tmem_sh;
+  // A (then P: row blocks 0, 1 in columns 0 .. 31, row blocks 2, 3 in columns 64 .. 95), G then dV, dQ, dK
+  constexpr uint32_t T_A = 0, T_V = 128, T_Q = 256, T_K = 384;
+  const Waits wait{p.wait_cycles, p.err, p.site, failed};
+  const int G = p.H / p.Hk;
+  const bool shared = gq32 != nullptr;
+  int it = 0;
+
+  if (warp == 9) {
+    // ---------------- loads and stores
+    if (lane == 0) {
+      bool ok = true;
+      int pos_out = -1, h_out = 0;           // the item before: its gradients, if the chunk is whole
+      auto store = [&]() {
+        ok = ok && wait(staged, it - 1, SITE_GRAD);
+        if (!ok) return;
+        if (pos_out >= 0) {
+          if (!shared) {
+#pragma unroll
+            for (int kb = 0; kb < DK / 64; ++kb) {
+              tma_store_3d(&maps.gq, smem_u32(sm + L::X) + kb * C * 128, kb * 64, h_out, pos_out);
+              tma_store_3d(&maps.gk, smem_u32(sm + L::X + L::X1) + kb * C * 128, kb * 64, h_out, pos_out);
+            }
+          }
+#pragma unroll
+          for (int kb = 0; kb < DV / 64; ++kb)
+            tma_store_3d(&maps.gv, smem_u32(sm + L::M) + kb * C * 128, kb * 64, h_out, pos_out);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        mbar_arrive(out_free);
+      };
+      auto load_state = [&](const CUtensorMap *map, int i, uint64_t *bar) {
+        mbar_arrive_expect_tx(bar, 2 * L::XT);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int kb = 0; kb < DV / 64; ++kb)
+            tma_load_3d(smem_u32(sm + L::X + x * L::X1) + kb * DK * 128, map, kb * 64, 0, (2 * i + x) * DK, bar);
+      };
+      int loads = 0;      // begun on full, s_full, d_full
+      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
+        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+        const int h = i % p.H, pos = sg.begin;
+        if (it > 0) ok = wait(dv_done, it - 1, SITE_GRAD + 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full, 2 * L::QT + 2 * L::VT);
+#pragma unroll
+        for (int kb = 0; kb < DK / 64; ++kb) {
+          tma_load_3d(smem_u32(sm + L::K) + kb * C * 128, &maps.k, kb * 64, h / G, pos, full);
+          tma_load_3d(smem_u32(sm + L::Q) + kb * C * 128, &maps.q, kb * 64, h / G, pos, full);
+        }
+#pragma unroll
+        for (int kb = 0; kb < DV / 64; ++kb) {
+          tma_load_3d(smem_u32(sm + L::V) + kb * C * 128, &maps.v, kb * 64, h, pos, full);
+          tma_load_3d(smem_u32(sm + L::O) + kb * C * 128, &maps.d_o, kb * 64, h, pos, full);
+        }
+        loads = 3 * it + 1;
+        if (it > 0) store();
+        if (!ok) break;
+        load_state(&maps.s, i, s_full);
+        ++loads;
+        ok = wait(e_done, it, SITE_GRAD + 2);
+        if (!ok) break;
+        load_state(&maps.d, i, d_full);
+        ++loads;
+        pos_out = pos + C <= sg.end ? pos : -1;
+        h_out = h;
+      }
+      if (it > 0) store();
+      bulk_wait_all();
+      if (!ok && loads > 0) {      // loads in flight land before the block ends
+        const int last = (loads - 1) / 3, k = (loads - 1) % 3;
+        mbar_wait(full, last & 1, 2000000);
+        if (k >= 1) mbar_wait(s_full, last & 1, 2000000);
+        if (k >= 2) mbar_wait(d_full, last & 1, 2000000);
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------- MMAs
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t sq = smem_u32(sm + L::Q), sk = smem_u32(sm + L::K), sv = smem_u32(sm + L::V), so = smem_u32(sm + L::O),
+                     sx = smem_u32(sm + L::X), smm = smem_u32(sm + L::M);
+      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
+        ok = wait(ready, it, SITE_GRAD + 3);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s)
+          mma_bf16(tm + T_A, desc_kmajor(sk, C, 0, s), desc_kmajor(sq, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
+        if (it > 0) ok = wait(acc_free, it - 1, SITE_GRAD + 4);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < DV / 16; ++s)
+          mma_bf16(tm + T_V, desc_kmajor(sv, C, 0, s), desc_kmajor(so, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
+        mma_commit(ag_done);
+        ok = wait(s_full, it, SITE_GRAD + 5);
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int s = 0; s < DV / 16; ++s)
+            mma_bf16(tm + T_Q, desc_kmajor(so, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
+                     x > 0 || s > 0);
+        mma_commit(e_done);
+        ok = wait(d_full, it, SITE_GRAD + 6);
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int s = 0; s < DV / 16; ++s)
+            mma_bf16(tm + T_K, desc_kmajor(sv, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
+                     x > 0 || s > 0);
+        mma_commit(f_done);
+        ok = wait(conv, it, SITE_GRAD + 7);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s)
+          mma_bf16(tm + T_V, desc_kmajor(sk, C, 0, s), desc_mnmajor(sx, DK, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
+        mma_commit(u_done);
+        ok = wait(e_scaled, it, SITE_GRAD + 8);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s)
+          mma_bf16(tm + T_Q, desc_mnmajor(smm, C, 0, s), desc_mnmajor(sk, C, 0, s), idesc_bf16(128, DK, 1, 1), 1);
+        mma_commit(dq_done);
+        ok = wait(f_scaled, it, SITE_GRAD + 9);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s)
+          mma_bf16(tm + T_K, desc_kmajor(smm, C, 0, s), desc_mnmajor(sq, C, 0, s), idesc_bf16(128, DK, 0, 1), 1);
+        mma_commit(dk_done);
+        ok = wait(u_scaled, it, SITE_GRAD + 10);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < C / 16; ++s)
+          mma_bf16_ta(tm + T_V, tm + T_A + 64 * (s >> 2) + 8 * (s & 3), desc_mnmajor(so, C, 0, s), idesc_bf16(128, DV, 0, 1),
+                      1);
+        mma_commit(dv_done);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, p.wait_cycles);
+    }
+  } else if (warp == 10) {
+    // ---------------- decays and rows to clear
+    bool ok = true;
+    RawDecays raw{};
+    auto next = [&](int i) {
+      if (i < nitems) {
+        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+        raw = load_decays(p, sg.begin, sg.end, i % p.H);
+      }
+    };
+    next(blockIdx.x);
+    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
+      double b[4], total;
+      uint32_t word;
+      const RawDecays now = raw;
+      next(i + gridDim.x);
+      const bool clean = scan_decays(now, b, total, word);
+      if (it > 0) ok = wait.warp(tab_free, it - 1, SITE_GRAD + 11);
+      if (!ok) break;
+      if ((lane & 7) == 0) valid[lane >> 3] = word;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float hi = (float)b[e];
+        hl[4 * lane + e] = make_float2(hi, (float)(b[e] - (double)hi));
+      }
+      __syncwarp();
+      ok = wait.warp(full, it, SITE_GRAD + 12);
+      if (!clean && ok) {
+        clear_rows<DK>(sm + L::Q, valid);
+        clear_rows<DK>(sm + L::K, valid);
+        clear_rows<DV>(sm + L::V, valid);
+        clear_rows<DV>(sm + L::O, valid);
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(ready);
+    }
+  } else {
+    // ---------------- thread: row r of the chunk (as s in P, M, F and U; as t in E and dQ)
+    const int r = tid & 127, w = warp & 3, y = warp >> 2;      // y: warpgroup
+    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+    bool ok = true;
+    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
+      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+      const int h = i % p.H, pos = sg.begin;
+      const bool whole_chunk = pos + C <= sg.end, in = pos + r < sg.end;
+      float thr = 0.f;
+      if (y == 0 && lane < DV / 8) thr = through[(size_t)i * (DV / 8) + lane];
+      ok = wait.warp(ready, it, SITE_GRAD + 13);
+      if (!ok) break;
+      const bool real = (valid[w] >> lane) & 1;
+      const float2 br = hl[r], be = hl[C - 1], ref = hl[32 * w + 31];
+      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
+      const float to = ex2((be.x - br.x) + (be.y - br.y)), from = ex2(br.x + br.y), whole = ex2(be.x + be.y);
+      const float rowf = ex2((ref.x - br.x) + (ref.y - br.y));
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {      // 2^{b_t - b_ref} of the blocks after the diagonal's
+        const int x = 2 * y + z;
+        if (x > w) {
+          const float2 bt = hl[32 * x + lane];
+          pairs[(x * (x + 1) / 2 + w) * 32 + lane] = ex2((bt.x - ref.x) + (bt.y - ref.y));
+        }
+      }
+      __syncwarp();
+      ok = wait.warp(ag_done, it, SITE_GRAD + 14);
+      if (it > 0) ok = ok && wait.warp(out_free, it - 1, SITE_GRAD + 15);
+      if (!ok) break;
+      fence_after_sync();
+      float rest = 0.f;                  // the row's pairs behind the diagonal block
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int x = 2 * y + z;         // columns 32 x .. 32 x + 31
+        const uint32_t pcol = tm + lanes + T_A + 64 * y + 16 * z;
+        unsigned char *mt = sm + L::M;
+        if (x < w) {
+          float zero[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+          tmem_st16(pcol, zero);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y, 4 * z + c, C)) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        uint32_t a[32], g[32];
+        tmem_ld32_issue(tm + lanes + T_A + 32 * x, a);
+        tmem_ld32_issue(tm + lanes + T_V + 32 * x, g);
+        float *slot = pairs + (x * (x + 1) / 2 + w) * 32;
+        float f[32];
+        if (x == w) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 bt = hl[32 * x + e];
+            f[e] = ex2((bt.x - br.x) + (bt.y - br.y));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 cf = *reinterpret_cast<const float4 *>(slot + e);
+            f[e] = rowf * cf.x; f[e + 1] = rowf * cf.y; f[e + 2] = rowf * cf.z; f[e + 3] = rowf * cf.w;
+          }
+        }
+        tmem_ld32_wait(a);
+        tmem_ld32_wait(g);
+        float pw[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float m[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = 8 * c + e;
+            const bool on = x > w || k >= lane;      // t >= s
+            const float P = on ? __uint_as_float(a[k]) * f[k] : 0.f;
+            m[e] = on ? __uint_as_float(g[k]) * f[k] : 0.f;
+            f[k] = P * __uint_as_float(g[k]);
+            a[k] = __float_as_uint(P);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            pw[4 * c + e] = __uint_as_float(pack_bf16x2(__uint_as_float(a[8 * c + 2 * e]), __uint_as_float(a[8 * c + 2 * e + 1])));
+          *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y, 4 * z + c, C)) = pack8(m);
+        }
+        tmem_st16(pcol, pw);
+        // pairs (s, t) with t >= u for column u; on the diagonal block only columns u > s
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 31; e >= 0; --e) {
+          acc += f[e];
+          f[e] = (x > w || e > lane) ? acc : 0.f;
+        }
+        if (x > w) rest += f[0];
+        const float col = column_sums(f);
+        __syncwarp();
+        slot[lane] = col;
+      }
+      {
+        const float before = exclusive_sum(rest);
+        __syncwarp();
+        if ((w >> 1) == y) pairs[(w * (w + 1) / 2 + w) * 32 + lane] += before;
+        else if (y == 1) extra[w * 32 + lane] = before;
+      }
+      tmem_st_wait();
+      fence_async_smem();
+      fence_before_sync();
+      mbar_arrive(conv);
+
+      // E or F: scaled in place; its rows' products with q or k
+      ok = wait.warp(y ? f_done : e_done, it, SITE_GRAD + 16);
+      if (!ok) break;
+      fence_after_sync();
+      float dot = 0.f;
+      {
+        const float fac = y ? to : from;
+        const unsigned char *tile = sm + (y ? L::K : L::Q);
+        const uint32_t col = tm + lanes + (y ? T_K : T_Q);
+        uint32_t a[2][32];
+        tmem_ld32_issue(col, a[0]);
+#pragma unroll
+        for (int x = 0; x < DK / 32; ++x) {
+          tmem_ld32_wait(a[x & 1]);
+          if (x + 1 < DK / 32) tmem_ld32_issue(col + 32 * (x + 1), a[(x + 1) & 1]);
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float f[8];
+            unpack8(*reinterpret_cast<const uint4 *>(tile + row_tile_chunk(r, x >> 1, 4 * (x & 1) + c, C)), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[8 * c + e] = __uint_as_float(a[x & 1][8 * c + e]) * fac;
+              dot = fmaf(v[8 * c + e], f[e], dot);
+            }
+          }
+          tmem_st32(col + 32 * x, v);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        mbar_arrive(y ? f_scaled : e_scaled);
+      }
+      ok = wait.warp(conv, it, SITE_GRAD + 17);      // no more readers of the decays: their place takes k.F
+      if (!ok) break;
+      if (y == 0) {
+        dot = suffix_sum(dot);
+        if (lane == 0) sums[w] = dot;
+      } else {
+        const float before = exclusive_sum(dot);
+        ksum[r] = before;
+        if (lane == 31) sums[4 + w] = before + dot;
+      }
+      ok = wait.warp(u_done, it, SITE_GRAD + 18);
+      if (!ok) break;
+      fence_after_sync();
+      {
+        const uint32_t col = tm + lanes + T_V + y * (DV / 2);
+#pragma unroll
+        for (int x = 0; x < DV / 64; ++x) {
+          float v[32];
+          tmem_ld32(col + 32 * x, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= to;
+          tmem_st32(col + 32 * x, v);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        mbar_arrive(u_scaled);
+      }
+      if (y == 0) {
+        // the decay's gradient of row u = r
+        ok = wait.warp(u_scaled, it, SITE_GRAD + 19);
+        if (!ok) break;
+        float g = dot + ksum[r];
+        for (int x = w + 1; x < 4; ++x) g += sums[x];
+        for (int x = 0; x < w; ++x) g += sums[4 + x];
+        for (int x = 0; x <= w; ++x) g += pairs[(w * (w + 1) / 2 + x) * 32 + lane];
+        for (int x = 0; x < w; ++x)
+          for (int z = w + 1; z < 4; ++z) g += pairs[(z * (z + 1) / 2 + x) * 32];
+        if (w < 2) g += extra[w * 32 + lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xFFFFFFFFu, thr, o);
+        g = fmaf(whole, thr, g);
+        // one decay per head: [H, N] for the sum that follows
+        if (in) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
+        mbar_arrive(tab_free);
+      }
+
+      // gradients: dQ by the first warpgroup, dK by the second, dV by both
+      auto out = [&](uint32_t col, int cols, unsigned char *tile, int tile0, uint16_t *row, float *row32) {
+        uint32_t a[2][32];
+        tmem_ld32_issue(col, a[0]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (32 * x >= cols) break;
+          tmem_ld32_wait(a[x & 1]);
+          if (32 * (x + 1) < cols) tmem_ld32_issue(col + 32 * (x + 1), a[(x + 1) & 1]);
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(a[x & 1][e]);
+          if (row32 != nullptr) {
+            if (in)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(row32 + 32 * x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int cc = tile0 + 4 * x + c;
+              if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * c);
+              else if (in) *reinterpret_cast<uint4 *>(row + 8 * cc) = pack8(f + 8 * c);
+            }
+          }
+        }
+      };
+      const size_t token = (size_t)(pos + r) * p.H + h;
+      ok = wait.warp(y ? dk_done : dq_done, it, SITE_GRAD + 20);
+      if (!ok) break;
+      fence_after_sync();
+      if (shared)
+        out(tm + lanes + (y ? T_K : T_Q), DK, nullptr, 0, nullptr, (y ? gk32 : gq32) + token * DK);
+      else
+        out(tm + lanes + (y ? T_K : T_Q), DK, sm + L::X + y * L::X1, 0,
+            reinterpret_cast<uint16_t *>(y ? p.gk : p.gq) + token * DK, nullptr);
+      ok = wait.warp(dv_done, it, SITE_GRAD + 21);
+      if (!ok) break;
+      fence_after_sync();
+      out(tm + lanes + T_V + y * (DV / 2), DV / 2, sm + L::M, y * (DV / 16), reinterpret_cast<uint16_t *>(p.gv) + token * DV,
+          nullptr);
+      fence_before_sync();
+      mbar_arrive(acc_free);
+      if (whole_chunk) fence_async_smem();
+      mbar_arrive(staged);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    fence_after_sync();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+// ============================================================ host
+struct BackwardWorkspace {
+  size_t sbase, through, s, d, gq32, gk32, gla, bytes;
+};
+inline BackwardWorkspace backward_layout(const LinearParams &p) {
+  const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
+  BackwardWorkspace w{};
+  auto take = [&](size_t n) {
+    const size_t at = w.bytes;
+    w.bytes += lin::align256(n);
+    return at;
+  };
+  w.sbase = take(lin::table_bytes(p.num_seqs));
+  w.through = take(chunks * p.H * (p.dv / 8) * 4);
+  w.s = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
+  w.d = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
+  const size_t per_head = p.H != p.Hk ? (size_t)p.N * p.H * p.dk * 4 : 0;
+  w.gq32 = take(per_head);
+  w.gk32 = take(per_head);
+  w.gla = take(p.decay_head ? (size_t)p.N * p.H * 4 : 0);
+  return w;
+}
+
+// State tiles as [rows][1][dv] in boxes of dk rows and 64 columns.
+inline bool encode_tiles(CUtensorMap *map, const void *ptr, int dk, int dv, size_t rows) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dv, 1u, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)dv * 2, (cuuint64_t)dv * 2};
+  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)dk}, one[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV>
+cudaError_t launch_backward(const LinearParams &p, const GradMaps &maps, const BackwardWorkspace &w, size_t chunks,
+                            cudaStream_t s) {
+  unsigned char *ws = static_cast<unsigned char *>(p.ws);
+  const int *sbase = reinterpret_cast<const int *>(ws + w.sbase);
+  float *through = reinterpret_cast<float *>(ws + w.through);
+  uint16_t *st = reinterpret_cast<uint16_t *>(ws + w.s), *dt = reinterpret_cast<uint16_t *>(ws + w.d);
+  const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice), items = chunks * p.H;
+  if (sweeps > 0x7FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  auto fwd = sweep_kernel<DK, DV, false>, rev = sweep_kernel<DK, DV, true>;
+  auto grad = grad_kernel<DK, DV>;
+  constexpr int sweep_smem = SweepSmem<DK>::END, grad_smem = GradSmem<DK, DV>::END;
+  cudaError_t e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, sweep_smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rev, cudaFuncAttributeMaxDynamicSharedMemorySize, sweep_smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem);
+  if (e != cudaSuccess) return e;
+  fwd<<<(unsigned)sweeps, kSweepThreads, sweep_smem, s>>>(p, maps.k, sbase, st, nullptr, nullptr);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  rev<<<(unsigned)sweeps, kSweepThreads, sweep_smem, s>>>(p, maps.q, sbase, dt, st, through);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.N == 0) return e;
+  const bool shared = p.H != p.Hk;
+  float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
+  const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
+  grad<<<grid, kGradThreads, grad_smem, s>>>(p, maps, sbase, through,
+                                             shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr,
+                                             shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr, gla);
+  return cudaGetLastError();
+}
+
+}  // namespace lintc
+
+size_t linear_backward_tc_workspace(const LinearParams &p) { return lintc::backward_layout(p).bytes; }
+
+cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float **gk32, float **gla, cudaStream_t s) {
+  using namespace lintc;
+  const BackwardWorkspace w = backward_layout(p);
+  const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
+  unsigned char *ws = static_cast<unsigned char *>(p.ws);
+  const bool shared = p.H != p.Hk;
+  *gq32 = shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr;
+  *gk32 = shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr;
+  *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
+  cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, s);
+  if (e != cudaSuccess) return e;
+  GradMaps m{};
+  if (p.N > 0) {
+    const size_t rows = chunks * p.H * 2 * p.dk;
+    bool ok = encode(&m.q, p.q, p.dk, p.Hk, p.N) && encode(&m.k, p.k, p.dk, p.Hk, p.N) &&
+              encode(&m.v, p.v, p.dv, p.H, p.N) && encode(&m.d_o, p.d_o, p.dv, p.H, p.N) &&
+              encode(&m.gv, p.gv, p.dv, p.H, p.N) && encode_tiles(&m.s, ws + w.s, p.dk, p.dv, rows) &&
+              encode_tiles(&m.d, ws + w.d, p.dk, p.dv, rows);
+    if (!shared) ok = ok && encode(&m.gq, p.gq, p.dk, p.H, p.N) && encode(&m.gk, p.gk, p.dk, p.H, p.N);
+    if (!ok) return cudaErrorNotSupported;
+  }
+  if (p.dk == 128)
+    return p.dv == 128 ? launch_backward<128, 128>(p, m, w, chunks, s) : launch_backward<128, 64>(p, m, w, chunks, s);
+  return p.dv == 128 ? launch_backward<64, 128>(p, m, w, chunks, s) : launch_backward<64, 64>(p, m, w, chunks, s);
+}
+
+}  // namespace kda

@@ -14,184 +14,19 @@
 // that move accumulators.  Off the diagonal a warp's 32 rows share a reference row R before them,
 // 2^{b_t - b_s} = 2^{b_t - R} 2^{R - b_s}, both factors <= 1: one exponential per row and column
 // instead of one per pair.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
 #include <cmath>
 
-#include "kda_linear.cuh"
-#include "kda_tc.cuh"
+#include "kda_linear_tc.cuh"
 
 namespace kda {
 namespace lintc {
 
-using namespace tc;
-using lin::Segment;
-
-constexpr int C = 128;
-
 // Wait sites reported with a timeout.
 enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
-
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-               :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2) : "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// D (TMEM) += A (TMEM, packed bf16) B (shared memory).
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
 
 struct Maps {
   CUtensorMap q, k, v, o;
 };
-
-// 2^x with results below 2^-126 taken as 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 32 fp32 columns of this thread's TMEM lane: issue, and wait for all loads issued before.
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// The registers pass through the wait, so that no use of them moves before it.
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
-}
-
-// Bounded waits of one block.  After one has run out every role leaves its loop; the waits of the
-// others then end too.
-struct Waits {
-  long long limit;
-  unsigned *err, *site;
-  volatile int *failed;
-  static __device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, P;\n\t}"
-        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return done != 0;
-  }
-  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t phase, unsigned code) const {
-    const uint32_t parity = phase & 1;
-    if (test(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!test(bar, parity)) {
-      if (*failed) return false;
-      if (clock64() - t0 > limit) {
-        note_timeout(site, code);
-        atomicOr(err, ERR_BIT_TIMEOUT);
-        *failed = 1;
-        return false;
-      }
-    }
-    return true;
-  }
-};
-
-// Zeroes the rows of a [128][D] tile that are not set in valid (one warp).
-template <int D>
-__device__ __forceinline__ void clear_rows(unsigned char *tile, const uint32_t *valid) {
-  const int lane = threadIdx.x & 31;
-  for (int w = 0; w < C / 32; ++w)
-    for (uint32_t pads = ~valid[w]; pads != 0; pads &= pads - 1) {
-      const int r = 32 * w + __ffs((int)pads) - 1;
-      if (lane < D / 8) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, lane >> 3, lane & 7, C)) = make_uint4(0, 0, 0, 0);
-    }
-}
-
-// A chunk's decays, one warp: lane's rows 4 lane .. 4 lane + 3.  Loading is apart from summing, so that the
-// next chunk's values are on their way while this one's are used.
-struct RawDecays {
-  float x[4];
-  uint32_t bits;        // bit e: row 4 lane + e is a real token
-};
-__device__ __forceinline__ RawDecays load_decays(const LinearParams &p, int pos0, int end, int h) {
-  RawDecays d;
-  const int pos = pos0 + 4 * (threadIdx.x & 31);
-  uint8_t m[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const bool in = pos + e < end;
-    m[e] = in ? (p.mask != nullptr ? p.mask[pos + e] : (uint8_t)1) : (uint8_t)0;
-    d.x[e] = in ? p.log_alpha[p.decay_head ? (size_t)h : (size_t)(pos + e) * p.H + h] : 0.f;
-  }
-  d.bits = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) d.bits |= (uint32_t)(m[e] != 0) << e;
-  return d;
-}
-// Inclusive sums b of log2 a, the total; word: lanes 0, 8, 16, 24 get the bits of rows 32 (lane / 8) .. + 31.
-// Returns whether all 128 rows are real tokens.
-__device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], double &total, uint32_t &word) {
-  const int lane = threadIdx.x & 31;
-  double s = 0.0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if ((d.bits >> e) & 1) s += fmax((double)d.x[e] * 1.4426950408889634074, -400.0);
-    b[e] = s;
-  }
-  double x = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = lin::shfl_up_f64(x, o);
-    if (lane >= o) x += y;
-  }
-  total = lin::shfl_f64(x, 31);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] += x - s;
-  word = d.bits << (4 * (lane & 7));
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  return __all_sync(0xFFFFFFFFu, d.bits == 0xFu);
-}
-
-// 8 bf16 of a 16-byte word as floats.
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
-  const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(a[e] << 16);
-    f[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
-  }
-}
-// Rounds 8 floats to bf16 (returned packed) and leaves the remainders in f.
-__device__ __forceinline__ uint4 take_bf16(float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-    f[2 * e] -= __uint_as_float(w[e] << 16);
-    f[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // ============================================================ parts
 // A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
@@ -377,12 +212,12 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
     int n = 0;
     for (int step = 0;; ++step) {
       const int st = step & 1, rs = step % kRing, acc = n & 1;
-      if (!wait(planned + rs, step / kRing, SITE_PARTS + 5)) break;
+      if (!wait.warp(planned + rs, step / kRing, SITE_PARTS + 5)) break;
       const int item = steps[rs].item;
       if (item < 0) break;
       const bool last = steps[rs].last != 0, real = (valid[4 * rs + (r >> 5)] >> (r & 31)) & 1;
       const float w = wgt[rs * C + r];
-      if (!wait(full + st, step >> 1, SITE_PARTS + 6)) break;
+      if (!wait.warp(full + st, step >> 1, SITE_PARTS + 6)) break;
       unsigned char *sk = sm + st * L::STAGE, *sv = sk + L::KT;
       uint4 u[NC];
 #pragma unroll
@@ -395,7 +230,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
           const int cc = half * (DK / 16) + c;
           *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
         }
-      if (step > 0 && !wait(w_free, step - 1, SITE_PARTS + 7)) break;
+      if (step > 0 && !wait.warp(w_free, step - 1, SITE_PARTS + 7)) break;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int cc = half * NC + c;
@@ -410,7 +245,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       fence_async_smem();
       mbar_arrive(w_ready);
       if (!last) continue;
-      if (!wait(s_done + acc, n >> 1, SITE_PARTS + 8)) break;
+      if (!wait.warp(s_done + acc, n >> 1, SITE_PARTS + 8)) break;
       fence_after_sync();
       float *out = part + ((size_t)item * DK + r) * DV + half * (DV / 2);
 #pragma unroll
@@ -508,7 +343,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
     // ---------------- loads, and stores of whole chunks (from the q tile, and k's where o is wider)
     if (lane == 0) {
       bool ok = true;
-      int done_pos[2], done_h[2];            // the chunk in each stage; pos < 0: its rows were stored directly
+      int done_pos[2] = {-1, -1}, done_h[2] = {0, 0};            // the chunk in each stage; pos < 0: its rows were stored directly
       auto retire = [&](int x) {             // chunk number x: its output leaves the stage
         const int st = x & 1;
         ok = ok && wait(o_staged + st, x >> 1, SITE_ROWS);
@@ -668,7 +503,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       const int h = i % p.H;
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
-        ok = wait(ready + st, step >> 1, SITE_ROWS + 8);
+        ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 8);
         if (!ok) break;
         const float2 *d = hl + st * C;
         const float2 bt = d[t], ref = d[warp > 0 ? 32 * warp - 1 : 0];
@@ -679,7 +514,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         }
         __syncwarp();
         const bool real = (valid[4 * st + warp] >> lane) & 1;
-        ok = wait(a_done, step, SITE_ROWS + 9);
+        ok = wait.warp(a_done, step, SITE_ROWS + 9);
         if (!ok) break;
         fence_after_sync();
         const uint32_t acol = tm + lanes + T_A;
@@ -724,7 +559,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         tmem_st_wait();
         fence_before_sync();
         mbar_arrive(p_ready);
-        ok = wait(o_done, step, SITE_ROWS + 10);
+        ok = wait.warp(o_done, step, SITE_ROWS + 10);
         if (!ok) break;
         fence_after_sync();
         unsigned char *tile = sm + st * L::STAGE;           // q's (and k's) tile: no longer read
@@ -770,8 +605,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
         const bool first = pos == sg.begin, last = pos + C >= sg.end;
-        ok = wait(ready + st, step >> 1, SITE_ROWS + 11);
-        if (wn > 0) ok = ok && wait(w_free, wn - 1, SITE_ROWS + 12);      // also: S has its last sum
+        ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 11);
+        if (wn > 0) ok = ok && wait.warp(w_free, wn - 1, SITE_ROWS + 12);      // also: S has its last sum
         if (!ok) break;
         fence_after_sync();
         const float keep = whole[st];
@@ -836,7 +671,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          ok = ok && wait(w_free, wn - 1, SITE_ROWS + 13);
+          ok = ok && wait.warp(w_free, wn - 1, SITE_ROWS + 13);
           if (ok) {
 #pragma unroll
             for (int c = 0; c < DV / 8; ++c)
@@ -858,42 +693,6 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
 }
 
 // ============================================================ host
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    return nullptr;
-  }();
-  return fn;
-}
-
-// [N, heads, d] bf16 in boxes of 128 rows of one head and 64 columns, 128-byte swizzle.
-bool encode(CUtensorMap *map, const void *ptr, int d, int heads, int N) {
-  auto fn = encoder();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)N};
-  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * heads};
-  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)C}, one[3] = {1u, 1u, 1u};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-  static std::atomic<int> n[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  int v = n[dev].load(std::memory_order_relaxed);
-  if (v == 0) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
-    n[dev].store(v, std::memory_order_relaxed);
-  }
-  return v;
-}
-
 // Chunks in a segment: the count with the shortest expected run, in chunk times: rounds of items over the
 // SMs, each item `per` chunks and about two more (fill of the pipeline, its state in and out).
 int segment_chunks(int N, int B, int H) {
