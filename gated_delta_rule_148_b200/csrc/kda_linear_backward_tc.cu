@@ -28,30 +28,37 @@ namespace lintc {
 enum : unsigned { SITE_SWEEP = 71, SITE_GRAD = 81 };
 
 // State tiles: [chunk x H + h][2 parts][DK][DV] bf16.
-__device__ __forceinline__ size_t tile_at(int chunk, int H, int h, int dk, int dv) {
-  return ((size_t)chunk * H + h) * 2 * dk * dv;
-}
 
 // ============================================================ sweep
-constexpr int kSweepThreads = 4 * 32 + 96;      // a warpgroup; MMA, preparing and load warps
+// Roles: a load warp (K tile and 32 columns of V, three stages ahead), a warp that prepares the weights, one
+// warpgroup that writes w V, an MMA thread, one warpgroup that holds the state.  A step's tiles of the state
+// leave (and S's arrive) through shared memory, since its rows are 64 bytes apart from each other's neighbours.
+constexpr int kSweepThreads = 8 * 32 + 96;
 constexpr int kSweepStages = 3;
 constexpr int kSlice = 32;                      // d_v columns of a block
 
-template <int DK>
+template <int DK, bool REVERSE>
 struct SweepSmem {
-  static constexpr uint32_t KT = C * DK * 2, WT = C * 64 * 2;
-  // w V of a step: 64-column tile with parts 0 and 1, and one with part 2 in its first half.
-  // DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and are not used
-  static constexpr uint32_t W = kSweepStages * KT, WGT = W + 2 * 2 * WT, VALID = WGT + 2 * C * 4, WHOLE = VALID + 32;
-  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 16 * 8;
+  static constexpr uint32_t KT = C * DK * 2, VT = C * kSlice * 2, STAGE = KT + VT, XT = DK * kSlice * 2;
+  // W: three parts of w V, two steps.  DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and
+  // are not used
+  static constexpr uint32_t W = kSweepStages * STAGE, OUT = W + 2 * 3 * VT, IN = OUT + 2 * XT;
+  static constexpr uint32_t WGT = IN + (REVERSE ? 2 * 2 * XT : 0), VALID = WGT + 2 * C * 4, WHOLE = VALID + 32;
+  static constexpr uint32_t BARS = WHOLE + 16, END = BARS + 24 * 8;
   static_assert(END <= 232448, "shared memory of a block");
+};
+
+// Byte offset of 16-byte word c of row r in a tile of 32 columns with the 64-byte swizzle.
+__device__ __forceinline__ uint32_t slice_at(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+struct SweepMaps {
+  CUtensorMap k, v, s, out;      // REVERSE: q, grad_o, the states of the sweep before; the tiles written
 };
 
 template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
-sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int *sbase, uint16_t *tiles,
-             const uint16_t *stiles, float *through) {
-  using L = SweepSmem<DK>;
+sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, float *through) {
+  using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -65,10 +72,11 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages,
-           *planned = empty + kSweepStages, *w_ready = planned + 2, *done = w_ready + 2, *drain = done + 2;
+           *planned = empty + kSweepStages, *w_ready = planned + 2, *done = planned + 4, *acc_free = planned + 6,
+           *s_full = planned + 8, *s_free = planned + 10, *drain = planned + 12;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
-  if (warp == 4) tmem_alloc(tmem_sh, 256);
+  if (warp == 8) tmem_alloc(tmem_sh, 256);
   if (tid == 0) {
     for (int i = 0; i < kSweepStages; ++i) {
       mbar_init(full + i, 1);
@@ -78,6 +86,9 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
       mbar_init(planned + i, 1);
       mbar_init(w_ready + i, 128);
       mbar_init(done + i, 1);
+      mbar_init(acc_free + i, 128);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 128);
     }
     mbar_init(drain, 1);
     *failed = 0;
@@ -88,54 +99,76 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
   const uint32_t tm = *tmem_sh;
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int hk = h / (p.H / p.Hk);
+  // first row of a step's first part in the state tiles
+  auto tile_row = [&](int j) { return (int)((((size_t)(chunk0 + at(j)) * p.H + h) * 2) * DK); };
 
-  if (warp == 6) {
+  if (warp == 9) {
     if (lane == 0) {
       bool ok = true;
-      int j = 0;
-      for (; j < n_mma && ok; ++j) {
+      int loaded = 0, states = 0;
+      for (int j = 0; j < n && ok; ++j) {
         const int st = j % kSweepStages;
-        if (j >= kSweepStages) ok = wait(empty + st, j / kSweepStages - 1, SITE_SWEEP);
-        if (!ok) break;
-        mbar_arrive_expect_tx(full + st, L::KT);
+        if (j < n_mma) {
+          if (j >= kSweepStages) ok = wait(empty + st, j / kSweepStages - 1, SITE_SWEEP);
+          if (!ok) break;
+          mbar_arrive_expect_tx(full + st, L::STAGE);
+          const uint32_t dst = smem_u32(sm + st * L::STAGE);
 #pragma unroll
-        for (int kb = 0; kb < DK / 64; ++kb)
-          tma_load_3d(smem_u32(sm + st * L::KT) + kb * C * 128, &kmap, kb * 64, hk, begin + at(j) * C, full + st);
+          for (int kb = 0; kb < DK / 64; ++kb) tma_load_3d(dst + kb * C * 128, &maps.k, kb * 64, hk, begin + at(j) * C, full + st);
+          tma_load_3d(dst + L::KT, &maps.v, c0, h, begin + at(j) * C, full + st);
+          ++loaded;
+        }
+        if constexpr (REVERSE) {
+          if (j >= 2) ok = wait(s_free + (j & 1), (j >> 1) - 1, SITE_SWEEP + 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(s_full + (j & 1), 2 * L::XT);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            tma_load_3d(smem_u32(sm + L::IN + ((j & 1) * 2 + x) * L::XT), &maps.s, c0, 0, tile_row(j) + x * DK, s_full + (j & 1));
+          ++states;
+        }
       }
-      if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i < j; ++i) mbar_wait(full + i % kSweepStages, (i / kSweepStages) & 1, 2000000);
+      if (!ok) {      // loads in flight land before the block ends
+        for (int i = 0; i < loaded; ++i) mbar_wait(full + i % kSweepStages, (i / kSweepStages) & 1, 2000000);
+        for (int i = 0; i < states; ++i) mbar_wait(s_full + (i & 1), (i >> 1) & 1, 2000000);
+      }
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     if (lane == 0) {
       bool ok = true;
       for (int j = 0; j < n_mma && ok; ++j) {
         const int st = j % kSweepStages, sl = j & 1;
-        ok = wait(full + st, j / kSweepStages, SITE_SWEEP + 1) && wait(w_ready + sl, j >> 1, SITE_SWEEP + 2);
+        if (j >= 2) ok = wait(acc_free + sl, (j >> 1) - 1, SITE_SWEEP + 2);
+        ok = ok && wait(w_ready + sl, j >> 1, SITE_SWEEP + 3);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t sk = smem_u32(sm + st * L::KT), sw = smem_u32(sm + L::W + sl * 2 * L::WT);
+        const uint32_t sk = smem_u32(sm + st * L::STAGE), sw = smem_u32(sm + L::W + sl * 3 * L::VT);
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16(tm + sl * 128, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 3 * kSlice, 1, 1),
-                   s > 0);
+          mma_bf16(tm + sl * 128, desc_mnmajor(sk, C, 0, s), sdesc(sw + s * 16 * 64, L::VT, 512, 4),
+                   idesc_bf16(128, 3 * kSlice, 1, 1), s > 0);
         mma_commit(empty + st);
         mma_commit(done + sl);
       }
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
-  } else if (warp == 5) {
+  } else if (warp == 10) {
+    // ---------------- weights; the decays are loaded two steps ahead
     bool ok = true;
-    RawDecays raw{};
-    if (n_mma > 0) raw = load_decays(p, begin + at(0) * C, end, h);
+    RawDecays raw[2] = {};
+    if (n_mma > 0) raw[0] = load_decays(p, begin + at(0) * C, end, h);
+    if (n_mma > 1) raw[1] = load_decays(p, begin + at(1) * C, end, h);
     for (int j = 0; j < n_mma && ok; ++j) {
       const int sl = j & 1;
-      const RawDecays now = raw;
-      if (j + 1 < n_mma) raw = load_decays(p, begin + at(j + 1) * C, end, h);
+      const RawDecays now = raw[0];
+      raw[0] = raw[1];
+      if (j + 2 < n_mma) raw[1] = load_decays(p, begin + at(j + 2) * C, end, h);
       double d[4], total;
       uint32_t word;
       scan_decays(now, d, total, word);
-      if (j >= 2) ok = wait.warp(w_ready + sl, (j >> 1) - 1, SITE_SWEEP + 3);      // the step before has read the slot
+      // step j - 2's weights have been read, and step j - 4's whole decay (its sums' place had to be free)
+      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 4);
       if (!ok) break;
       float4 w;
       w.x = ex2((float)(REVERSE ? d[0] : total - d[0]));
@@ -144,18 +177,51 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
       w.w = ex2((float)(REVERSE ? d[3] : total - d[3]));
       reinterpret_cast<float4 *>(wgt + sl * C)[lane] = w;
       if ((lane & 7) == 0) valid[4 * sl + (lane >> 3)] = word;
-      if (lane == 0) whole[sl] = ex2((float)total);
+      if (lane == 0) whole[j & 3] = ex2((float)total);
       __syncwarp();
       if (lane == 0) mbar_arrive(planned + sl);
     }
-  } else {
-    // thread: row of the chunk (w V), then row of the state
+  } else if (warp < 4) {
+    // ---------------- w V (thread: row of the chunk)
     const int r = tid;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const uint16_t *vals = reinterpret_cast<const uint16_t *>(REVERSE ? p.d_o : p.v);
+    bool ok = true;
+    for (int j = 0; j < n_mma && ok; ++j) {
+      const int sl = j & 1, st = j % kSweepStages;
+      ok = wait.warp(planned + sl, j >> 1, SITE_SWEEP + 6) && wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 7);
+      if (!ok) break;
+      const bool real = (valid[4 * sl + warp] >> lane) & 1;
+      const float w = wgt[sl * C + r];
+      unsigned char *sk = sm + st * L::STAGE;
+      uint4 u[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        u[c] = real ? *reinterpret_cast<const uint4 *>(sk + L::KT + slice_at(r, c)) : make_uint4(0, 0, 0, 0);
+      if (!real)
+#pragma unroll
+        for (int c = 0; c < DK / 8; ++c)
+          *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
+      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 8);
+      if (!ok) break;
+      unsigned char *sw = sm + L::W + sl * 3 * L::VT;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f[8];
+        unpack8(u[c], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= w;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint4 *>(sw + x * L::VT + slice_at(r, c)) = take_bf16(f);
+      }
+      fence_async_smem();
+      mbar_arrive(w_ready + sl);
+    }
+  } else {
+    // ---------------- the state (thread: its row)
+    const int r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float *in = REVERSE ? p.d_final : p.init_state;
     const size_t own = (((size_t)b * p.H + h) * DK + r) * DV + c0;
-    float S[kSlice], keep = 0.f, keep_next = 0.f;
+    float S[kSlice];
 #pragma unroll
     for (int e = 0; e < kSlice; ++e) S[e] = 0.f;
     if (in != nullptr && r < DK)
@@ -164,107 +230,65 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
         const float4 f = *reinterpret_cast<const float4 *>(in + own + e);
         S[e] = f.x; S[e + 1] = f.y; S[e + 2] = f.z; S[e + 3] = f.w;
       }
-    uint4 u[4];
-    auto fetch = [&](int j) {
-      const int pos = begin + at(j) * C + r;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        u[c] = pos < end ? __ldcs(reinterpret_cast<const uint4 *>(vals + ((size_t)pos * p.H + h) * DV + c0) + c)
-                         : make_uint4(0, 0, 0, 0);
-    };
-    if (n_mma > 0) fetch(0);
     bool ok = true;
-    for (int j = 0; j <= n && ok; ++j) {
-      keep = keep_next;
-      if (j < n_mma) {
-        const int sl = j & 1, st = j % kSweepStages;
-        ok = wait.warp(planned + sl, j >> 1, SITE_SWEEP + 4);
-        if (!ok) break;
-        const bool real = (valid[4 * sl + warp] >> lane) & 1;
-        const float w = wgt[sl * C + r];
-        keep_next = whole[sl];
-        if (!__all_sync(0xFFFFFFFFu, real)) {
-          ok = wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 5);
-          if (!ok) break;
-          if (!real) {
-#pragma unroll
-            for (int c = 0; c < DK / 8; ++c)
-              *reinterpret_cast<uint4 *>(sm + st * L::KT + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) u[c] = make_uint4(0, 0, 0, 0);
-          }
-        }
-        unsigned char *sw = sm + L::W + sl * 2 * L::WT;      // its MMA (two steps ago) is done
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float f[8];
-          unpack8(u[c], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= w;
-          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 0, c, C)) = take_bf16(f);
-          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 0, 4 + c, C)) = take_bf16(f);
-          *reinterpret_cast<uint4 *>(sw + row_tile_chunk(r, 1, c, C)) = take_bf16(f);
-        }
-        fence_async_smem();
-        fence_before_sync();
-        mbar_arrive(w_ready + sl);
-        if (j + 1 < n_mma) fetch(j + 1);
-      }
-      if (j == 0) continue;
-      // step j - 1: the state before it goes out, then takes the chunk in
-      const int x = j - 1, sl = x & 1;
-      const size_t tile = tile_at(chunk0 + at(x), p.H, h, DK, DV) + (size_t)r * DV + c0;
-      float dot = 0.f;
-      if (r < DK) {
-        if constexpr (REVERSE) {
-          const uint4 *s0 = reinterpret_cast<const uint4 *>(stiles + tile), *s1 = reinterpret_cast<const uint4 *>(stiles + tile + (size_t)DK * DV);
-          uint4 hi[4], lo[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            hi[c] = __ldg(s0 + c);
-            lo[c] = __ldg(s1 + c);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float f[8], g[8];
-            unpack8(hi[c], f);
-            unpack8(lo[c], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(f[e] + g[e], S[8 * c + e], dot);
-          }
-        }
-        uint4 *d0 = reinterpret_cast<uint4 *>(tiles + tile), *d1 = reinterpret_cast<uint4 *>(tiles + tile + (size_t)DK * DV);
+    for (int j = 0; j < n && ok; ++j) {
+      const int sl = j & 1;
+      if (r == 0) bulk_wait_read();
+      asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before has left
+      if (r < DK)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = S[8 * c + e];
-          d0[c] = take_bf16(f);
-          d1[c] = take_bf16(f);
+          *reinterpret_cast<uint4 *>(sm + L::OUT + slice_at(r, c)) = take_bf16(f);
+          *reinterpret_cast<uint4 *>(sm + L::OUT + L::XT + slice_at(r, c)) = take_bf16(f);
         }
+      fence_async_smem();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (r == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tma_store_3d(&maps.out, smem_u32(sm + L::OUT + x * L::XT), c0, 0, tile_row(j) + x * DK);
+        bulk_commit();
       }
       if constexpr (REVERSE) {
+        ok = wait.warp(s_full + sl, j >> 1, SITE_SWEEP + 9);
+        if (!ok) break;
+        const unsigned char *t = sm + L::IN + sl * 2 * L::XT;
+        float dot = 0.f;
+        if (r < DK)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float f[8], g[8];
+            unpack8(*reinterpret_cast<const uint4 *>(t + slice_at(r, c)), f);
+            unpack8(*reinterpret_cast<const uint4 *>(t + L::XT + slice_at(r, c)), g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(f[e] + g[e], S[8 * c + e], dot);
+          }
+        mbar_arrive(s_free + sl);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-        if (lane == 0) through[(((size_t)(chunk0 + at(x)) * p.H + h) * SL + c0 / kSlice) * 4 + warp] = dot;
+        if (lane == 0) through[(((size_t)(chunk0 + at(j)) * p.H + h) * SL + c0 / kSlice) * 4 + (warp & 3)] = dot;
       }
-      if (x >= n_mma) continue;
-      ok = wait.warp(done + sl, x >> 1, SITE_SWEEP + 6);
+      if (j >= n_mma) continue;
+      ok = wait.warp(done + sl, j >> 1, SITE_SWEEP + 10);
       if (!ok) break;
       fence_after_sync();
-      const float a = keep;
-      uint32_t y[32], z[32];
-      tmem_ld32_issue(tm + lanes + sl * 128, y);
-      tmem_ld32_issue(tm + lanes + sl * 128 + 32, z);
+      const float a = whole[j & 3];
+      uint32_t x[32], y[32], z[32];
+      tmem_ld32_issue(tm + lanes + sl * 128, x);
+      tmem_ld32_issue(tm + lanes + sl * 128 + 32, y);
+      tmem_ld32_issue(tm + lanes + sl * 128 + 64, z);
+      tmem_ld32_wait(x);
       tmem_ld32_wait(y);
       tmem_ld32_wait(z);
+      fence_before_sync();
+      mbar_arrive(acc_free + sl);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) S[e] = fmaf(a, S[e], __uint_as_float(y[e]) + __uint_as_float(z[e]));
-      tmem_ld32_issue(tm + lanes + sl * 128 + 64, y);
-      tmem_ld32_wait(y);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) S[e] += __uint_as_float(y[e]);
+      for (int e = 0; e < 32; ++e)
+        S[e] = fmaf(a, S[e], __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e])));
     }
+    if (r == 0) bulk_wait_all();
     if (REVERSE && p.g_init != nullptr && ok && r < DK)
 #pragma unroll
       for (int e = 0; e < kSlice; e += 4)
@@ -272,7 +296,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ CUtensorMap kmap, const int
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     fence_after_sync();
     tmem_dealloc(tm, 256);
   }
@@ -820,42 +844,29 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
   return w;
 }
 
-// State tiles as [rows][1][dv] in boxes of dk rows and 64 columns.
-inline bool encode_tiles(CUtensorMap *map, const void *ptr, int dk, int dv, size_t rows) {
-  auto fn = encoder();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)dv, 1u, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)dv * 2, (cuuint64_t)dv * 2};
-  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)dk}, one[3] = {1u, 1u, 1u};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int DK, int DV>
-cudaError_t launch_backward(const LinearParams &p, const GradMaps &maps, const BackwardWorkspace &w, size_t chunks,
-                            cudaStream_t s) {
+cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const SweepMaps &mr, const GradMaps &mg,
+                            const BackwardWorkspace &w, size_t items, cudaStream_t s) {
   unsigned char *ws = static_cast<unsigned char *>(p.ws);
   const int *sbase = reinterpret_cast<const int *>(ws + w.sbase);
   float *through = reinterpret_cast<float *>(ws + w.through);
-  uint16_t *st = reinterpret_cast<uint16_t *>(ws + w.s), *dt = reinterpret_cast<uint16_t *>(ws + w.d);
-  const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice), items = chunks * p.H;
+  const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice);
   if (sweeps > 0x7FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   auto fwd = sweep_kernel<DK, DV, false>, rev = sweep_kernel<DK, DV, true>;
   auto grad = grad_kernel<DK, DV>;
-  constexpr int sweep_smem = SweepSmem<DK>::END, grad_smem = GradSmem<DK, DV>::END;
-  cudaError_t e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, sweep_smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rev, cudaFuncAttributeMaxDynamicSharedMemorySize, sweep_smem);
+  constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END, grad_smem = GradSmem<DK, DV>::END;
+  cudaError_t e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rev, cudaFuncAttributeMaxDynamicSharedMemorySize, rev_smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem);
   if (e != cudaSuccess) return e;
-  fwd<<<(unsigned)sweeps, kSweepThreads, sweep_smem, s>>>(p, maps.k, sbase, st, nullptr, nullptr);
+  fwd<<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, nullptr);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  rev<<<(unsigned)sweeps, kSweepThreads, sweep_smem, s>>>(p, maps.q, sbase, dt, st, through);
+  rev<<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, through);
   if ((e = cudaGetLastError()) != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
-  grad<<<grid, kGradThreads, grad_smem, s>>>(p, maps, sbase, through,
+  grad<<<grid, kGradThreads, grad_smem, s>>>(p, mg, sbase, through,
                                              shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr,
                                              shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr, gla);
   return cudaGetLastError();
@@ -868,7 +879,7 @@ size_t linear_backward_tc_workspace(const LinearParams &p) { return lintc::backw
 cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float **gk32, float **gla, cudaStream_t s) {
   using namespace lintc;
   const BackwardWorkspace w = backward_layout(p);
-  const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
+  const size_t items = lin::max_segments(p.N, p.num_seqs, C) * p.H;
   unsigned char *ws = static_cast<unsigned char *>(p.ws);
   const bool shared = p.H != p.Hk;
   *gq32 = shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr;
@@ -876,19 +887,28 @@ cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float
   *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, s);
   if (e != cudaSuccess) return e;
-  GradMaps m{};
+  GradMaps mg{};
+  SweepMaps mf{}, mr{};
   if (p.N > 0) {
-    const size_t rows = chunks * p.H * 2 * p.dk;
-    bool ok = encode(&m.q, p.q, p.dk, p.Hk, p.N) && encode(&m.k, p.k, p.dk, p.Hk, p.N) &&
-              encode(&m.v, p.v, p.dv, p.H, p.N) && encode(&m.d_o, p.d_o, p.dv, p.H, p.N) &&
-              encode(&m.gv, p.gv, p.dv, p.H, p.N) && encode_tiles(&m.s, ws + w.s, p.dk, p.dv, rows) &&
-              encode_tiles(&m.d, ws + w.d, p.dk, p.dv, rows);
-    if (!shared) ok = ok && encode(&m.gq, p.gq, p.dk, p.H, p.N) && encode(&m.gk, p.gk, p.dk, p.H, p.N);
+    const size_t rows = items * 2 * p.dk;
+    const void *st = ws + w.s, *dt = ws + w.d;
+    bool ok = encode(&mg.q, p.q, p.dk, p.Hk, p.N) && encode(&mg.k, p.k, p.dk, p.Hk, p.N) &&
+              encode(&mg.v, p.v, p.dv, p.H, p.N) && encode(&mg.d_o, p.d_o, p.dv, p.H, p.N) &&
+              encode(&mg.gv, p.gv, p.dv, p.H, p.N) && encode(&mg.s, st, p.dv, 1, rows, p.dk) &&
+              encode(&mg.d, dt, p.dv, 1, rows, p.dk) && encode(&mf.v, p.v, p.dv, p.H, p.N, C, kSlice) &&
+              encode(&mr.v, p.d_o, p.dv, p.H, p.N, C, kSlice) && encode(&mf.out, st, p.dv, 1, rows, p.dk, kSlice) &&
+              encode(&mr.out, dt, p.dv, 1, rows, p.dk, kSlice);
+    if (!shared) ok = ok && encode(&mg.gq, p.gq, p.dk, p.H, p.N) && encode(&mg.gk, p.gk, p.dk, p.H, p.N);
     if (!ok) return cudaErrorNotSupported;
+    mf.k = mg.k;
+    mr.k = mg.q;
+    mr.s = mf.out;
   }
   if (p.dk == 128)
-    return p.dv == 128 ? launch_backward<128, 128>(p, m, w, chunks, s) : launch_backward<128, 64>(p, m, w, chunks, s);
-  return p.dv == 128 ? launch_backward<64, 128>(p, m, w, chunks, s) : launch_backward<64, 64>(p, m, w, chunks, s);
+    return p.dv == 128 ? launch_backward<128, 128>(p, mf, mr, mg, w, items, s)
+                       : launch_backward<128, 64>(p, mf, mr, mg, w, items, s);
+  return p.dv == 128 ? launch_backward<64, 128>(p, mf, mr, mg, w, items, s)
+                     : launch_backward<64, 64>(p, mf, mr, mg, w, items, s);
 }
 
 }  // namespace kda

@@ -189,16 +189,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// [N, heads, d] bf16 in boxes of 128 rows of one head and 64 columns, 128-byte swizzle.
-inline bool encode(CUtensorMap *map, const void *ptr, int d, int heads, int N) {
+// [N, heads, d] bf16 in boxes of `rows` rows of one head and 64 columns with the 128-byte swizzle, or 32 columns
+// with the 64-byte one.
+inline bool encode(CUtensorMap *map, const void *ptr, int d, int heads, size_t N, int rows = C, int cols = 64) {
   auto fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)N};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * heads};
-  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)C}, one[3] = {1u, 1u, 1u};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, 1u, (cuuint32_t)rows}, one[3] = {1u, 1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline int sm_count() {
