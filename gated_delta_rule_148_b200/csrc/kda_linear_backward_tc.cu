@@ -25,15 +25,41 @@ namespace kda {
 namespace lintc {
 
 // Wait sites reported with a timeout.
-enum : unsigned { SITE_SWEEP = 71, SITE_GRAD = 81 };
+enum : unsigned { SITE_SWEEP = 71, SITE_GRAD = 91 };
 
 // State tiles: [chunk x H + h][2 parts][DK][DV] bf16.
 
+// ============================================================ tables
+// The sweep's weights of a chunk and head, one warp each: 2^{b_C - b_s}, 2^{b_t}; bits of the real rows, 2^{b_C}.
+// Apart from the sweep, where the sums of one chunk took longer than its products.
+struct Table {
+  float to[C], from[C];
+  uint32_t valid[4];
+  float whole, pad[3];
+};
+
+__global__ void __launch_bounds__(256) table_kernel(LinearParams p, const int *sbase, Table *tables) {
+  if (device_error_latched(p.err)) return;
+  const size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= (size_t)sbase[p.num_seqs] * p.H) return;
+  const int lane = threadIdx.x & 31;
+  const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, (int)(i / p.H), C);
+  double b[4], total;
+  uint32_t word;
+  scan_decays(load_decays(p, sg.begin, sg.end, (int)(i % p.H)), b, total, word);
+  Table &t = tables[i];
+  reinterpret_cast<float4 *>(t.to)[lane] = make_float4(ex2((float)(total - b[0])), ex2((float)(total - b[1])),
+                                                       ex2((float)(total - b[2])), ex2((float)(total - b[3])));
+  reinterpret_cast<float4 *>(t.from)[lane] = make_float4(ex2((float)b[0]), ex2((float)b[1]), ex2((float)b[2]), ex2((float)b[3]));
+  if ((lane & 7) == 0) t.valid[lane >> 3] = word;
+  if (lane == 0) t.whole = ex2((float)total);
+}
+
 // ============================================================ sweep
-// Roles: a load warp (K tile and 32 columns of V, three stages ahead), a warp that prepares the weights, one
-// warpgroup that writes w V, an MMA thread, one warpgroup that holds the state.  A step's tiles of the state
+// Roles: a load warp (K tile, 32 columns of V and the weights, three stages ahead), one warpgroup that writes
+// w V, an MMA thread, one warpgroup that holds the state.  A step's tiles of the state
 // leave (and S's arrive) through shared memory, since its rows are 64 bytes apart from each other's neighbours.
-constexpr int kSweepThreads = 8 * 32 + 96;
+constexpr int kSweepThreads = 8 * 32 + 64;
 constexpr int kSweepStages = 3;
 constexpr int kSlice = 32;                      // d_v columns of a block
 
@@ -43,8 +69,8 @@ struct SweepSmem {
   // W: three parts of w V, two steps.  DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and
   // are not used
   static constexpr uint32_t W = kSweepStages * STAGE, OUT = W + 2 * 3 * VT, IN = OUT + 2 * XT;
-  static constexpr uint32_t WGT = IN + (REVERSE ? 2 * 2 * XT : 0), VALID = WGT + 2 * C * 4, WHOLE = VALID + 32;
-  static constexpr uint32_t BARS = WHOLE + 16, END = BARS + 24 * 8;
+  static constexpr uint32_t WGT = IN + (REVERSE ? 2 * 2 * XT : 0), VALID = WGT + kSweepStages * C * 4;
+  static constexpr uint32_t BARS = VALID + kSweepStages * 16, END = BARS + 24 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -57,7 +83,7 @@ struct SweepMaps {
 
 template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
-sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, float *through) {
+sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const Table *tables, float *through) {
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
@@ -70,10 +96,8 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   auto at = [&](int j) { return REVERSE ? n - 1 - j : j; };      // chunk of step j
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
-  float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages,
-           *planned = empty + kSweepStages, *w_ready = planned + 2, *done = planned + 4, *acc_free = planned + 6,
-           *s_full = planned + 8, *s_free = planned + 10, *drain = planned + 12;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages, *w_ready = empty + kSweepStages,
+           *done = w_ready + 2, *acc_free = w_ready + 4, *s_full = w_ready + 6, *s_free = w_ready + 8, *drain = w_ready + 10;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 8) tmem_alloc(tmem_sh, 256);
@@ -83,7 +107,6 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(planned + i, 1);
       mbar_init(w_ready + i, 128);
       mbar_init(done + i, 1);
       mbar_init(acc_free + i, 128);
@@ -99,6 +122,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   const uint32_t tm = *tmem_sh;
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int hk = h / (p.H / p.Hk);
+  const Table *table = tables + (size_t)chunk0 * p.H + h;
   // first row of a step's first part in the state tiles
   auto tile_row = [&](int j) { return (int)((((size_t)(chunk0 + at(j)) * p.H + h) * 2) * DK); };
 
@@ -111,8 +135,11 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         if (j < n_mma) {
           if (j >= kSweepStages) ok = wait(empty + st, j / kSweepStages - 1, SITE_SWEEP);
           if (!ok) break;
-          mbar_arrive_expect_tx(full + st, L::STAGE);
+          mbar_arrive_expect_tx(full + st, L::STAGE + C * 4 + 16);
           const uint32_t dst = smem_u32(sm + st * L::STAGE);
+          const Table &t = table[(size_t)at(j) * p.H];
+          bulk_load(wgt + st * C, REVERSE ? t.from : t.to, C * 4, full + st);
+          bulk_load(valid + st * 4, t.valid, 16, full + st);
 #pragma unroll
           for (int kb = 0; kb < DK / 64; ++kb) tma_load_3d(dst + kb * C * 128, &maps.k, kb * 64, hk, begin + at(j) * C, full + st);
           tma_load_3d(dst + L::KT, &maps.v, c0, h, begin + at(j) * C, full + st);
@@ -153,44 +180,16 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
-  } else if (warp == 10) {
-    // ---------------- weights; the decays are loaded two steps ahead
-    bool ok = true;
-    RawDecays raw[2] = {};
-    if (n_mma > 0) raw[0] = load_decays(p, begin + at(0) * C, end, h);
-    if (n_mma > 1) raw[1] = load_decays(p, begin + at(1) * C, end, h);
-    for (int j = 0; j < n_mma && ok; ++j) {
-      const int sl = j & 1;
-      const RawDecays now = raw[0];
-      raw[0] = raw[1];
-      if (j + 2 < n_mma) raw[1] = load_decays(p, begin + at(j + 2) * C, end, h);
-      double d[4], total;
-      uint32_t word;
-      scan_decays(now, d, total, word);
-      // step j - 2's weights have been read, and step j - 4's whole decay (its sums' place had to be free)
-      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 4);
-      if (!ok) break;
-      float4 w;
-      w.x = ex2((float)(REVERSE ? d[0] : total - d[0]));
-      w.y = ex2((float)(REVERSE ? d[1] : total - d[1]));
-      w.z = ex2((float)(REVERSE ? d[2] : total - d[2]));
-      w.w = ex2((float)(REVERSE ? d[3] : total - d[3]));
-      reinterpret_cast<float4 *>(wgt + sl * C)[lane] = w;
-      if ((lane & 7) == 0) valid[4 * sl + (lane >> 3)] = word;
-      if (lane == 0) whole[j & 3] = ex2((float)total);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(planned + sl);
-    }
   } else if (warp < 4) {
     // ---------------- w V (thread: row of the chunk)
     const int r = tid;
     bool ok = true;
     for (int j = 0; j < n_mma && ok; ++j) {
       const int sl = j & 1, st = j % kSweepStages;
-      ok = wait.warp(planned + sl, j >> 1, SITE_SWEEP + 6) && wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 7);
+      ok = wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 4);
       if (!ok) break;
-      const bool real = (valid[4 * sl + warp] >> lane) & 1;
-      const float w = wgt[sl * C + r];
+      const bool real = (valid[4 * st + warp] >> lane) & 1;
+      const float w = wgt[st * C + r];
       unsigned char *sk = sm + st * L::STAGE;
       uint4 u[4];
 #pragma unroll
@@ -200,7 +199,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
 #pragma unroll
         for (int c = 0; c < DK / 8; ++c)
           *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
-      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 8);
+      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 5);
       if (!ok) break;
       unsigned char *sw = sm + L::W + sl * 3 * L::VT;
 #pragma unroll
@@ -231,8 +230,11 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         S[e] = f.x; S[e + 1] = f.y; S[e + 2] = f.z; S[e + 3] = f.w;
       }
     bool ok = true;
+    float next = n > 0 ? table[(size_t)at(0) * p.H].whole : 0.f;
     for (int j = 0; j < n && ok; ++j) {
       const int sl = j & 1;
+      const float a = next;
+      if (j + 1 < n) next = table[(size_t)at(j + 1) * p.H].whole;
       if (r == 0) bulk_wait_read();
       asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before has left
       if (r < DK)
@@ -252,7 +254,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         bulk_commit();
       }
       if constexpr (REVERSE) {
-        ok = wait.warp(s_full + sl, j >> 1, SITE_SWEEP + 9);
+        ok = wait.warp(s_full + sl, j >> 1, SITE_SWEEP + 6);
         if (!ok) break;
         const unsigned char *t = sm + L::IN + sl * 2 * L::XT;
         float dot = 0.f;
@@ -271,10 +273,9 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         if (lane == 0) through[(((size_t)(chunk0 + at(j)) * p.H + h) * SL + c0 / kSlice) * 4 + (warp & 3)] = dot;
       }
       if (j >= n_mma) continue;
-      ok = wait.warp(done + sl, j >> 1, SITE_SWEEP + 10);
+      ok = wait.warp(done + sl, j >> 1, SITE_SWEEP + 7);
       if (!ok) break;
       fence_after_sync();
-      const float a = whole[j & 3];
       uint32_t x[32], y[32], z[32];
       tmem_ld32_issue(tm + lanes + sl * 128, x);
       tmem_ld32_issue(tm + lanes + sl * 128 + 32, y);
@@ -823,7 +824,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
 
 // ============================================================ host
 struct BackwardWorkspace {
-  size_t sbase, through, s, d, gq32, gk32, gla, bytes;
+  size_t sbase, through, tables, s, d, gq32, gk32, gla, bytes;
 };
 inline BackwardWorkspace backward_layout(const LinearParams &p) {
   const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
@@ -835,6 +836,7 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
   };
   w.sbase = take(lin::table_bytes(p.num_seqs));
   w.through = take(chunks * p.H * (p.dv / 8) * 4);
+  w.tables = take(chunks * p.H * sizeof(Table));
   w.s = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
   w.d = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
   const size_t per_head = p.H != p.Hk ? (size_t)p.N * p.H * p.dk * 4 : 0;
@@ -859,9 +861,12 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   if (e == cudaSuccess) e = cudaFuncSetAttribute(rev, cudaFuncAttributeMaxDynamicSharedMemorySize, rev_smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem);
   if (e != cudaSuccess) return e;
-  fwd<<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, nullptr);
+  Table *tables = reinterpret_cast<Table *>(ws + w.tables);
+  if (items > 0) table_kernel<<<(unsigned)((items + 7) / 8), 256, 0, s>>>(p, sbase, tables);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  rev<<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, through);
+  fwd<<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, tables, nullptr);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  rev<<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, tables, through);
   if ((e = cudaGetLastError()) != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
