@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(256) table_kernel(LinearParams p, const int *s
 
 // ============================================================ sweep
 // Roles: a load warp (K tile, 32 columns of V and the weights, three stages ahead), one warpgroup that writes
-// w V, an MMA thread, one warpgroup that holds the state.  A step's tiles of the state
+// w V, an MMA thread, one warpgroup that holds the state, a warp that stores it.  A step's tiles of the state
 // leave (and S's arrive) through shared memory, since its rows are 64 bytes apart from each other's neighbours.
-constexpr int kSweepThreads = 8 * 32 + 64;
+constexpr int kSweepThreads = 8 * 32 + 96;
 constexpr int kSweepStages = 3;
 constexpr int kSlice = 32;                      // d_v columns of a block
 
@@ -97,7 +97,8 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages, *w_ready = empty + kSweepStages,
-           *done = w_ready + 2, *acc_free = w_ready + 4, *s_full = w_ready + 6, *s_free = w_ready + 8, *drain = w_ready + 10;
+           *done = w_ready + 2, *acc_free = w_ready + 4, *s_full = w_ready + 6, *s_free = w_ready + 8, *staged = w_ready + 10, *out_free = w_ready + 11,
+           *drain = w_ready + 12;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 8) tmem_alloc(tmem_sh, 256);
@@ -113,6 +114,8 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       mbar_init(s_full + i, 1);
       mbar_init(s_free + i, 128);
     }
+    mbar_init(staged, 128);
+    mbar_init(out_free, 1);
     mbar_init(drain, 1);
     *failed = 0;
   }
@@ -180,6 +183,18 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
+  } else if (warp == 10) {
+    if (lane == 0) {
+      for (int j = 0; j < n; ++j) {
+        if (!wait(staged, j, SITE_SWEEP + 8)) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tma_store_3d(&maps.out, smem_u32(sm + L::OUT + x * L::XT), c0, 0, tile_row(j) + x * DK);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(out_free);
+      }
+      bulk_wait_all();
+    }
   } else if (warp < 4) {
     // ---------------- w V (thread: row of the chunk)
     const int r = tid;
@@ -235,8 +250,8 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       const int sl = j & 1;
       const float a = next;
       if (j + 1 < n) next = table[(size_t)at(j + 1) * p.H].whole;
-      if (r == 0) bulk_wait_read();
-      asm volatile("bar.sync 1, 128;" ::: "memory");      // the tile before has left
+      if (j > 0) ok = wait.warp(out_free, j - 1, SITE_SWEEP + 9);
+      if (!ok) break;
       if (r < DK)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -247,12 +262,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
           *reinterpret_cast<uint4 *>(sm + L::OUT + L::XT + slice_at(r, c)) = take_bf16(f);
         }
       fence_async_smem();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (r == 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) tma_store_3d(&maps.out, smem_u32(sm + L::OUT + x * L::XT), c0, 0, tile_row(j) + x * DK);
-        bulk_commit();
-      }
+      mbar_arrive(staged);
       if constexpr (REVERSE) {
         ok = wait.warp(s_full + sl, j >> 1, SITE_SWEEP + 6);
         if (!ok) break;
@@ -289,7 +299,6 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
       for (int e = 0; e < 32; ++e)
         S[e] = fmaf(a, S[e], __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e])));
     }
-    if (r == 0) bulk_wait_all();
     if (REVERSE && p.g_init != nullptr && ok && r < DK)
 #pragma unroll
       for (int e = 0; e < kSlice; e += 4)
@@ -304,7 +313,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
 }
 
 // ============================================================ grad
-constexpr int kGradThreads = 8 * 32 + 96;
+constexpr int kGradThreads = 16 * 32 + 96;      // four warpgroups
 
 struct GradMaps {
   CUtensorMap q, k, v, d_o, s, d, gq, gk, gv;
@@ -317,8 +326,8 @@ struct GradSmem {
   static constexpr uint32_t X1 = XT > QT ? XT : QT;
   static constexpr uint32_t Q = 0, K = QT, V = 2 * QT, O = V + VT, X = O + VT, M = X + 2 * X1, HL = M + C * C * 2;
   // column factors of the blocks (w, x) of 32 x 32 pairs, then the blocks' pair sums; the rest of the decays' sums
-  static constexpr uint32_t PAIRS = HL + C * 8, EXTRA = PAIRS + 10 * 32 * 4, SUMS = EXTRA + 2 * 32 * 4;
-  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 24 * 8;
+  static constexpr uint32_t PAIRS = HL + C * 8 + 256, SUMS = PAIRS + 10 * 32 * 4;
+  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 26 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -373,58 +382,63 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
   const int nitems = sbase[p.num_seqs] * p.H;
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
   float *ksum = reinterpret_cast<float *>(sm + L::HL);      // after the pairs' decays are done with
-  float *pairs = reinterpret_cast<float *>(sm + L::PAIRS), *extra = reinterpret_cast<float *>(sm + L::EXTRA);
+  float *extra = ksum + C;                                  // of the blocks (w, x), w < x; also then
+  float *pairs = reinterpret_cast<float *>(sm + L::PAIRS);
   float *sums = reinterpret_cast<float *>(sm + L::SUMS);    // warps' totals: q.E, k.F
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 1, *s_full = full + 2, *d_full = full + 3,
            *ag_done = full + 4, *e_done = full + 5, *f_done = full + 6, *u_done = full + 7, *conv = full + 8,
            *e_scaled = full + 9, *f_scaled = full + 10, *u_scaled = full + 11, *dq_done = full + 12, *dk_done = full + 13,
-           *dv_done = full + 14, *staged = full + 15, *out_free = full + 16, *acc_free = full + 17, *tab_free = full + 18,
-           *drain = full + 19;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 20);
+           *dv_done = full + 14, *qk_staged = full + 15, *v_staged = full + 16, *m_free = full + 17, *q_free = full + 18,
+           *k_free = full + 19, *v_free = full + 20, *tab_free = full + 21, *summed = full + 22, *drain = full + 23;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 24);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
-  if (warp == 8) tmem_alloc(tmem_sh, 512);
+  if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
-    for (int i = 0; i < 20; ++i) {
-      const bool both = i == 8 || i == 11 || i == 15 || i == 17, one = i == 9 || i == 10 || i == 18;
-      mbar_init(full + i, both ? 256 : one ? 128 : 1);
-    }
+    // arrivals: 1, or every thread of one to four warpgroups
+    const int groups[24] = {0, 0, 0, 0, 0, 0, 0, 0, 4, 1, 1, 2, 0, 0, 0, 2, 2, 0, 1, 1, 2, 1, 4, 0};
+    for (int i = 0; i < 24; ++i) mbar_init(full + i, groups[i] ? 128 * groups[i] : 1);
     *failed = 0;
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = *tmem_sh;
-  // A (then P: row blocks 0, 1 in columns 0 .. 31, row blocks 2, 3 in columns 64 .. 95), G then dV, dQ, dK
-  constexpr uint32_t T_A = 0, T_V = 128, T_Q = 256, T_K = 384;
+  // A (then P: row block x in columns 32 x .. 32 x + 15), dK; G then dV, and dQ change places from item to item, since
+  // the item before gives up dQ first
+  constexpr uint32_t T_A = 0, T_K = 384;
+  auto t_v = [&](int item) { return item & 1 ? 256u : 128u; };
+  auto t_q = [&](int item) { return item & 1 ? 128u : 256u; };
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int G = p.H / p.Hk;
   const bool shared = gq32 != nullptr;
   int it = 0;
 
-  if (warp == 9) {
+  if (warp == 17) {
     // ---------------- loads and stores
     if (lane == 0) {
       bool ok = true;
       int pos_out = -1, h_out = 0;           // the item before: its gradients, if the chunk is whole
       auto store = [&]() {
-        ok = ok && wait(staged, it - 1, SITE_GRAD);
+        ok = ok && wait(v_staged, it - 1, SITE_GRAD);
         if (!ok) return;
-        if (pos_out >= 0) {
-          if (!shared) {
-#pragma unroll
-            for (int kb = 0; kb < DK / 64; ++kb) {
-              tma_store_3d(&maps.gq, smem_u32(sm + L::X) + kb * C * 128, kb * 64, h_out, pos_out);
-              tma_store_3d(&maps.gk, smem_u32(sm + L::X + L::X1) + kb * C * 128, kb * 64, h_out, pos_out);
-            }
-          }
+        if (pos_out >= 0)
 #pragma unroll
           for (int kb = 0; kb < DV / 64; ++kb)
             tma_store_3d(&maps.gv, smem_u32(sm + L::M) + kb * C * 128, kb * 64, h_out, pos_out);
-          bulk_commit();
-          bulk_wait_read();
-        }
-        mbar_arrive(out_free);
+        bulk_commit();
+        ok = wait(qk_staged, it - 1, SITE_GRAD + 1);
+        if (!ok) return;
+        if (pos_out >= 0 && !shared)
+#pragma unroll
+          for (int kb = 0; kb < DK / 64; ++kb) {
+            tma_store_3d(&maps.gq, smem_u32(sm + L::X) + kb * C * 128, kb * 64, h_out, pos_out);
+            tma_store_3d(&maps.gk, smem_u32(sm + L::X + L::X1) + kb * C * 128, kb * 64, h_out, pos_out);
+          }
+        bulk_commit();
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        mbar_arrive(m_free);
+        bulk_wait_read();
       };
       auto load_state = [&](const CUtensorMap *map, int i, uint64_t *bar) {
         mbar_arrive_expect_tx(bar, 2 * L::XT);
@@ -438,25 +452,29 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
         const int h = i % p.H, pos = sg.begin;
-        if (it > 0) ok = wait(dv_done, it - 1, SITE_GRAD + 1);
+        // each tile once its last reader is done (K, Q: also the row sums, before dK's product)
+        if (it > 0) ok = wait(dq_done, it - 1, SITE_GRAD + 2);
         if (!ok) break;
         mbar_arrive_expect_tx(full, 2 * L::QT + 2 * L::VT);
+        loads = 3 * it + 1;
+#pragma unroll
+        for (int kb = 0; kb < DV / 64; ++kb) tma_load_3d(smem_u32(sm + L::V) + kb * C * 128, &maps.v, kb * 64, h, pos, full);
+        if (it > 0) ok = wait(dk_done, it - 1, SITE_GRAD + 3);
+        if (!ok) break;
 #pragma unroll
         for (int kb = 0; kb < DK / 64; ++kb) {
           tma_load_3d(smem_u32(sm + L::K) + kb * C * 128, &maps.k, kb * 64, h / G, pos, full);
           tma_load_3d(smem_u32(sm + L::Q) + kb * C * 128, &maps.q, kb * 64, h / G, pos, full);
         }
+        if (it > 0) ok = wait(dv_done, it - 1, SITE_GRAD + 4);
+        if (!ok) break;
 #pragma unroll
-        for (int kb = 0; kb < DV / 64; ++kb) {
-          tma_load_3d(smem_u32(sm + L::V) + kb * C * 128, &maps.v, kb * 64, h, pos, full);
-          tma_load_3d(smem_u32(sm + L::O) + kb * C * 128, &maps.d_o, kb * 64, h, pos, full);
-        }
-        loads = 3 * it + 1;
+        for (int kb = 0; kb < DV / 64; ++kb) tma_load_3d(smem_u32(sm + L::O) + kb * C * 128, &maps.d_o, kb * 64, h, pos, full);
         if (it > 0) store();
         if (!ok) break;
         load_state(&maps.s, i, s_full);
         ++loads;
-        ok = wait(e_done, it, SITE_GRAD + 2);
+        ok = wait(e_done, it, SITE_GRAD + 5);
         if (!ok) break;
         load_state(&maps.d, i, d_full);
         ++loads;
@@ -472,37 +490,42 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         if (k >= 2) mbar_wait(d_full, last & 1, 2000000);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ---------------- MMAs
     if (lane == 0) {
       bool ok = true;
       const uint32_t sq = smem_u32(sm + L::Q), sk = smem_u32(sm + L::K), sv = smem_u32(sm + L::V), so = smem_u32(sm + L::O),
                      sx = smem_u32(sm + L::X), smm = smem_u32(sm + L::M);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
-        ok = wait(ready, it, SITE_GRAD + 3);
+        const uint32_t T_V = tm + t_v(it), T_Q = tm + t_q(it);
+        ok = wait(ready, it, SITE_GRAD + 6);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s)
           mma_bf16(tm + T_A, desc_kmajor(sk, C, 0, s), desc_kmajor(sq, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
-        if (it > 0) ok = wait(acc_free, it - 1, SITE_GRAD + 4);
+        if (it > 0) ok = wait(q_free, it - 1, SITE_GRAD + 7);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DV / 16; ++s)
-          mma_bf16(tm + T_V, desc_kmajor(sv, C, 0, s), desc_kmajor(so, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
+          mma_bf16(T_V, desc_kmajor(sv, C, 0, s), desc_kmajor(so, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
         mma_commit(ag_done);
-        ok = wait(s_full, it, SITE_GRAD + 5);
+        if (it > 0) ok = wait(v_free, it - 1, SITE_GRAD + 8);
+        ok = ok && wait(s_full, it, SITE_GRAD + 9);
         if (!ok) break;
+        fence_after_sync();
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int s = 0; s < DV / 16; ++s)
-            mma_bf16(tm + T_Q, desc_kmajor(so, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
+            mma_bf16(T_Q, desc_kmajor(so, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
         mma_commit(e_done);
-        ok = wait(d_full, it, SITE_GRAD + 6);
+        if (it > 0) ok = wait(k_free, it - 1, SITE_GRAD + 10);
+        ok = ok && wait(d_full, it, SITE_GRAD + 11);
         if (!ok) break;
+        fence_after_sync();
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -510,40 +533,39 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
             mma_bf16(tm + T_K, desc_kmajor(sv, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
         mma_commit(f_done);
-        ok = wait(conv, it, SITE_GRAD + 7);
+        ok = wait(conv, it, SITE_GRAD + 12);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s)
-          mma_bf16(tm + T_V, desc_kmajor(sk, C, 0, s), desc_mnmajor(sx, DK, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
+          mma_bf16(T_V, desc_kmajor(sk, C, 0, s), desc_mnmajor(sx, DK, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
         mma_commit(u_done);
-        ok = wait(e_scaled, it, SITE_GRAD + 8);
+        ok = wait(e_scaled, it, SITE_GRAD + 13);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16(tm + T_Q, desc_mnmajor(smm, C, 0, s), desc_mnmajor(sk, C, 0, s), idesc_bf16(128, DK, 1, 1), 1);
+          mma_bf16(T_Q, desc_mnmajor(smm, C, 0, s), desc_mnmajor(sk, C, 0, s), idesc_bf16(128, DK, 1, 1), 1);
         mma_commit(dq_done);
-        ok = wait(f_scaled, it, SITE_GRAD + 9);
+        ok = wait(f_scaled, it, SITE_GRAD + 14);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
           mma_bf16(tm + T_K, desc_kmajor(smm, C, 0, s), desc_mnmajor(sq, C, 0, s), idesc_bf16(128, DK, 0, 1), 1);
         mma_commit(dk_done);
-        ok = wait(u_scaled, it, SITE_GRAD + 10);
+        ok = wait(u_scaled, it, SITE_GRAD + 15);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16_ta(tm + T_V, tm + T_A + 64 * (s >> 2) + 8 * (s & 3), desc_mnmajor(so, C, 0, s), idesc_bf16(128, DV, 0, 1),
-                      1);
+          mma_bf16_ta(T_V, tm + T_A + 32 * (s >> 1) + 8 * (s & 1), desc_mnmajor(so, C, 0, s), idesc_bf16(128, DV, 0, 1), 1);
         mma_commit(dv_done);
       }
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ---------------- decays and rows to clear
     bool ok = true;
     RawDecays raw{};
@@ -560,7 +582,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       const RawDecays now = raw;
       next(i + gridDim.x);
       const bool clean = scan_decays(now, b, total, word);
-      if (it > 0) ok = wait.warp(tab_free, it - 1, SITE_GRAD + 11);
+      if (it > 0) ok = wait.warp(tab_free, it - 1, SITE_GRAD + 16);
       if (!ok) break;
       if ((lane & 7) == 0) valid[lane >> 3] = word;
 #pragma unroll
@@ -569,7 +591,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         hl[4 * lane + e] = make_float2(hi, (float)(b[e] - (double)hi));
       }
       __syncwarp();
-      ok = wait.warp(full, it, SITE_GRAD + 12);
+      ok = wait.warp(full, it, SITE_GRAD + 17);
       if (!clean && ok) {
         clear_rows<DK>(sm + L::Q, valid);
         clear_rows<DK>(sm + L::K, valid);
@@ -582,136 +604,122 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
     }
   } else {
     // ---------------- thread: row r of the chunk (as s in P, M, F and U; as t in E and dQ)
-    const int r = tid & 127, w = warp & 3, y = warp >> 2;      // y: warpgroup
+    // Warpgroup y: columns 32 y .. 32 y + 31 of P and M; then E and dQ (0), F and dK (1), U and dV (2 and 3, half each)
+    const int r = tid & 127, w = warp & 3, y = warp >> 2;
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     bool ok = true;
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
       const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
       const int h = i % p.H, pos = sg.begin;
       const bool whole_chunk = pos + C <= sg.end, in = pos + r < sg.end;
+      const uint32_t T_V = tm + lanes + t_v(it), T_Q = tm + lanes + t_q(it);
       float thr = 0.f;
       if (y == 0 && lane < DV / 8) thr = through[(size_t)i * (DV / 8) + lane];
-      ok = wait.warp(ready, it, SITE_GRAD + 13);
+      ok = wait.warp(ready, it, SITE_GRAD + 18);
       if (!ok) break;
       const bool real = (valid[w] >> lane) & 1;
-      const float2 br = hl[r], be = hl[C - 1], ref = hl[32 * w + 31];
-      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
-      const float to = ex2((be.x - br.x) + (be.y - br.y)), from = ex2(br.x + br.y), whole = ex2(be.x + be.y);
-      const float rowf = ex2((ref.x - br.x) + (ref.y - br.y));
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {      // 2^{b_t - b_ref} of the blocks after the diagonal's
-        const int x = 2 * y + z;
-        if (x > w) {
-          const float2 bt = hl[32 * x + lane];
-          pairs[(x * (x + 1) / 2 + w) * 32 + lane] = ex2((bt.x - ref.x) + (bt.y - ref.y));
-        }
+      const float2 br = hl[r];
+      float fac, whole;      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
+      {
+        const float2 be = hl[C - 1];
+        fac = y == 0 ? ex2(br.x + br.y) : ex2((be.x - br.x) + (be.y - br.y));
+        whole = ex2(be.x + be.y);
+      }
+      float *slot = pairs + (y * (y + 1) / 2 + w) * 32;      // of this warp's block (w <= y)
+      float rowf = 0.f;
+      if (y > w) {      // 2^{b_t - b_ref} and 2^{b_ref - b_s}: the reference is the row block's last row
+        const float2 ref = hl[32 * w + 31], bt = hl[32 * y + lane];
+        rowf = ex2((ref.x - br.x) + (ref.y - br.y));
+        slot[lane] = ex2((bt.x - ref.x) + (bt.y - ref.y));
       }
       __syncwarp();
-      ok = wait.warp(ag_done, it, SITE_GRAD + 14);
-      if (it > 0) ok = ok && wait.warp(out_free, it - 1, SITE_GRAD + 15);
+      ok = wait.warp(ag_done, it, SITE_GRAD + 19);
+      if (it > 0) ok = ok && wait.warp(m_free, it - 1, SITE_GRAD + 20);
       if (!ok) break;
       fence_after_sync();
-      float rest = 0.f;                  // the row's pairs behind the diagonal block
+      float before = 0.f;                // of the rows before this one in the block: their pairs
+      unsigned char *mt = sm + L::M;
+      if (y < w) {
+        float zero[16];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int x = 2 * y + z;         // columns 32 x .. 32 x + 31
-        const uint32_t pcol = tm + lanes + T_A + 64 * y + 16 * z;
-        unsigned char *mt = sm + L::M;
-        if (x < w) {
-          float zero[16];
+        for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+        tmem_st16(tm + lanes + T_A + 32 * y, zero);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) zero[e] = 0.f;
-          tmem_st16(pcol, zero);
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y >> 1, 4 * (y & 1) + c, C)) = make_uint4(0, 0, 0, 0);
+      } else {
+        float f[32], pw[16];             // pairs; P as packed bf16
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y, 4 * z + c, C)) = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        uint32_t a[32], g[32];
-        tmem_ld32_issue(tm + lanes + T_A + 32 * x, a);
-        tmem_ld32_issue(tm + lanes + T_V + 32 * x, g);
-        float *slot = pairs + (x * (x + 1) / 2 + w) * 32;
-        float f[32];
-        if (x == w) {
+        for (int z = 0; z < 2; ++z) {
+          float a[16], g[16];
+          tmem_ld16(tm + lanes + T_A + 32 * y + 16 * z, a);
+          tmem_ld16(T_V + 32 * y + 16 * z, g);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 bt = hl[32 * x + e];
-            f[e] = ex2((bt.x - br.x) + (bt.y - br.y));
-          }
-        } else {
+          for (int e = 0; e < 16; e += 4) {
+            float d[4];
+            if (y == w) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 cf = *reinterpret_cast<const float4 *>(slot + e);
-            f[e] = rowf * cf.x; f[e + 1] = rowf * cf.y; f[e + 2] = rowf * cf.z; f[e + 3] = rowf * cf.w;
-          }
-        }
-        tmem_ld32_wait(a);
-        tmem_ld32_wait(g);
-        float pw[16];
+              for (int x = 0; x < 4; ++x) {
+                const float2 bt = hl[32 * y + 16 * z + e + x];
+                d[x] = ex2((bt.x - br.x) + (bt.y - br.y));
+              }
+            } else {
+              const float4 cf = *reinterpret_cast<const float4 *>(slot + 16 * z + e);
+              d[0] = rowf * cf.x; d[1] = rowf * cf.y; d[2] = rowf * cf.z; d[3] = rowf * cf.w;
+            }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float m[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 8 * c + e;
-            const bool on = x > w || k >= lane;      // t >= s
-            const float P = on ? __uint_as_float(a[k]) * f[k] : 0.f;
-            m[e] = on ? __uint_as_float(g[k]) * f[k] : 0.f;
-            f[k] = P * __uint_as_float(g[k]);
-            a[k] = __float_as_uint(P);
+            for (int x = 0; x < 4; ++x) {
+              const bool on = y > w || 16 * z + e + x >= lane;      // t >= s
+              a[e + x] = on ? a[e + x] * d[x] : 0.f;
+              f[16 * z + e + x] = a[e + x] * g[e + x];
+              g[e + x] = on ? g[e + x] * d[x] : 0.f;
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            pw[4 * c + e] = __uint_as_float(pack_bf16x2(__uint_as_float(a[8 * c + 2 * e]), __uint_as_float(a[8 * c + 2 * e + 1])));
-          *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y, 4 * z + c, C)) = pack8(m);
+          for (int e = 0; e < 8; ++e) pw[8 * z + e] = __uint_as_float(pack_bf16x2(a[2 * e], a[2 * e + 1]));
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y >> 1, 4 * (y & 1) + 2 * z + c, C)) = pack8(g + 8 * c);
         }
-        tmem_st16(pcol, pw);
+        tmem_st16(tm + lanes + T_A + 32 * y, pw);
         // pairs (s, t) with t >= u for column u; on the diagonal block only columns u > s
         float acc = 0.f;
 #pragma unroll
         for (int e = 31; e >= 0; --e) {
-          acc += f[e];
-          f[e] = (x > w || e > lane) ? acc : 0.f;
+          const float x = f[e];
+          acc += (y > w || e >= lane) ? x : 0.f;
+          f[e] = (y > w || e > lane) ? acc : 0.f;
         }
-        if (x > w) rest += f[0];
+        if (y > w) before = exclusive_sum(acc);
         const float col = column_sums(f);
         __syncwarp();
         slot[lane] = col;
+        tmem_st_wait();
       }
-      {
-        const float before = exclusive_sum(rest);
-        __syncwarp();
-        if ((w >> 1) == y) pairs[(w * (w + 1) / 2 + w) * 32 + lane] += before;
-        else if (y == 1) extra[w * 32 + lane] = before;
-      }
-      tmem_st_wait();
+      if (y < w) tmem_st_wait();
       fence_async_smem();
       fence_before_sync();
       mbar_arrive(conv);
 
       // E or F: scaled in place; its rows' products with q or k
-      ok = wait.warp(y ? f_done : e_done, it, SITE_GRAD + 16);
-      if (!ok) break;
-      fence_after_sync();
       float dot = 0.f;
-      {
-        const float fac = y ? to : from;
+      if (y < 2) {
+        ok = wait.warp(y ? f_done : e_done, it, SITE_GRAD + 21);
+        if (!ok) break;
+        fence_after_sync();
         const unsigned char *tile = sm + (y ? L::K : L::Q);
-        const uint32_t col = tm + lanes + (y ? T_K : T_Q);
-        uint32_t a[2][32];
-        tmem_ld32_issue(col, a[0]);
+        const uint32_t col = y ? tm + lanes + T_K : T_Q;
 #pragma unroll
         for (int x = 0; x < DK / 32; ++x) {
-          tmem_ld32_wait(a[x & 1]);
-          if (x + 1 < DK / 32) tmem_ld32_issue(col + 32 * (x + 1), a[(x + 1) & 1]);
           float v[32];
+          tmem_ld32(col + 32 * x, v);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float f[8];
             unpack8(*reinterpret_cast<const uint4 *>(tile + row_tile_chunk(r, x >> 1, 4 * (x & 1) + c, C)), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              v[8 * c + e] = __uint_as_float(a[x & 1][8 * c + e]) * fac;
+              v[8 * c + e] *= fac;
               dot = fmaf(v[8 * c + e], f[e], dot);
             }
           }
@@ -721,64 +729,63 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         fence_before_sync();
         mbar_arrive(y ? f_scaled : e_scaled);
       }
-      ok = wait.warp(conv, it, SITE_GRAD + 17);      // no more readers of the decays: their place takes k.F
+      ok = wait.warp(conv, it, SITE_GRAD + 22);      // no more readers of the decays: their place takes sums
       if (!ok) break;
+      if (y > w) extra[(y * (y - 1) / 2 + w) * 32 + lane] = before;
       if (y == 0) {
         dot = suffix_sum(dot);
         if (lane == 0) sums[w] = dot;
-      } else {
-        const float before = exclusive_sum(dot);
-        ksum[r] = before;
-        if (lane == 31) sums[4 + w] = before + dot;
-      }
-      ok = wait.warp(u_done, it, SITE_GRAD + 18);
-      if (!ok) break;
-      fence_after_sync();
-      {
-        const uint32_t col = tm + lanes + T_V + y * (DV / 2);
-#pragma unroll
-        for (int x = 0; x < DV / 64; ++x) {
-          float v[32];
-          tmem_ld32(col + 32 * x, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= to;
-          tmem_st32(col + 32 * x, v);
-        }
-        tmem_st_wait();
-        fence_before_sync();
-        mbar_arrive(u_scaled);
-      }
-      if (y == 0) {
+        mbar_arrive(summed);
         // the decay's gradient of row u = r
-        ok = wait.warp(u_scaled, it, SITE_GRAD + 19);
+        ok = wait.warp(summed, it, SITE_GRAD + 23);
         if (!ok) break;
         float g = dot + ksum[r];
         for (int x = w + 1; x < 4; ++x) g += sums[x];
         for (int x = 0; x < w; ++x) g += sums[4 + x];
         for (int x = 0; x <= w; ++x) g += pairs[(w * (w + 1) / 2 + x) * 32 + lane];
-        for (int x = 0; x < w; ++x)
-          for (int z = w + 1; z < 4; ++z) g += pairs[(z * (z + 1) / 2 + x) * 32];
-        if (w < 2) g += extra[w * 32 + lane];
+        for (int z = w + 1; z < 4; ++z) {
+          g += extra[(z * (z - 1) / 2 + w) * 32 + lane];
+          for (int x = 0; x < w; ++x) g += pairs[(z * (z + 1) / 2 + x) * 32];
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xFFFFFFFFu, thr, o);
         g = fmaf(whole, thr, g);
         // one decay per head: [H, N] for the sum that follows
         if (in) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
         mbar_arrive(tab_free);
+      } else {
+        if (y == 1) {
+          const float k = exclusive_sum(dot);
+          ksum[r] = k;
+          if (lane == 31) sums[4 + w] = k + dot;
+        }
+        mbar_arrive(summed);
+      }
+      if (y >= 2) {
+        ok = wait.warp(u_done, it, SITE_GRAD + 24);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t col = T_V + (y - 2) * (DV / 2);
+#pragma unroll
+        for (int x = 0; x < DV / 64; ++x) {
+          float v[32];
+          tmem_ld32(col + 32 * x, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= fac;
+          tmem_st32(col + 32 * x, v);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        mbar_arrive(u_scaled);
       }
 
-      // gradients: dQ by the first warpgroup, dK by the second, dV by both
-      auto out = [&](uint32_t col, int cols, unsigned char *tile, int tile0, uint16_t *row, float *row32) {
-        uint32_t a[2][32];
-        tmem_ld32_issue(col, a[0]);
+      // gradients: columns of `col` to 16-byte words word0 .. of the tile, or straight to the row
+      auto out = [&](uint32_t col, int cols, unsigned char *tile, int word0, uint16_t *row, float *row32) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           if (32 * x >= cols) break;
-          tmem_ld32_wait(a[x & 1]);
-          if (32 * (x + 1) < cols) tmem_ld32_issue(col + 32 * (x + 1), a[(x + 1) & 1]);
           float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(a[x & 1][e]);
+          tmem_ld32(col + 32 * x, f);
           if (row32 != nullptr) {
             if (in)
 #pragma unroll
@@ -787,7 +794,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int cc = tile0 + 4 * x + c;
+              const int cc = word0 + 4 * x + c;
               if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * c);
               else if (in) *reinterpret_cast<uint4 *>(row + 8 * cc) = pack8(f + 8 * c);
             }
@@ -795,28 +802,25 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         }
       };
       const size_t token = (size_t)(pos + r) * p.H + h;
-      ok = wait.warp(y ? dk_done : dq_done, it, SITE_GRAD + 20);
+      ok = wait.warp(y == 0 ? dq_done : y == 1 ? dk_done : dv_done, it, SITE_GRAD + 25);
       if (!ok) break;
       fence_after_sync();
-      if (shared)
-        out(tm + lanes + (y ? T_K : T_Q), DK, nullptr, 0, nullptr, (y ? gk32 : gq32) + token * DK);
-      else
-        out(tm + lanes + (y ? T_K : T_Q), DK, sm + L::X + y * L::X1, 0,
-            reinterpret_cast<uint16_t *>(y ? p.gk : p.gq) + token * DK, nullptr);
-      ok = wait.warp(dv_done, it, SITE_GRAD + 21);
-      if (!ok) break;
-      fence_after_sync();
-      out(tm + lanes + T_V + y * (DV / 2), DV / 2, sm + L::M, y * (DV / 16), reinterpret_cast<uint16_t *>(p.gv) + token * DV,
-          nullptr);
+      if (y >= 2) {
+        out(T_V + (y - 2) * (DV / 2), DV / 2, mt, (y - 2) * (DV / 16), reinterpret_cast<uint16_t *>(p.gv) + token * DV, nullptr);
+      } else {
+        const uint32_t col = y ? tm + lanes + T_K : T_Q;
+        if (shared) out(col, DK, nullptr, 0, nullptr, (y ? gk32 : gq32) + token * DK);
+        else out(col, DK, sm + L::X + y * L::X1, 0, reinterpret_cast<uint16_t *>(y ? p.gk : p.gq) + token * DK, nullptr);
+      }
       fence_before_sync();
-      mbar_arrive(acc_free);
+      mbar_arrive(y == 0 ? q_free : y == 1 ? k_free : v_free);
       if (whole_chunk) fence_async_smem();
-      mbar_arrive(staged);
+      mbar_arrive(y < 2 ? qk_staged : v_staged);
     }
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     fence_after_sync();
     tmem_dealloc(tm, 512);
   }
