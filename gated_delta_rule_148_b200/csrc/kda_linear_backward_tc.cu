@@ -18,7 +18,7 @@
 //           TMEM over A.  E, F and U are scaled in TMEM, where the second products add to them; on
 //           the way the row sums q.E and k.F give the decays' gradients, in fp32.
 // The grad kernel is a persistent block per SM: a load/store warp, an MMA thread, a warp that
-// prepares decays and clears rows that are pads or belong to the next sequence, and two warpgroups.
+// prepares decays and clears rows that are pads or belong to the next sequence, and four warpgroups.
 #include "kda_linear_tc.cuh"
 
 namespace kda {
@@ -322,12 +322,13 @@ struct GradMaps {
 template <int DK, int DV>
 struct GradSmem {
   static constexpr uint32_t QT = C * DK * 2, VT = C * DV * 2, XT = DK * DV * 2;
-  // X: the two parts of S, then of D, then the gradients of q and k on their way out; M's tile: also grad_v
-  static constexpr uint32_t X1 = XT > QT ? XT : QT;
+  // X: the two parts of S, then of D, then (first) dQ and (second) dV on their way out; M's tile: also dK
+  static constexpr uint32_t X1 = QT > VT ? QT : VT;
+  static_assert(X1 >= XT && C * C * 2 >= QT, "tiles on their way out");
   static constexpr uint32_t Q = 0, K = QT, V = 2 * QT, O = V + VT, X = O + VT, M = X + 2 * X1, HL = M + C * C * 2;
   // column factors of the blocks (w, x) of 32 x 32 pairs, then the blocks' pair sums; the rest of the decays' sums
-  static constexpr uint32_t PAIRS = HL + C * 8 + 256, SUMS = PAIRS + 10 * 32 * 4;
-  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 26 * 8;
+  static constexpr uint32_t PAIRS = HL + C * 8, SUMS = PAIRS + 10 * 32 * 4;
+  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 32 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -381,23 +382,35 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
-  float *ksum = reinterpret_cast<float *>(sm + L::HL);      // after the pairs' decays are done with
-  float *extra = ksum + C;                                  // of the blocks (w, x), w < x; also then
+  float *extra = reinterpret_cast<float *>(sm + L::HL);     // of the blocks (w, x), w < x: after the pairs' decays are done with
   float *pairs = reinterpret_cast<float *>(sm + L::PAIRS);
   float *sums = reinterpret_cast<float *>(sm + L::SUMS);    // warps' totals: q.E, k.F
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 1, *s_full = full + 2, *d_full = full + 3,
-           *ag_done = full + 4, *e_done = full + 5, *f_done = full + 6, *u_done = full + 7, *conv = full + 8,
-           *e_scaled = full + 9, *f_scaled = full + 10, *u_scaled = full + 11, *dq_done = full + 12, *dk_done = full + 13,
-           *dv_done = full + 14, *qk_staged = full + 15, *v_staged = full + 16, *m_free = full + 17, *q_free = full + 18,
-           *k_free = full + 19, *v_free = full + 20, *tab_free = full + 21, *summed = full + 22, *drain = full + 23;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 24);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 1, *x_full = full + 2,      // S, S, D, D
+           *ag_done = full + 6, *eh_done = full + 7, *e_done = full + 8, *f_done = full + 9, *u_done = full + 10,
+           *conv = full + 11, *e_scaled = full + 12, *f_scaled = full + 13, *u_scaled = full + 14, *dq_done = full + 15,
+           *dk_done = full + 16, *dv_done = full + 17, *dq_staged = full + 18, *dk_staged = full + 19,
+           *dv_staged = full + 20, *m_free = full + 21, *q_free = full + 22, *k_free = full + 23, *v_free = full + 24,
+           *tab_free = full + 25, *paired = full + 26, *summed = full + 27, *drain = full + 28;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 29);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
-    // arrivals: 1, or every thread of one to four warpgroups
-    const int groups[24] = {0, 0, 0, 0, 0, 0, 0, 0, 4, 1, 1, 2, 0, 0, 0, 2, 2, 0, 1, 1, 2, 1, 4, 0};
-    for (int i = 0; i < 24; ++i) mbar_init(full + i, groups[i] ? 128 * groups[i] : 1);
+    for (int i = 0; i < 29; ++i) mbar_init(full + i, 1);
+    // every thread of one to four warpgroups
+    mbar_init(conv, 512);
+    mbar_init(paired, 512);
+    mbar_init(e_scaled, 128);
+    mbar_init(f_scaled, 128);
+    mbar_init(u_scaled, 256);
+    mbar_init(summed, 256);
+    mbar_init(dq_staged, 128);
+    mbar_init(dk_staged, 128);
+    mbar_init(dv_staged, 256);
+    mbar_init(q_free, 128);
+    mbar_init(k_free, 128);
+    mbar_init(v_free, 256);
+    mbar_init(tab_free, 128);
     *failed = 0;
   }
   fence_before_sync();
@@ -419,76 +432,94 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
     if (lane == 0) {
       bool ok = true;
       int pos_out = -1, h_out = 0;           // the item before: its gradients, if the chunk is whole
-      auto store = [&]() {
-        ok = ok && wait(v_staged, it - 1, SITE_GRAD);
-        if (!ok) return;
-        if (pos_out >= 0)
+      auto store_q = [&]() {
+        ok = ok && wait(dq_staged, it - 1, SITE_GRAD);
+        if (ok && pos_out >= 0 && !shared)
 #pragma unroll
-          for (int kb = 0; kb < DV / 64; ++kb)
-            tma_store_3d(&maps.gv, smem_u32(sm + L::M) + kb * C * 128, kb * 64, h_out, pos_out);
-        bulk_commit();
-        ok = wait(qk_staged, it - 1, SITE_GRAD + 1);
-        if (!ok) return;
-        if (pos_out >= 0 && !shared)
-#pragma unroll
-          for (int kb = 0; kb < DK / 64; ++kb) {
+          for (int kb = 0; kb < DK / 64; ++kb)
             tma_store_3d(&maps.gq, smem_u32(sm + L::X) + kb * C * 128, kb * 64, h_out, pos_out);
-            tma_store_3d(&maps.gk, smem_u32(sm + L::X + L::X1) + kb * C * 128, kb * 64, h_out, pos_out);
-          }
         bulk_commit();
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        mbar_arrive(m_free);
-        bulk_wait_read();
       };
-      auto load_state = [&](const CUtensorMap *map, int i, uint64_t *bar) {
-        mbar_arrive_expect_tx(bar, 2 * L::XT);
+      auto store_k = [&]() {
+        ok = ok && wait(dk_staged, it - 1, SITE_GRAD + 1);
+        if (ok && pos_out >= 0 && !shared)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int kb = 0; kb < DK / 64; ++kb)
+            tma_store_3d(&maps.gk, smem_u32(sm + L::M) + kb * C * 128, kb * 64, h_out, pos_out);
+        bulk_commit();
+      };
+      auto store_v = [&]() {
+        ok = ok && wait(dv_staged, it - 1, SITE_GRAD + 2);
+        if (ok && pos_out >= 0)
 #pragma unroll
           for (int kb = 0; kb < DV / 64; ++kb)
-            tma_load_3d(smem_u32(sm + L::X + x * L::X1) + kb * DK * 128, map, kb * 64, 0, (2 * i + x) * DK, bar);
+            tma_store_3d(&maps.gv, smem_u32(sm + L::X + L::X1) + kb * C * 128, kb * 64, h_out, pos_out);
+        bulk_commit();
       };
-      int loads = 0;      // begun on full, s_full, d_full
+      auto one_left = []() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); };
+      auto load_state = [&](const CUtensorMap *map, int i, int x, uint64_t *bar) {      // part x
+        mbar_arrive_expect_tx(bar, L::XT);
+#pragma unroll
+        for (int kb = 0; kb < DV / 64; ++kb)
+          tma_load_3d(smem_u32(sm + L::X + x * L::X1) + kb * DK * 128, map, kb * 64, 0, (2 * i + x) * DK, bar);
+      };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
         const int h = i % p.H, pos = sg.begin;
         // each tile once its last reader is done (K, Q: also the row sums, before dK's product)
-        if (it > 0) ok = wait(dq_done, it - 1, SITE_GRAD + 2);
+        if (it > 0) ok = wait(dq_done, it - 1, SITE_GRAD + 3);
         if (!ok) break;
         mbar_arrive_expect_tx(full, 2 * L::QT + 2 * L::VT);
-        loads = 3 * it + 1;
 #pragma unroll
         for (int kb = 0; kb < DV / 64; ++kb) tma_load_3d(smem_u32(sm + L::V) + kb * C * 128, &maps.v, kb * 64, h, pos, full);
-        if (it > 0) ok = wait(dk_done, it - 1, SITE_GRAD + 3);
+        if (it > 0) ok = wait(dk_done, it - 1, SITE_GRAD + 4);
         if (!ok) break;
 #pragma unroll
         for (int kb = 0; kb < DK / 64; ++kb) {
           tma_load_3d(smem_u32(sm + L::K) + kb * C * 128, &maps.k, kb * 64, h / G, pos, full);
           tma_load_3d(smem_u32(sm + L::Q) + kb * C * 128, &maps.q, kb * 64, h / G, pos, full);
         }
-        if (it > 0) ok = wait(dv_done, it - 1, SITE_GRAD + 4);
+        if (it > 0) {
+          store_q();
+          ok = ok && wait(dv_done, it - 1, SITE_GRAD + 5);
+        }
         if (!ok) break;
 #pragma unroll
         for (int kb = 0; kb < DV / 64; ++kb) tma_load_3d(smem_u32(sm + L::O) + kb * C * 128, &maps.d_o, kb * 64, h, pos, full);
-        if (it > 0) store();
+        if (it > 0) {
+          store_k();
+          one_left();
+        }
         if (!ok) break;
-        load_state(&maps.s, i, s_full);
-        ++loads;
-        ok = wait(e_done, it, SITE_GRAD + 5);
+        load_state(&maps.s, i, 0, x_full);
+        if (it > 0) {
+          store_v();
+          one_left();
+          mbar_arrive(m_free);
+          bulk_wait_read();
+        }
         if (!ok) break;
-        load_state(&maps.d, i, d_full);
-        ++loads;
+        load_state(&maps.s, i, 1, x_full + 1);
+        ok = wait(eh_done, it, SITE_GRAD + 6);
+        if (!ok) break;
+        load_state(&maps.d, i, 0, x_full + 2);
+        ok = wait(e_done, it, SITE_GRAD + 7);
+        if (!ok) break;
+        load_state(&maps.d, i, 1, x_full + 3);
         pos_out = pos + C <= sg.end ? pos : -1;
         h_out = h;
       }
-      if (it > 0) store();
-      bulk_wait_all();
-      if (!ok && loads > 0) {      // loads in flight land before the block ends
-        const int last = (loads - 1) / 3, k = (loads - 1) % 3;
-        mbar_wait(full, last & 1, 2000000);
-        if (k >= 1) mbar_wait(s_full, last & 1, 2000000);
-        if (k >= 2) mbar_wait(d_full, last & 1, 2000000);
+      if (it > 0) {
+        store_q();
+        store_k();
+        store_v();
       }
+      bulk_wait_all();
+      if (!ok)      // loads in flight (of this item and the one before) land before the block ends
+        for (int x = 0; x < 10; ++x) {
+          uint64_t *bar = x < 2 ? full : x_full + (x >> 1) - 1;
+          mbar_wait(bar, (it + 1 + x) & 1, 2000000);
+        }
     }
   } else if (warp == 16) {
     // ---------------- MMAs
@@ -512,26 +543,29 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           mma_bf16(T_V, desc_kmajor(sv, C, 0, s), desc_kmajor(so, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
         mma_commit(ag_done);
         if (it > 0) ok = wait(v_free, it - 1, SITE_GRAD + 8);
-        ok = ok && wait(s_full, it, SITE_GRAD + 9);
-        if (!ok) break;
-        fence_after_sync();
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && wait(x_full + x, it, SITE_GRAD + 9);
+          if (!ok) break;
+          fence_after_sync();
 #pragma unroll
           for (int s = 0; s < DV / 16; ++s)
             mma_bf16(T_Q, desc_kmajor(so, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
-        mma_commit(e_done);
-        if (it > 0) ok = wait(k_free, it - 1, SITE_GRAD + 10);
-        ok = ok && wait(d_full, it, SITE_GRAD + 11);
-        if (!ok) break;
-        fence_after_sync();
+          mma_commit(x ? e_done : eh_done);
+        }
+        if (it > 0) ok = ok && wait(k_free, it - 1, SITE_GRAD + 10);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && wait(x_full + 2 + x, it, SITE_GRAD + 11);
+          if (!ok) break;
+          fence_after_sync();
 #pragma unroll
           for (int s = 0; s < DV / 16; ++s)
             mma_bf16(tm + T_K, desc_kmajor(sv, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
+        }
+        if (!ok) break;
         mma_commit(f_done);
         ok = wait(conv, it, SITE_GRAD + 12);
         if (!ok) break;
@@ -614,7 +648,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       const bool whole_chunk = pos + C <= sg.end, in = pos + r < sg.end;
       const uint32_t T_V = tm + lanes + t_v(it), T_Q = tm + lanes + t_q(it);
       float thr = 0.f;
-      if (y == 0 && lane < DV / 8) thr = through[(size_t)i * (DV / 8) + lane];
+      if (y == 2 && lane < DV / 8) thr = through[(size_t)i * (DV / 8) + lane];
       ok = wait.warp(ready, it, SITE_GRAD + 18);
       if (!ok) break;
       const bool real = (valid[w] >> lane) & 1;
@@ -637,8 +671,8 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       if (it > 0) ok = ok && wait.warp(m_free, it - 1, SITE_GRAD + 20);
       if (!ok) break;
       fence_after_sync();
-      float before = 0.f;                // of the rows before this one in the block: their pairs
       unsigned char *mt = sm + L::M;
+      float f[32];                       // pairs (s, t) of this row and the warp's columns
       if (y < w) {
         float zero[16];
 #pragma unroll
@@ -648,7 +682,6 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y >> 1, 4 * (y & 1) + c, C)) = make_uint4(0, 0, 0, 0);
       } else {
-        float f[32], pw[16];             // pairs; P as packed bf16
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           float a[16], g[16];
@@ -675,38 +708,45 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
               g[e + x] = on ? g[e + x] * d[x] : 0.f;
             }
           }
+          uint32_t pw[8];                // P as packed bf16
 #pragma unroll
-          for (int e = 0; e < 8; ++e) pw[8 * z + e] = __uint_as_float(pack_bf16x2(a[2 * e], a[2 * e + 1]));
+          for (int e = 0; e < 8; ++e) pw[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+          tmem_st8(tm + lanes + T_A + 32 * y + 8 * z, pw);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y >> 1, 4 * (y & 1) + 2 * z + c, C)) = pack8(g + 8 * c);
         }
-        tmem_st16(tm + lanes + T_A + 32 * y, pw);
-        // pairs (s, t) with t >= u for column u; on the diagonal block only columns u > s
+      }
+      tmem_st_wait();
+      fence_async_smem();
+      fence_before_sync();
+      mbar_arrive(conv);
+
+      // while the products run: pairs (s, t) with t >= u for column u; on the diagonal block only columns u > s
+      float before = 0.f;                // of the rows before this one in the block: their pairs
+      if (y >= w) {
         float acc = 0.f;
 #pragma unroll
         for (int e = 31; e >= 0; --e) {
-          const float x = f[e];
-          acc += (y > w || e >= lane) ? x : 0.f;
+          acc += (y > w || e >= lane) ? f[e] : 0.f;
           f[e] = (y > w || e > lane) ? acc : 0.f;
         }
         if (y > w) before = exclusive_sum(acc);
         const float col = column_sums(f);
         __syncwarp();
         slot[lane] = col;
-        tmem_st_wait();
       }
-      if (y < w) tmem_st_wait();
-      fence_async_smem();
-      fence_before_sync();
-      mbar_arrive(conv);
+      ok = wait.warp(conv, it, SITE_GRAD + 21);      // no more readers of the decays: their place takes sums
+      if (!ok) break;
+      if (y > w) extra[(y * (y - 1) / 2 + w) * 32 + lane] = before;
+      mbar_arrive(paired);
 
-      // E or F: scaled in place; its rows' products with q or k
-      float dot = 0.f;
       if (y < 2) {
-        ok = wait.warp(y ? f_done : e_done, it, SITE_GRAD + 21);
+        // E or F: scaled in place; its rows' products with q or k
+        ok = wait.warp(y ? f_done : e_done, it, SITE_GRAD + 22);
         if (!ok) break;
         fence_after_sync();
+        float dot = 0.f;
         const unsigned char *tile = sm + (y ? L::K : L::Q);
         const uint32_t col = y ? tm + lanes + T_K : T_Q;
 #pragma unroll
@@ -715,12 +755,12 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           tmem_ld32(col + 32 * x, v);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4 *>(tile + row_tile_chunk(r, x >> 1, 4 * (x & 1) + c, C)), f);
+            float k[8];
+            unpack8(*reinterpret_cast<const uint4 *>(tile + row_tile_chunk(r, x >> 1, 4 * (x & 1) + c, C)), k);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               v[8 * c + e] *= fac;
-              dot = fmaf(v[8 * c + e], f[e], dot);
+              dot = fmaf(v[8 * c + e], k[e], dot);
             }
           }
           tmem_st32(col + 32 * x, v);
@@ -728,40 +768,27 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         tmem_st_wait();
         fence_before_sync();
         mbar_arrive(y ? f_scaled : e_scaled);
-      }
-      ok = wait.warp(conv, it, SITE_GRAD + 22);      // no more readers of the decays: their place takes sums
-      if (!ok) break;
-      if (y > w) extra[(y * (y - 1) / 2 + w) * 32 + lane] = before;
-      if (y == 0) {
-        dot = suffix_sum(dot);
-        if (lane == 0) sums[w] = dot;
+        // over the rows from this one on (q.E) or before this one (k.F): to the third warpgroup, in TMEM beside P
+        const float sum = y ? exclusive_sum(dot) : suffix_sum(dot);
+        if (lane == (y ? 31 : 0)) sums[4 * y + w] = y ? sum + dot : sum;
+        tmem_st1(tm + lanes + T_A + 16 + y, sum);
+        tmem_st_wait();
+        fence_before_sync();
         mbar_arrive(summed);
-        // the decay's gradient of row u = r
-        ok = wait.warp(summed, it, SITE_GRAD + 23);
-        if (!ok) break;
-        float g = dot + ksum[r];
-        for (int x = w + 1; x < 4; ++x) g += sums[x];
-        for (int x = 0; x < w; ++x) g += sums[4 + x];
-        for (int x = 0; x <= w; ++x) g += pairs[(w * (w + 1) / 2 + x) * 32 + lane];
-        for (int z = w + 1; z < 4; ++z) {
-          g += extra[(z * (z - 1) / 2 + w) * 32 + lane];
-          for (int x = 0; x < w; ++x) g += pairs[(z * (z + 1) / 2 + x) * 32];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xFFFFFFFFu, thr, o);
-        g = fmaf(whole, thr, g);
-        // one decay per head: [H, N] for the sum that follows
-        if (in) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
-        mbar_arrive(tab_free);
       } else {
-        if (y == 1) {
-          const float k = exclusive_sum(dot);
-          ksum[r] = k;
-          if (lane == 31) sums[4 + w] = k + dot;
+        float g = 0.f;                   // the decay's gradient of row u = r
+        if (y == 2) {
+          ok = wait.warp(paired, it, SITE_GRAD + 23);
+          if (!ok) break;
+          for (int x = 0; x <= w; ++x) g += pairs[(w * (w + 1) / 2 + x) * 32 + lane];
+          for (int z = w + 1; z < 4; ++z) {
+            g += extra[(z * (z - 1) / 2 + w) * 32 + lane];
+            for (int x = 0; x < w; ++x) g += pairs[(z * (z + 1) / 2 + x) * 32];
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xFFFFFFFFu, thr, o);
+          g = fmaf(whole, thr, g);
         }
-        mbar_arrive(summed);
-      }
-      if (y >= 2) {
         ok = wait.warp(u_done, it, SITE_GRAD + 24);
         if (!ok) break;
         fence_after_sync();
@@ -777,6 +804,20 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         tmem_st_wait();
         fence_before_sync();
         mbar_arrive(u_scaled);
+        if (y == 2) {
+          ok = wait.warp(summed, it, SITE_GRAD + 25);
+          if (!ok) break;
+          fence_after_sync();
+          float rows[2];
+          tmem_ld2(tm + lanes + T_A + 16, rows);
+          g += rows[0] + rows[1];
+          for (int x = w + 1; x < 4; ++x) g += sums[x];
+          for (int x = 0; x < w; ++x) g += sums[4 + x];
+          // one decay per head: [H, N] for the sum that follows
+          if (in) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
+          fence_before_sync();
+          mbar_arrive(tab_free);
+        }
       }
 
       // gradients: columns of `col` to 16-byte words word0 .. of the tile, or straight to the row
@@ -802,20 +843,20 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         }
       };
       const size_t token = (size_t)(pos + r) * p.H + h;
-      ok = wait.warp(y == 0 ? dq_done : y == 1 ? dk_done : dv_done, it, SITE_GRAD + 25);
+      ok = wait.warp(y == 0 ? dq_done : y == 1 ? dk_done : dv_done, it, SITE_GRAD + 26);
       if (!ok) break;
       fence_after_sync();
       if (y >= 2) {
-        out(T_V + (y - 2) * (DV / 2), DV / 2, mt, (y - 2) * (DV / 16), reinterpret_cast<uint16_t *>(p.gv) + token * DV, nullptr);
+        out(T_V + (y - 2) * (DV / 2), DV / 2, sm + L::X + L::X1, (y - 2) * (DV / 16), reinterpret_cast<uint16_t *>(p.gv) + token * DV, nullptr);
       } else {
         const uint32_t col = y ? tm + lanes + T_K : T_Q;
         if (shared) out(col, DK, nullptr, 0, nullptr, (y ? gk32 : gq32) + token * DK);
-        else out(col, DK, sm + L::X + y * L::X1, 0, reinterpret_cast<uint16_t *>(y ? p.gk : p.gq) + token * DK, nullptr);
+        else out(col, DK, y ? mt : sm + L::X, 0, reinterpret_cast<uint16_t *>(y ? p.gk : p.gq) + token * DK, nullptr);
       }
       fence_before_sync();
       mbar_arrive(y == 0 ? q_free : y == 1 ? k_free : v_free);
       if (whole_chunk) fence_async_smem();
-      mbar_arrive(y < 2 ? qk_staged : v_staged);
+      mbar_arrive(y == 0 ? dq_staged : y == 1 ? dk_staged : dv_staged);
     }
   }
   fence_before_sync();
