@@ -368,10 +368,6 @@ __device__ __forceinline__ float suffix_sum(float s) {
   }
   return s;
 }
-__device__ __forceinline__ uint4 pack8(const float *f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1)
 grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sbase, const float *through, float *gq32,

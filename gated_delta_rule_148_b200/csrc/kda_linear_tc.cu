@@ -25,7 +25,7 @@ namespace lintc {
 enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
 
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v;
 };
 
 // ============================================================ parts
@@ -284,15 +284,21 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
 }
 
 // ============================================================ rows
-constexpr int kRowsThreads = 8 * 32 + 96;       // two warpgroups; TMA, MMA and preparing warps
+// Four warpgroups that take each step of a chunk together, a quarter of its columns each (a warpgroup for each step
+// measured slower: a step then takes four times as long, and few of them run side by side); TMA, MMA and
+// preparing warps.
+constexpr int kRowsThreads = 16 * 32 + 96;
 
 template <int DK, int DV>
 struct RowsSmem {
   static constexpr uint32_t QT = C * DK * 2, VT = C * DV * 2;
-  static constexpr uint32_t STAGE = 2 * QT + VT, W = 2 * STAGE;      // W: S, then w V, as bf16
+  static constexpr uint32_t STAGE = 2 * QT + VT, W = 2 * STAGE;      // W: S, then w V's first part, as bf16
   static constexpr uint32_t WB = (DK > C ? DK : C) * DV * 2;
-  static constexpr uint32_t HL = W + WB, COLF = HL + 2 * C * 8, VALID = COLF + 192 * 4, WHOLE = VALID + 32;
-  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 16 * 8;
+  // w V's second part: q's tile, which Q S reads last, where it fits
+  static constexpr bool kLoInQ = DV <= DK;
+  static constexpr uint32_t LO = W + WB;
+  static constexpr uint32_t HL = LO + (kLoInQ ? 0 : VT), COLF = HL + 2 * C * 8, VALID = COLF + 192 * 4, WHOLE = VALID + 32;
+  static constexpr uint32_t BARS = WHOLE + 8, END = BARS + 18 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -307,138 +313,117 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4,
-           *a_done = full + 6, *p_ready = full + 7, *w_ready = full + 8, *w_free = full + 9, *o_done = full + 10,
-           *o_free = full + 11, *drain = full + 12, *o_staged = full + 14;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 13);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4, *a_done = full + 6,
+           *p_ready = full + 7, *w_ready = full + 8, *qs_done = full + 9, *l_ready = full + 10, *s_done = full + 11,
+           *o_done = full + 12, *drain = full + 13;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 14);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
-  if (warp == 8) tmem_alloc(tmem_sh, 512);
+  if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(ready + i, 1);
-      mbar_init(empty + i, 1);
-      mbar_init(o_staged + i, 128);
-    }
-    mbar_init(a_done, 1);
-    mbar_init(p_ready, 128);
-    mbar_init(w_ready, 128);
-    mbar_init(w_free, 1);
-    mbar_init(o_done, 1);
-    mbar_init(o_free, 128);
-    mbar_init(drain, 1);
+    for (int i = 0; i < 14; ++i) mbar_init(full + i, 1);
+    mbar_init(p_ready, 512);
+    mbar_init(w_ready, 512);
+    mbar_init(l_ready, 512);
     *failed = 0;
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = *tmem_sh;
-  constexpr uint32_t T_S = 0, T_A = 128, T_O1 = 256, T_O2 = 384;      // P overlays A
+  constexpr uint32_t T_S = 0, T_A = 128, T_O1 = 256, T_O2 = 384;
+  // P overlays A: its columns 32 x .. 32 x + 31 in 32 x .. 32 x + 15
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int G = p.H / p.Hk;
-  int step = 0;
-  uint32_t wn = 0;           // fills of W
+  int step = 0, ln = 0;      // chunks; those among them whose S goes on to another
 
-  if (warp == 9) {
-    // ---------------- loads, and stores of whole chunks (from the q tile, and k's where o is wider)
+  if (warp == 17) {
+    // ---------------- loads
     if (lane == 0) {
       bool ok = true;
-      int done_pos[2] = {-1, -1}, done_h[2] = {0, 0};            // the chunk in each stage; pos < 0: its rows were stored directly
-      auto retire = [&](int x) {             // chunk number x: its output leaves the stage
-        const int st = x & 1;
-        ok = ok && wait(o_staged + st, x >> 1, SITE_ROWS);
-        if (!ok || done_pos[st] < 0) return;
-#pragma unroll
-        for (int kb = 0; kb < DV / 64; ++kb)
-          tma_store_3d(&maps.o, smem_u32(sm + st * L::STAGE) + kb * C * 128, kb * 64, done_h[st], done_pos[st]);
-        bulk_commit();
-        bulk_wait_read();
-      };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
         const int h = i % p.H;
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
           const uint32_t dst = smem_u32(sm + st * L::STAGE);
-          if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 14);
+          if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS);
           if (!ok) break;
           mbar_arrive_expect_tx(full + st, L::STAGE);
 #pragma unroll
+          for (int kb = 0; kb < DK / 64; ++kb) {
+            tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
+            tma_load_3d(dst + kb * C * 128, &maps.q, kb * 64, h / G, pos, full + st);
+          }
+#pragma unroll
           for (int kb = 0; kb < DV / 64; ++kb)
             tma_load_3d(dst + 2 * L::QT + kb * C * 128, &maps.v, kb * 64, h, pos, full + st);
-          if constexpr (DV <= DK)
-#pragma unroll
-            for (int kb = 0; kb < DK / 64; ++kb)
-              tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
-          if (step >= 2) retire(step - 2);
-          // (a failed wait leaves q's bytes missing: the chunk is never used)
-          if (!ok) break;
-          if constexpr (DV > DK)
-#pragma unroll
-            for (int kb = 0; kb < DK / 64; ++kb)
-              tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
-#pragma unroll
-          for (int kb = 0; kb < DK / 64; ++kb)
-            tma_load_3d(dst + kb * C * 128, &maps.q, kb * 64, h / G, pos, full + st);
-          done_pos[st] = pos + C <= sg.end ? pos : -1;
-          done_h[st] = h;
         }
       }
-      for (int x = step > 2 ? step - 2 : 0; x < step; ++x) retire(x);
-      bulk_wait_all();
       if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i <= step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+        for (int i = 0; i < step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
     }
-  } else if (warp == 8) {
-    // ---------------- MMAs
+  } else if (warp == 16) {
+    // ---------------- MMAs; a chunk's A goes ahead of Q S, which needs S complete
     if (lane == 0) {
       bool ok = true;
       const uint32_t sw = smem_u32(sm + L::W);
+      const uint32_t stage[2] = {smem_u32(sm), smem_u32(sm + L::STAGE)};
+      auto issue_a = [&](int x) {            // chunk number x
+        ok = ok && wait(ready + (x & 1), x >> 1, SITE_ROWS + 1);
+        if (!ok) return;
+        fence_after_sync();
+        const uint32_t sq = x & 1 ? stage[1] : stage[0];
+        const uint64_t q = desc_kmajor(sq, C, 0, 0), k = desc_kmajor(sq + L::QT, C, 0, 0);
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s)
+          mma_bf16(tm + T_A, kmajor_step<C>(q, s), kmajor_step<C>(k, s), idesc_bf16(128, C, 0, 0), s > 0);
+        mma_commit(a_done);
+      };
+      if (blockIdx.x < nitems) issue_a(0);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
-          const bool last = pos + C >= sg.end;
-          const uint32_t sq = smem_u32(sm + st * L::STAGE), sk = sq + L::QT, sv = sk + L::QT;
-          ok = wait(ready + st, step >> 1, SITE_ROWS + 1);
+          const bool last = pos + C >= sg.end, more = !last || i + (int)gridDim.x < nitems;
+          const uint32_t sq = st ? stage[1] : stage[0], sk = sq + L::QT, sv = sk + L::QT;
+          const uint64_t q = desc_kmajor(sq, C, 0, 0), w = desc_mnmajor(sw, DK, 0, 0), k = desc_mnmajor(sk, C, 0, 0),
+                         v = desc_mnmajor(sv, C, 0, 0), hi = desc_mnmajor(sw, C, 0, 0),
+                         lo = desc_mnmajor(L::kLoInQ ? sq : smem_u32(sm + L::LO), C, 0, 0);
+          ok = wait(w_ready, step, SITE_ROWS + 3);
           if (!ok) break;
           fence_after_sync();
 #pragma unroll
           for (int s = 0; s < DK / 16; ++s)
-            mma_bf16(tm + T_A, desc_kmajor(sq, C, 0, s), desc_kmajor(sk, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
-          mma_commit(a_done);
-          if (step > 0) ok = wait(o_free, step - 1, SITE_ROWS + 2);
-          ok = ok && wait(w_ready, wn++, SITE_ROWS + 3);
-          if (!ok) break;
-          fence_after_sync();
-#pragma unroll
-          for (int s = 0; s < DK / 16; ++s)
-            mma_bf16(tm + T_O1, desc_kmajor(sq, C, 0, s), desc_mnmajor(sw, DK, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
-          mma_commit(w_free);
-          if (!last)
-            for (int x = 0; x < 2 && ok; ++x) {
-              ok = wait(w_ready, wn++, SITE_ROWS + 4);
-              if (!ok) break;
-              fence_after_sync();
-#pragma unroll
-              for (int s = 0; s < C / 16; ++s)
-                mma_bf16(tm + T_S, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, DV, 1, 1), 1);
-              mma_commit(w_free);
-            }
-          ok = ok && wait(p_ready, step, SITE_ROWS + 5);
+            mma_bf16(tm + T_O1, kmajor_step<C>(q, s), mnmajor_step(w, s), idesc_bf16(128, DV, 0, 1), s > 0);
+          mma_commit(qs_done);
+          ok = wait(p_ready, step, SITE_ROWS + 4);
           if (!ok) break;
           fence_after_sync();
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
-            mma_bf16_ta(tm + T_O2, tm + T_A + 8 * s, desc_mnmajor(sv, C, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
+            mma_bf16_ta(tm + T_O2, tm + T_A + 32 * (s >> 1) + 8 * (s & 1), mnmajor_step(v, s), idesc_bf16(128, DV, 0, 1),
+                        s > 0);
           mma_commit(o_done);
+          if (!last) {                       // S += K^T (w V)
+            ok = wait(l_ready, ln++, SITE_ROWS + 5);
+            if (!ok) break;
+            fence_after_sync();
+#pragma unroll
+            for (int s = 0; s < C / 16; ++s)
+              mma_bf16(tm + T_S, mnmajor_step(k, s), mnmajor_step(hi, s), idesc_bf16(128, DV, 1, 1), 1);
+#pragma unroll
+            for (int s = 0; s < C / 16; ++s)
+              mma_bf16(tm + T_S, mnmajor_step(k, s), mnmajor_step(lo, s), idesc_bf16(128, DV, 1, 1), 1);
+            mma_commit(s_done);
+          }
           mma_commit(empty + st);
+          if (more) issue_a(step + 1);
         }
       }
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ---------------- decays and rows to clear; the next chunk's decays are loaded a chunk ahead
     bool ok = true;
     int ni = blockIdx.x, npos = 0;           // the chunk whose decays are on their way
@@ -468,9 +453,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         const RawDecays now = raw;
         raw = next();
         const bool clean = scan_decays(now, b, total, word);
-        // the stage's MMAs are done, and its output (which reads the tables) is staged
-        if (step >= 2)
-          ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 6) && wait(o_staged + st, (step >> 1) - 1, SITE_ROWS + 15);
+        // the stage's MMAs are done, and with them the readers of its tables
+        if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 6);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         if ((lane & 7) == 0) valid[4 * st + (lane >> 3)] = word;
@@ -492,201 +476,171 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         if (lane == 0 && ok) mbar_arrive(ready + st);
       }
     }
-  } else if (warp < 4) {
-    // ---------------- P, and the output (thread: row t of the chunk)
-    const int t = tid;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    float *colf = reinterpret_cast<float *>(sm + L::COLF) + 16 * warp * (warp - 1);     // 32 warp entries
+  } else {
+    // ---------------- thread: row r of the chunk, or of the state; warpgroup y: a quarter of the columns
+    const int r = tid & 127, w = warp & 3, y = warp >> 2;
+    constexpr int COLS = DV / 4;
+    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+    float *colf = reinterpret_cast<float *>(sm + L::COLF) + (w * (w - 1) / 2 + y) * 32;      // y < w
     bool ok = true;
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
       const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
       const int h = i % p.H;
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
+        const bool first = pos == sg.begin, last = pos + C >= sg.end;
         ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 8);
         if (!ok) break;
         const float2 *d = hl + st * C;
-        const float2 bt = d[t], ref = d[warp > 0 ? 32 * warp - 1 : 0];
-        const float rowf = ex2((bt.x - ref.x) + (bt.y - ref.y)), from = ex2(bt.x + bt.y);
-        for (int x = 0; x < warp; ++x) {
-          const float2 bs = d[32 * x + lane];
-          colf[32 * x + lane] = ex2((ref.x - bs.x) + (ref.y - bs.y));
+        const float2 bt = d[r];
+        const bool real = (valid[4 * st + w] >> lane) & 1;
+        const float keep = whole[st], from = ex2(bt.x + bt.y);
+        float to, rowf = 0.f;
+        {
+          const float2 be = d[C - 1];
+          to = ex2((be.x - bt.x) + (be.y - bt.y));
+        }
+        if (y < w) {                         // 2^{b_t - b_ref} and 2^{b_ref - b_s}: the row before the warp's rows
+          const float2 ref = d[32 * w - 1], bs = d[32 * y + lane];
+          rowf = ex2((bt.x - ref.x) + (bt.y - ref.y));
+          colf[lane] = ex2((ref.x - bs.x) + (ref.y - bs.y));
         }
         __syncwarp();
-        const bool real = (valid[4 * st + warp] >> lane) & 1;
-        ok = wait.warp(a_done, step, SITE_ROWS + 9);
+
+        // S as an operand; S <- 2^{b_C} S
+        if (!first) ok = wait.warp(s_done, ln - 1, SITE_ROWS + 12);
+        else if (step > 0) ok = wait.warp(qs_done, step - 1, SITE_ROWS + 13);      // the item before: W is free
         if (!ok) break;
         fence_after_sync();
-        const uint32_t acol = tm + lanes + T_A;
-        {
-          // the diagonal's 32 columns: each pair by itself
-          uint32_t a[32];
-          float w[16];
-          tmem_ld32_issue(acol + 32 * warp, a);
-          float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 bs = d[32 * warp + e];
-            f[e] = ex2(fminf((bt.x - bs.x) + (bt.y - bs.y), 0.f));
-          }
-          tmem_ld32_wait(a);
-          // P's columns 16 x .. lie under A's 16 x .., which A's first pieces must have left
-          uint32_t o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = e <= lane ? __uint_as_float(a[e]) * f[e] : 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(pack_bf16x2(f[2 * e], f[2 * e + 1]));
-#pragma unroll
-          for (int x = 0; x < 3; ++x) {
-            if (x < warp) {
-              tmem_ld32_issue(acol + 32 * x, o);
-              float g[16];
-              tmem_ld32_wait(o);
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(colf + 32 * x + e);
-                g[e / 2] = __uint_as_float(pack_bf16x2(__uint_as_float(o[e]) * (rowf * c.x), __uint_as_float(o[e + 1]) * (rowf * c.y)));
-                g[e / 2 + 1] = __uint_as_float(pack_bf16x2(__uint_as_float(o[e + 2]) * (rowf * c.z), __uint_as_float(o[e + 3]) * (rowf * c.w)));
-              }
-              tmem_st16(acol + 16 * x, g);
-            }
-          }
-          tmem_st16(acol + 16 * warp, w);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = 0.f;
-          for (int x = warp + 1; x < 4; ++x) tmem_st16(acol + 16 * x, w);
-        }
-        tmem_st_wait();
-        fence_before_sync();
-        mbar_arrive(p_ready);
-        ok = wait.warp(o_done, step, SITE_ROWS + 10);
-        if (!ok) break;
-        fence_after_sync();
-        unsigned char *tile = sm + st * L::STAGE;           // q's (and k's) tile: no longer read
-        const bool whole_chunk = pos + C <= sg.end;
-        uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + t) * p.H + h) * DV;
-        uint32_t a[2][32], b[2][32];
-        tmem_ld32_issue(tm + lanes + T_O1, a[0]);
-        tmem_ld32_issue(tm + lanes + T_O2, b[0]);
-#pragma unroll
-        for (int x = 0; x < DV / 32; ++x) {
-          tmem_ld32_wait(a[x & 1]);
-          tmem_ld32_wait(b[x & 1]);
-          if (x + 1 < DV / 32) {
-            tmem_ld32_issue(tm + lanes + T_O1 + 32 * (x + 1), a[(x + 1) & 1]);
-            tmem_ld32_issue(tm + lanes + T_O2 + 32 * (x + 1), b[(x + 1) & 1]);
-          }
-          float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            f[e] = real ? fmaf(from, __uint_as_float(a[x & 1][e]), __uint_as_float(b[x & 1][e])) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 u = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                       pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-            const int cc = 4 * x + e;
-            if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(t, cc >> 3, cc & 7, C)) = u;
-            else if (pos + t < sg.end) *reinterpret_cast<uint4 *>(orow + 8 * cc) = u;
-          }
-        }
-        fence_before_sync();
-        mbar_arrive(o_free);
-        if (whole_chunk) fence_async_smem();
-        mbar_arrive(o_staged + st);
-      }
-    }
-  } else {
-    // ---------------- S as an operand, S <- 2^{b_C} S, w V (thread: row of the state, then of the chunk)
-    const int r = tid & 127;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    bool ok = true;
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
-      for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
-        const int st = step & 1;
-        const bool first = pos == sg.begin, last = pos + C >= sg.end;
-        ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 11);
-        if (wn > 0) ok = ok && wait.warp(w_free, wn - 1, SITE_ROWS + 12);      // also: S has its last sum
-        if (!ok) break;
-        fence_after_sync();
-        const float keep = whole[st];
-        const float *in = start + ((size_t)i * DK + r) * DV;
         if (r < DK) {
+          const float *in = start + ((size_t)i * DK + r) * DV + y * COLS;
+          const uint32_t col = tm + lanes + T_S + y * COLS;
+          uint32_t v[COLS];
+          if (first) {
 #pragma unroll
-          for (int x = 0; x < DV / 32; x += 2) {       // 64 columns at a time
-            uint32_t v[2][32];
-            if (first) {
+            for (int e = 0; e < COLS; e += 4)
+              *reinterpret_cast<uint4 *>(&v[e]) = __ldcs(reinterpret_cast<const uint4 *>(in + e));
+          } else if constexpr (COLS == 32) {
+            tmem_ld32_issue(col, v);
+            tmem_ld32_wait(v);
+          } else {
+            tmem_ld16_issue(col, v);
+            tmem_ld16_wait(v);
+          }
+          float f[COLS];
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
+          for (int e = 0; e < COLS; ++e) f[e] = __uint_as_float(v[e]);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<uint4 *>(&v[y][e]) = __ldcs(reinterpret_cast<const uint4 *>(in + 32 * (x + y) + e));
-            } else {
-              tmem_ld32_issue(tm + lanes + T_S + 32 * x, v[0]);
-              tmem_ld32_issue(tm + lanes + T_S + 32 * (x + 1), v[1]);
-              tmem_ld32_wait(v[0]);
-              tmem_ld32_wait(v[1]);
-            }
+          for (int e = 0; e < COLS / 8; ++e) {
+            const int cc = y * (COLS / 8) + e;
+            *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, cc >> 3, cc & 7, DK)) = pack8(f + 8 * e);
+          }
+          if (!last) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float f[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[y][e]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int cc = 4 * (x + y) + e;
-                *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, cc >> 3, cc & 7, DK)) =
-                    make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                               pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-              }
-              if (!last) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] *= keep;
-                tmem_st32(tm + lanes + T_S + 32 * (x + y), f);
-              }
-            }
+            for (int e = 0; e < COLS; ++e) f[e] *= keep;
+            if constexpr (COLS == 32) tmem_st32(col, f);
+            else tmem_st16(col, f);
           }
           tmem_st_wait();
         }
         fence_async_smem();
         fence_before_sync();
         mbar_arrive(w_ready);
-        ++wn;
-        if (last) continue;
-        // both parts of w V while Q S runs; each goes to W as the product before it is done
-        const float2 bs = hl[st * C + r], be = hl[st * C + C - 1];
-        const float w = ex2((be.x - bs.x) + (be.y - bs.y));
-        const unsigned char *sv = sm + st * L::STAGE + 2 * L::QT;
-        uint4 hi[DV / 8], lo[DV / 8];
+
+        // P's columns 32 y .. 32 y + 31
+        ok = wait.warp(a_done, step, SITE_ROWS + 9);
+        if (!ok) break;
+        fence_after_sync();
+        {
+          const uint32_t col = tm + lanes + T_A + 32 * y;
+          float g[16];
+          if (y > w) {
 #pragma unroll
-        for (int c = 0; c < DV / 8; ++c) hi[c] = *reinterpret_cast<const uint4 *>(sv + row_tile_chunk(r, c >> 3, c & 7, C));
+            for (int e = 0; e < 16; ++e) g[e] = 0.f;
+          } else {
+            uint32_t a[32];
+            tmem_ld32_issue(col, a);
+            if (y < w) {
+              tmem_ld32_wait(a);
 #pragma unroll
-        for (int c = 0; c < DV / 8; ++c) {
-          float f[8];
-          unpack8(hi[c], f);
+              for (int e = 0; e < 32; e += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(colf + e);
+                g[e / 2] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e]) * (rowf * c.x), __uint_as_float(a[e + 1]) * (rowf * c.y)));
+                g[e / 2 + 1] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e + 2]) * (rowf * c.z), __uint_as_float(a[e + 3]) * (rowf * c.w)));
+              }
+            } else {                         // the diagonal: each pair by itself
+              float f[32];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= w;
-          hi[c] = take_bf16(f);
-          lo[c] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-        }
+              for (int e = 0; e < 32; ++e) {
+                const float2 bs = d[32 * y + e];
+                f[e] = ex2((bt.x - bs.x) + (bt.y - bs.y));
+              }
+              tmem_ld32_wait(a);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          ok = ok && wait.warp(w_free, wn - 1, SITE_ROWS + 13);
-          if (ok) {
+              for (int e = 0; e < 32; ++e) f[e] = e <= lane ? __uint_as_float(a[e]) * f[e] : 0.f;
 #pragma unroll
-            for (int c = 0; c < DV / 8; ++c)
-              *reinterpret_cast<uint4 *>(sm + L::W + row_tile_chunk(r, c >> 3, c & 7, C)) = x ? lo[c] : hi[c];
-            fence_async_smem();
-            mbar_arrive(w_ready);
-            ++wn;
+              for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(pack_bf16x2(f[2 * e], f[2 * e + 1]));
+            }
           }
+          tmem_st16(col, g);
+          tmem_st_wait();
+          fence_before_sync();
+          mbar_arrive(p_ready);
+        }
+
+        // the two parts of w V, once Q S is done
+        if (!last) {
+          const unsigned char *sv = sm + st * L::STAGE + 2 * L::QT;
+          unsigned char *slo = L::kLoInQ ? sm + st * L::STAGE : sm + L::LO;
+          ok = wait.warp(qs_done, step, SITE_ROWS + 14);
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < COLS / 8; ++e) {
+            const int cc = y * (COLS / 8) + e;
+            const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
+            float f[8];
+            unpack8(*reinterpret_cast<const uint4 *>(sv + at), f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= to;
+            *reinterpret_cast<uint4 *>(sm + L::W + at) = take_bf16(f);
+            *reinterpret_cast<uint4 *>(slo + at) = take_bf16(f);
+          }
+          fence_async_smem();
+          mbar_arrive(l_ready);
+          ++ln;
+        }
+
+        // the output, straight to global memory: a tile kept back for it would be loaded that much later
+        ok = wait.warp(o_done, step, SITE_ROWS + 10);
+        if (!ok) break;
+        fence_after_sync();
+        {
+          uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + r) * p.H + h) * DV + y * COLS;
+          uint32_t a[COLS], b[COLS];
+          if constexpr (COLS == 32) {
+            tmem_ld32_issue(tm + lanes + T_O1 + y * COLS, a);
+            tmem_ld32_issue(tm + lanes + T_O2 + y * COLS, b);
+            tmem_ld32_wait(a);
+            tmem_ld32_wait(b);
+          } else {
+            tmem_ld16_issue(tm + lanes + T_O1 + y * COLS, a);
+            tmem_ld16_issue(tm + lanes + T_O2 + y * COLS, b);
+            tmem_ld16_wait(a);
+            tmem_ld16_wait(b);
+          }
+          float f[COLS];
+#pragma unroll
+          for (int e = 0; e < COLS; ++e) f[e] = real ? fmaf(from, __uint_as_float(a[e]), __uint_as_float(b[e])) : 0.f;
+          if (pos + r < sg.end)
+#pragma unroll
+            for (int e = 0; e < COLS / 8; ++e) *reinterpret_cast<uint4 *>(orow + 8 * e) = pack8(f + 8 * e);
         }
       }
     }
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     fence_after_sync();
     tmem_dealloc(tm, 512);
   }
@@ -748,7 +702,7 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&
-                   encode(&maps.v, p.v, p.dv, p.H, p.N) && encode(&maps.o, p.o, p.dv, p.H, p.N)))
+                   encode(&maps.v, p.v, p.dv, p.H, p.N)))
     return cudaErrorNotSupported;
   if (p.dk == 128)
     return p.dv == 128 ? launch<128, 128>(p, maps, sbase, part, whole, per, segs, s)

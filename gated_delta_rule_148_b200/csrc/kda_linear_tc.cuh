@@ -33,6 +33,12 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, 
       :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
+// Descriptor of a tile's K-step s from that of step 0: one addition in the issuing thread, where computing each
+// from its address took longer than the product.
+template <int R>
+__device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int s) { return d + (uint32_t)(((s >> 2) * R * 128 + (s & 3) * 32) >> 4); }
+__device__ __forceinline__ uint64_t mnmajor_step(uint64_t d, int s) { return d + (uint32_t)(16 * s * 128 >> 4); }
+
 // 2^x with results below 2^-126 taken as 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -62,6 +68,19 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
         "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
 }
 
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
+}
 // Eight columns stored; one column stored, two loaded.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -180,6 +199,9 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
     f[2 * e] = __uint_as_float(a[e] << 16);
     f[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
   }
+}
+__device__ __forceinline__ uint4 pack8(const float *f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 // Rounds 8 floats to bf16 (returned packed) and leaves the remainders in f.
 __device__ __forceinline__ uint4 take_bf16(float (&f)[8]) {
