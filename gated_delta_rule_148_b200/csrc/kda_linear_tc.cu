@@ -25,7 +25,7 @@ namespace lintc {
 enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 // ============================================================ parts
@@ -315,12 +315,13 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4, *a_done = full + 6,
            *p_ready = full + 7, *w_ready = full + 8, *qs_done = full + 9, *l_ready = full + 10, *s_done = full + 11,
-           *o_done = full + 12, *drain = full + 13;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 14);
+           *o_done = full + 12, *drain = full + 13, *o_staged = full + 14;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 16);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
     for (int i = 0; i < 14; ++i) mbar_init(full + i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(o_staged + i, 512);
     mbar_init(p_ready, 512);
     mbar_init(w_ready, 512);
     mbar_init(l_ready, 512);
@@ -337,9 +338,19 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   int step = 0, ln = 0;      // chunks; those among them whose S goes on to another
 
   if (warp == 17) {
-    // ---------------- loads
+    // ---------------- loads, and stores of whole chunks (from the v tile)
     if (lane == 0) {
       bool ok = true;
+      int out_pos[2] = {-1, -1}, out_h[2] = {0, 0};      // the chunk in each stage; pos < 0: its rows were stored directly
+      auto store = [&](int st, int x) {                  // chunk number x
+        ok = ok && wait(o_staged + st, x >> 1, SITE_ROWS + 2);
+        if (!ok || out_pos[st] < 0) return;
+#pragma unroll
+        for (int kb = 0; kb < DV / 64; ++kb)
+          tma_store_3d(&maps.o, smem_u32(sm + st * L::STAGE + 2 * L::QT) + kb * C * 128, kb * 64, out_h[st], out_pos[st]);
+        bulk_commit();
+        bulk_wait_read();
+      };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
         const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
         const int h = i % p.H;
@@ -354,13 +365,19 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
             tma_load_3d(dst + L::QT + kb * C * 128, &maps.k, kb * 64, h / G, pos, full + st);
             tma_load_3d(dst + kb * C * 128, &maps.q, kb * 64, h / G, pos, full + st);
           }
+          if (step >= 2) store(st, step - 2);
+          if (!ok) break;
 #pragma unroll
           for (int kb = 0; kb < DV / 64; ++kb)
             tma_load_3d(dst + 2 * L::QT + kb * C * 128, &maps.v, kb * 64, h, pos, full + st);
+          out_pos[st] = pos + C <= sg.end ? pos : -1;
+          out_h[st] = h;
         }
       }
+      for (int x = step > 2 ? step - 2 : 0; x < step; ++x) store(x & 1, x);
+      bulk_wait_all();
       if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i < step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+        for (int i = 0; i <= step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
     }
   } else if (warp == 16) {
     // ---------------- MMAs; a chunk's A goes ahead of Q S, which needs S complete
@@ -610,12 +627,14 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           ++ln;
         }
 
-        // the output, straight to global memory: a tile kept back for it would be loaded that much later
+        // the output: into v's tile, each thread over the words that it alone has read and the products no longer need
         ok = wait.warp(o_done, step, SITE_ROWS + 10);
         if (!ok) break;
         fence_after_sync();
         {
-          uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + r) * p.H + h) * DV + y * COLS;
+          unsigned char *tile = sm + st * L::STAGE + 2 * L::QT;
+          const bool whole_chunk = pos + C <= sg.end;
+          uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + r) * p.H + h) * DV;
           uint32_t a[COLS], b[COLS];
           if constexpr (COLS == 32) {
             tmem_ld32_issue(tm + lanes + T_O1 + y * COLS, a);
@@ -631,9 +650,14 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           float f[COLS];
 #pragma unroll
           for (int e = 0; e < COLS; ++e) f[e] = real ? fmaf(from, __uint_as_float(a[e]), __uint_as_float(b[e])) : 0.f;
-          if (pos + r < sg.end)
 #pragma unroll
-            for (int e = 0; e < COLS / 8; ++e) *reinterpret_cast<uint4 *>(orow + 8 * e) = pack8(f + 8 * e);
+          for (int e = 0; e < COLS / 8; ++e) {
+            const int cc = y * (COLS / 8) + e;
+            if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * e);
+            else if (pos + r < sg.end) *reinterpret_cast<uint4 *>(orow + 8 * cc) = pack8(f + 8 * e);
+          }
+          if (whole_chunk) fence_async_smem();
+          mbar_arrive(o_staged + st);
         }
       }
     }
@@ -702,7 +726,7 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&
-                   encode(&maps.v, p.v, p.dv, p.H, p.N)))
+                   encode(&maps.v, p.v, p.dv, p.H, p.N) && encode(&maps.o, p.o, p.dv, p.H, p.N)))
     return cudaErrorNotSupported;
   if (p.dk == 128)
     return p.dv == 128 ? launch<128, 128>(p, maps, sbase, part, whole, per, segs, s)
