@@ -172,10 +172,11 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         ok = ok && wait(w_ready + sl, j >> 1, SITE_SWEEP + 3);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t sk = smem_u32(sm + st * L::STAGE), sw = smem_u32(sm + L::W + sl * 3 * L::VT);
+        const uint64_t k = desc_mnmajor(smem_u32(sm + st * L::STAGE), C, 0, 0),
+                       v = sdesc(smem_u32(sm + L::W + sl * 3 * L::VT), L::VT, 512, 4);
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16(tm + sl * 128, desc_mnmajor(sk, C, 0, s), sdesc(sw + s * 16 * 64, L::VT, 512, 4),
+          mma_bf16(tm + sl * 128, mnmajor_step(k, s), v + (uint32_t)(s * 16 * 64 >> 4),
                    idesc_bf16(128, 3 * kSlice, 1, 1), s > 0);
         mma_commit(empty + st);
         mma_commit(done + sl);
@@ -521,8 +522,13 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
     // ---------------- MMAs
     if (lane == 0) {
       bool ok = true;
-      const uint32_t sq = smem_u32(sm + L::Q), sk = smem_u32(sm + L::K), sv = smem_u32(sm + L::V), so = smem_u32(sm + L::O),
-                     sx = smem_u32(sm + L::X), smm = smem_u32(sm + L::M);
+      const uint32_t sx = smem_u32(sm + L::X), smm = smem_u32(sm + L::M);
+      // descriptors of step 0, read K-major and MN-major
+      const uint64_t qk = desc_kmajor(smem_u32(sm + L::Q), C, 0, 0), qm = desc_mnmajor(smem_u32(sm + L::Q), C, 0, 0),
+                     kk = desc_kmajor(smem_u32(sm + L::K), C, 0, 0), km = desc_mnmajor(smem_u32(sm + L::K), C, 0, 0),
+                     vk = desc_kmajor(smem_u32(sm + L::V), C, 0, 0), ogk = desc_kmajor(smem_u32(sm + L::O), C, 0, 0),
+                     om = desc_mnmajor(smem_u32(sm + L::O), C, 0, 0), xm = desc_mnmajor(sx, DK, 0, 0),
+                     xk[2] = {desc_kmajor(sx, DK, 0, 0), desc_kmajor(sx + L::X1, DK, 0, 0)}, mk = desc_kmajor(smm, C, 0, 0), mm = desc_mnmajor(smm, C, 0, 0);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
         const uint32_t T_V = tm + t_v(it), T_Q = tm + t_q(it);
         ok = wait(ready, it, SITE_GRAD + 6);
@@ -530,13 +536,13 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s)
-          mma_bf16(tm + T_A, desc_kmajor(sk, C, 0, s), desc_kmajor(sq, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
+          mma_bf16(tm + T_A, kmajor_step<C>(kk, s), kmajor_step<C>(qk, s), idesc_bf16(128, C, 0, 0), s > 0);
         if (it > 0) ok = wait(q_free, it - 1, SITE_GRAD + 7);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DV / 16; ++s)
-          mma_bf16(T_V, desc_kmajor(sv, C, 0, s), desc_kmajor(so, C, 0, s), idesc_bf16(128, C, 0, 0), s > 0);
+          mma_bf16(T_V, kmajor_step<C>(vk, s), kmajor_step<C>(ogk, s), idesc_bf16(128, C, 0, 0), s > 0);
         mma_commit(ag_done);
         if (it > 0) ok = wait(v_free, it - 1, SITE_GRAD + 8);
 #pragma unroll
@@ -546,7 +552,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           fence_after_sync();
 #pragma unroll
           for (int s = 0; s < DV / 16; ++s)
-            mma_bf16(T_Q, desc_kmajor(so, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
+            mma_bf16(T_Q, kmajor_step<C>(ogk, s), kmajor_step<DK>(xk[x], s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
           mma_commit(x ? e_done : eh_done);
         }
@@ -558,7 +564,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           fence_after_sync();
 #pragma unroll
           for (int s = 0; s < DV / 16; ++s)
-            mma_bf16(tm + T_K, desc_kmajor(sv, C, 0, s), desc_kmajor(sx + x * L::X1, DK, 0, s), idesc_bf16(128, DK, 0, 0),
+            mma_bf16(tm + T_K, kmajor_step<C>(vk, s), kmajor_step<DK>(xk[x], s), idesc_bf16(128, DK, 0, 0),
                      x > 0 || s > 0);
         }
         if (!ok) break;
@@ -568,28 +574,28 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s)
-          mma_bf16(T_V, desc_kmajor(sk, C, 0, s), desc_mnmajor(sx, DK, 0, s), idesc_bf16(128, DV, 0, 1), s > 0);
+          mma_bf16(T_V, kmajor_step<C>(kk, s), mnmajor_step(xm, s), idesc_bf16(128, DV, 0, 1), s > 0);
         mma_commit(u_done);
         ok = wait(e_scaled, it, SITE_GRAD + 13);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16(T_Q, desc_mnmajor(smm, C, 0, s), desc_mnmajor(sk, C, 0, s), idesc_bf16(128, DK, 1, 1), 1);
+          mma_bf16(T_Q, mnmajor_step(mm, s), mnmajor_step(km, s), idesc_bf16(128, DK, 1, 1), 1);
         mma_commit(dq_done);
         ok = wait(f_scaled, it, SITE_GRAD + 14);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16(tm + T_K, desc_kmajor(smm, C, 0, s), desc_mnmajor(sq, C, 0, s), idesc_bf16(128, DK, 0, 1), 1);
+          mma_bf16(tm + T_K, kmajor_step<C>(mk, s), mnmajor_step(qm, s), idesc_bf16(128, DK, 0, 1), 1);
         mma_commit(dk_done);
         ok = wait(u_scaled, it, SITE_GRAD + 15);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          mma_bf16_ta(T_V, tm + T_A + 32 * (s >> 1) + 8 * (s & 1), desc_mnmajor(so, C, 0, s), idesc_bf16(128, DV, 0, 1), 1);
+          mma_bf16_ta(T_V, tm + T_A + 32 * (s >> 1) + 8 * (s & 1), mnmajor_step(om, s), idesc_bf16(128, DV, 0, 1), 1);
         mma_commit(dv_done);
       }
       mma_commit(drain);

@@ -32,7 +32,7 @@ struct Maps {
 // A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
 // weights; the others follow.  It goes from a segment's last chunk to its first and stops once every
 // weight that is left is 0 in fp32 (decays of 2^-151 and less): those rows are not read, their share is 0.
-constexpr int kPartsThreads = 8 * 32 + 64;      // two warpgroups, a TMA + MMA warp, a preparing warp
+constexpr int kPartsThreads = 16 * 32 + 64;     // four warpgroups, a TMA + MMA warp, a preparing warp
 constexpr int kRing = 4;
 
 struct PartsStep {
@@ -68,19 +68,19 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
            *s_free = s_done + 2, *drain = s_free + 2;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
-  if (warp == 8) tmem_alloc(tmem_sh, 512);
+  if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
       mbar_init(s_done + i, 1);
-      mbar_init(s_free + i, 256);
+      mbar_init(s_free + i, 512);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(planned + i, 1);
       mbar_init(done + i, 1);
     }
-    mbar_init(w_ready, 256);
+    mbar_init(w_ready, 512);
     mbar_init(w_free, 1);
     mbar_init(drain, 1);
     *failed = 0;
@@ -93,7 +93,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   const int G = p.H / p.Hk;
   constexpr int kCols = 256;      // TMEM columns of an item's accumulators: DV of w V's first part, DV of the others
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---------------- loads and MMAs (one thread)
     if (lane == 0) {
       int loaded = 0, n = 0;
@@ -125,18 +125,20 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
         ok = ok && wait(w_ready, step, SITE_PARTS + 3);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t sk = smem_u32(sm + st * L::STAGE), sw = smem_u32(sm + L::W), d = tm + acc * kCols;
+        const uint32_t d = tm + acc * kCols;
+        const uint64_t k = desc_mnmajor(smem_u32(sm + st * L::STAGE), C, 0, 0), v = desc_mnmajor(smem_u32(sm + L::W), C, 0, 0);
         if constexpr (DV == 128) {      // first two parts side by side (N = 256), the third into the second's sum
+          const uint64_t v2 = desc_mnmajor(smem_u32(sm + L::W + 2 * L::VT), C, 0, 0);
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
-            mma_bf16(d, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 256, 1, 1), !first || s > 0);
+            mma_bf16(d, mnmajor_step(k, s), mnmajor_step(v, s), idesc_bf16(128, 256, 1, 1), !first || s > 0);
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
-            mma_bf16(d + DV, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw + 2 * L::VT, C, 0, s), idesc_bf16(128, DV, 1, 1), 1);
+            mma_bf16(d + DV, mnmajor_step(k, s), mnmajor_step(v2, s), idesc_bf16(128, DV, 1, 1), 1);
         } else {
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
-            mma_bf16(d, desc_mnmajor(sk, C, 0, s), desc_mnmajor(sw, C, 0, s), idesc_bf16(128, 3 * DV, 1, 1), !first || s > 0);
+            mma_bf16(d, mnmajor_step(k, s), mnmajor_step(v, s), idesc_bf16(128, 3 * DV, 1, 1), !first || s > 0);
         }
         mma_commit(w_free);
         mma_commit(empty + st);
@@ -151,7 +153,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---------------- the plan
     const int nitems = sbase[p.num_seqs] * p.H;
     int step = 0;
@@ -206,8 +208,8 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
     if (ok && reserve()) publish(-1, 0, 0, false, false);
   } else {
     // ---------------- w V in three parts; at a segment's end the state to global memory
-    const int r = tid & 127, half = tid >> 7;          // row of the chunk (of the state), column half
-    constexpr int NC = DV / 16;                        // 16-byte words of the half
+    const int r = tid & 127, part_of = tid >> 7;       // row of the chunk (of the state), quarter of the columns
+    constexpr int COLS = DV / 4, NC = COLS / 8;        // columns, 16-byte words of the quarter
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int n = 0;
     for (int step = 0;; ++step) {
@@ -222,18 +224,18 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       uint4 u[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int cc = half * NC + c;
+        const int cc = part_of * NC + c;
         u[c] = real ? *reinterpret_cast<const uint4 *>(sv + row_tile_chunk(r, cc >> 3, cc & 7, C)) : make_uint4(0, 0, 0, 0);
       }
       if (!real)
-        for (int c = 0; c < DK / 16; ++c) {
-          const int cc = half * (DK / 16) + c;
+        for (int c = 0; c < DK / 32; ++c) {
+          const int cc = part_of * (DK / 32) + c;
           *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
         }
       if (step > 0 && !wait.warp(w_free, step - 1, SITE_PARTS + 7)) break;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int cc = half * NC + c;
+        const int cc = part_of * NC + c;
         const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
         float f[8];
         unpack8(u[c], f);
@@ -247,29 +249,31 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       if (!last) continue;
       if (!wait.warp(s_done + acc, n >> 1, SITE_PARTS + 8)) break;
       fence_after_sync();
-      float *out = part + ((size_t)item * DK + r) * DV + half * (DV / 2);
-#pragma unroll
-      for (int c = 0; c < DV / 64; ++c) {
-        const uint32_t col = tm + lanes + acc * kCols + half * (DV / 2) + c * 32;
+      float *out = part + ((size_t)item * DK + r) * DV + part_of * COLS;
+      const uint32_t col = tm + lanes + acc * kCols + part_of * COLS;
+      float v[COLS];
+      if constexpr (DV == 128) {
         uint32_t x[32], y[32];
-        float v[32];
         tmem_ld32_issue(col, x);
         tmem_ld32_issue(col + DV, y);
         tmem_ld32_wait(x);
         tmem_ld32_wait(y);
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
-        if constexpr (DV == 64) {
-          tmem_ld32_issue(col + 2 * DV, x);
-          tmem_ld32_wait(x);
+      } else {
+        uint32_t x[16], y[16], z[16];
+        tmem_ld16_issue(col, x);
+        tmem_ld16_issue(col + DV, y);
+        tmem_ld16_issue(col + 2 * DV, z);
+        tmem_ld16_wait(x);
+        tmem_ld16_wait(y);
+        tmem_ld16_wait(z);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(x[e]);
-        }
-        if (r < DK)
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(out + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e]));
       }
+      if (r < DK)
+#pragma unroll
+        for (int e = 0; e < COLS; e += 4) *reinterpret_cast<float4 *>(out + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
       fence_before_sync();
       mbar_arrive(s_free + acc);
       ++n;
@@ -277,7 +281,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     fence_after_sync();
     tmem_dealloc(tm, 512);
   }
