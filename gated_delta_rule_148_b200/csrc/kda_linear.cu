@@ -183,6 +183,22 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
     if (tid == 1023) carry = before + x;
     __syncthreads();
   }
+  Segment *table = const_cast<Segment *>(segment_table(sbase, p.num_seqs));
+  const int segs = carry;
+  for (int i = tid; i < segs; i += 1024) {
+    int lo = 0, hi = p.num_seqs - 1;         // the last sequence whose segments begin at or before i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sbase[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    Segment s;
+    const int e = p.cu[lo + 1];
+    s.b = lo;
+    s.begin = p.cu[lo] + (i - sbase[lo]) * tokens;
+    s.end = min(e, s.begin + tokens);
+    s.last = s.begin + tokens >= e;
+    table[i] = s;
+  }
 }
 
 // ------------------------------------------------------------------ parts
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) parts_kernel(LinearParams p, const i
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
-  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, tokens);
+  const Segment sg = locate(sbase, p.num_seqs, seg);
   if (blockIdx.y == 0) parts_block<DK, BF16, false>(p, sg, seg, h, c0, part, whole, sm, dec, tokens);
   else parts_block<DK, BF16, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec, tokens);
 }
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
-  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, tokens);
+  const Segment sg = locate(sbase, p.num_seqs, seg);
   const int hk = h / (p.H / p.Hk);
   const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16, n0 = (warp >> 2) * 32;
   float S[MT][4][4];                 // rows MT m0 .., columns n0 .. of the state
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   if (device_error_latched(p.err)) return;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
   if (seg >= sbase[p.num_seqs]) return;
-  const Segment sg = locate(p.cu, sbase, p.num_seqs, seg, C);
+  const Segment sg = locate(sbase, p.num_seqs, seg);
   const int hk = h / (p.H / p.Hk), pos0 = sg.begin, tid = threadIdx.x;
   const int warp = tid >> 5, m0 = (warp & 3) * 16, wn = warp >> 2, n0 = wn * 32;
   float *sq = sm + L::Q, *sk = sm + L::K, *sv = sm + L::V, *so = sm + L::O, *sP = sm + L::P, *sM = sm + L::M,
@@ -600,7 +616,7 @@ size_t linear_prefill_workspace(const LinearParams &p, bool bf16) {
   if (bf16) return linear_prefill_tc_workspace(p);
   const int per = segment_chunks(p.N, p.num_seqs, p.H * (p.dv / kSlice), C);
   const size_t segs = max_segments(p.N, p.num_seqs, C * per);
-  return table_bytes(p.num_seqs) + align256(segs * p.H * 4) + state_bytes(p, segs);
+  return table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4) + state_bytes(p, segs);
 }
 
 cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t s) {
@@ -611,8 +627,8 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   const size_t segs = max_segments(p.N, p.num_seqs, tokens);
   unsigned char *w = static_cast<unsigned char *>(p.ws);
   int *sbase = reinterpret_cast<int *>(w);
-  float *whole = reinterpret_cast<float *>(w + table_bytes(p.num_seqs));
-  float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs) + align256(segs * p.H * 4));
+  float *whole = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs));
+  float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4));
   cudaError_t e = launch_linear_plan(p, sbase, tokens, s);
   if (e != cudaSuccess) return e;
   e = launch_parts_chain(p, bf16, sbase, part, nullptr, whole, segs, tokens, s);
@@ -629,7 +645,7 @@ size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
   using namespace lin;
   if (bf16) return linear_backward_tc_workspace(p);
   const size_t segs = max_segments(p.N, p.num_seqs, C);
-  size_t n = table_bytes(p.num_seqs) + align256(segs * p.H * 4) + 2 * state_bytes(p, segs);
+  size_t n = table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4) + 2 * state_bytes(p, segs);
   if (p.H != p.Hk) n += 2 * align256((size_t)p.N * p.H * p.dk * 4);
   if (p.decay_head) n += align256((size_t)p.N * p.H * 4);
   return n;
@@ -652,7 +668,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
       w += align256(n);
       return reinterpret_cast<float *>(at);
     };
-    int *sbase = reinterpret_cast<int *>(take(table_bytes(p.num_seqs)));
+    int *sbase = reinterpret_cast<int *>(take(table_bytes(p.num_seqs, segs)));
     float *whole = take(segs * p.H * 4), *part = take(state_bytes(p, segs)), *rpart = take(state_bytes(p, segs));
     if (shared) {
       gq32 = take((size_t)p.N * p.H * p.dk * 4);

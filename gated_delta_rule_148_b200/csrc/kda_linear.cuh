@@ -17,29 +17,21 @@ namespace lin {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs).
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-__host__ __device__ inline size_t table_bytes(int B) { return align256((size_t)(B + 1) * 4); }
-__host__ __device__ inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
 
-// A segment's sequence, rows [begin, end) and first row of the sequence's next segment.
-struct Segment {
-  int b, begin, end;
-  bool last;         // the sequence's last segment
+// Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs), and behind them each segment's
+// sequence, rows [begin, end) and whether it is the sequence's last.
+struct alignas(16) Segment {
+  int b, begin, end, last;
 };
-__device__ __forceinline__ Segment locate(const int32_t *cu, const int *sbase, int num_seqs, int seg, int tokens) {
-  int lo = 0, hi = num_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sbase[mid] <= seg) lo = mid; else hi = mid - 1;
-  }
-  Segment s;
-  s.b = lo;
-  const int e = cu[lo + 1];
-  s.begin = cu[lo] + (seg - sbase[lo]) * tokens;
-  s.end = min(e, s.begin + tokens);
-  s.last = s.begin + tokens >= e;
-  return s;
+inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
+inline size_t table_bytes(int B, size_t segs) { return align256((size_t)(B + 1) * 4) + align256(segs * sizeof(Segment)); }
+__device__ __forceinline__ const Segment *segment_table(const int *sbase, int num_seqs) {
+  return reinterpret_cast<const Segment *>(sbase + align256((size_t)(num_seqs + 1) * 4) / 4);
+}
+__device__ __forceinline__ Segment locate(const int *sbase, int num_seqs, int seg) {
+  const int4 x = __ldg(reinterpret_cast<const int4 *>(segment_table(sbase, num_seqs) + seg));
+  return Segment{x.x, x.y, x.z, x.w};
 }
 
 __device__ __forceinline__ double shfl_up_f64(double x, int o) {

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) table_kernel(LinearParams p, const int *s
   const size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= (size_t)sbase[p.num_seqs] * p.H) return;
   const int lane = threadIdx.x & 31;
-  const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, (int)(i / p.H), C);
+  const Segment sg = lin::locate(sbase, p.num_seqs, (int)(i / p.H));
   double b[4], total;
   uint32_t word;
   scan_decays(load_decays(p, sg.begin, sg.end, (int)(i % p.H)), b, total, word);
@@ -329,7 +329,7 @@ struct GradSmem {
   static constexpr uint32_t Q = 0, K = QT, V = 2 * QT, O = V + VT, X = O + VT, M = X + 2 * X1, HL = M + C * C * 2;
   // column factors of the blocks (w, x) of 32 x 32 pairs, then the blocks' pair sums; the rest of the decays' sums
   static constexpr uint32_t PAIRS = HL + C * 8, SUMS = PAIRS + 10 * 32 * 4;
-  static constexpr uint32_t VALID = SUMS + 8 * 4, BARS = VALID + 16, END = BARS + 32 * 8;
+  static constexpr uint32_t VALID = SUMS + 10 * 4, BARS = VALID + 16, END = BARS + 32 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
@@ -382,6 +382,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
   float *extra = reinterpret_cast<float *>(sm + L::HL);     // of the blocks (w, x), w < x: after the pairs' decays are done with
   float *pairs = reinterpret_cast<float *>(sm + L::PAIRS);
   float *sums = reinterpret_cast<float *>(sm + L::SUMS);    // warps' totals: q.E, k.F
+  float *whole = sums + 8;                                  // 2^{b_C}
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 1, *x_full = full + 2,      // S, S, D, D
            *ag_done = full + 6, *eh_done = full + 7, *e_done = full + 8, *f_done = full + 9, *u_done = full + 10,
@@ -461,7 +462,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           tma_load_3d(smem_u32(sm + L::X + x * L::X1) + kb * DK * 128, map, kb * 64, 0, (2 * i + x) * DK, bar);
       };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
-        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+        const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
         const int h = i % p.H, pos = sg.begin;
         // each tile once its last reader is done (K, Q: also the row sums, before dK's product)
         if (it > 0) ok = wait(dq_done, it - 1, SITE_GRAD + 3);
@@ -607,7 +608,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
     RawDecays raw{};
     auto next = [&](int i) {
       if (i < nitems) {
-        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+        const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
         raw = load_decays(p, sg.begin, sg.end, i % p.H);
       }
     };
@@ -645,21 +646,18 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     bool ok = true;
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, C);
+      const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
       const int h = i % p.H, pos = sg.begin;
-      const bool whole_chunk = pos + C <= sg.end, in = pos + r < sg.end;
+      const int rows = sg.end - pos;
       const uint32_t T_V = tm + lanes + t_v(it), T_Q = tm + lanes + t_q(it);
-      float thr = 0.f;
-      if (y == 2 && lane < DV / 8) thr = through[(size_t)i * (DV / 8) + lane];
       ok = wait.warp(ready, it, SITE_GRAD + 18);
       if (!ok) break;
-      const bool real = (valid[w] >> lane) & 1;
       const float2 br = hl[r];
-      float fac, whole;      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
+      float fac;      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
       {
         const float2 be = hl[C - 1];
         fac = y == 0 ? ex2(br.x + br.y) : ex2((be.x - br.x) + (be.y - br.y));
-        whole = ex2(be.x + be.y);
+        if (tid == 0) *whole = ex2(be.x + be.y);
       }
       float *slot = pairs + (y * (y + 1) / 2 + w) * 32;      // of this warp's block (w <= y)
       float rowf = 0.f;
@@ -782,6 +780,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         if (y == 2) {
           ok = wait.warp(paired, it, SITE_GRAD + 23);
           if (!ok) break;
+          float thr = lane < DV / 8 ? through[(size_t)i * (DV / 8) + lane] : 0.f;
           for (int x = 0; x <= w; ++x) g += pairs[(w * (w + 1) / 2 + x) * 32 + lane];
           for (int z = w + 1; z < 4; ++z) {
             g += extra[(z * (z - 1) / 2 + w) * 32 + lane];
@@ -789,7 +788,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xFFFFFFFFu, thr, o);
-          g = fmaf(whole, thr, g);
+          g = fmaf(*whole, thr, g);
         }
         ok = wait.warp(u_done, it, SITE_GRAD + 24);
         if (!ok) break;
@@ -810,13 +809,13 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           ok = wait.warp(summed, it, SITE_GRAD + 25);
           if (!ok) break;
           fence_after_sync();
-          float rows[2];
-          tmem_ld2(tm + lanes + T_A + 16, rows);
-          g += rows[0] + rows[1];
+          float qk[2];
+          tmem_ld2(tm + lanes + T_A + 16, qk);
+          g += qk[0] + qk[1];
           for (int x = w + 1; x < 4; ++x) g += sums[x];
           for (int x = 0; x < w; ++x) g += sums[4 + x];
           // one decay per head: [H, N] for the sum that follows
-          if (in) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
+          if (r < rows) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = ((valid[w] >> lane) & 1) ? g : 0.f;
           fence_before_sync();
           mbar_arrive(tab_free);
         }
@@ -830,7 +829,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           float f[32];
           tmem_ld32(col + 32 * x, f);
           if (row32 != nullptr) {
-            if (in)
+            if (r < rows)
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4 *>(row32 + 32 * x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
@@ -838,8 +837,8 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int cc = word0 + 4 * x + c;
-              if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * c);
-              else if (in) *reinterpret_cast<uint4 *>(row + 8 * cc) = pack8(f + 8 * c);
+              if (rows >= C) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * c);
+              else if (r < rows) *reinterpret_cast<uint4 *>(row + 8 * cc) = pack8(f + 8 * c);
             }
           }
         }
@@ -857,7 +856,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       }
       fence_before_sync();
       mbar_arrive(y == 0 ? q_free : y == 1 ? k_free : v_free);
-      if (whole_chunk) fence_async_smem();
+      if (rows >= C) fence_async_smem();
       mbar_arrive(y == 0 ? dq_staged : y == 1 ? dk_staged : dv_staged);
     }
   }
@@ -881,7 +880,7 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
     w.bytes += lin::align256(n);
     return at;
   };
-  w.sbase = take(lin::table_bytes(p.num_seqs));
+  w.sbase = take(lin::table_bytes(p.num_seqs, chunks));
   w.through = take(chunks * p.H * (p.dv / 8) * 4);
   w.tables = take(chunks * p.H * sizeof(Table));
   w.s = take(chunks * p.H * (size_t)p.dk * p.dv * 4);

@@ -25,7 +25,7 @@ namespace lintc {
 enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
 
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v, o, part;
 };
 
 // ============================================================ parts
@@ -45,17 +45,16 @@ struct PartsStep {
 template <int DK, int DV>
 struct PartsSmem {
   static constexpr uint32_t KT = C * DK * 2, VT = C * DV * 2;
-  static constexpr uint32_t STAGE = KT + VT, W = 2 * STAGE;          // W: the three parts of w V
+  static constexpr uint32_t STAGE = KT + VT, W = 2 * STAGE;          // W: the three parts of w V; the state on its way out
   // DK = 64: the MMA's rows 64 .. 127 come from the bytes after the K tile and are not used
   static constexpr uint32_t WGT = W + 3 * VT, VALID = WGT + kRing * C * 4, STEPS = VALID + kRing * 16;
-  static constexpr uint32_t BARS = STEPS + kRing * 32, END = BARS + 20 * 8;
+  static constexpr uint32_t BARS = STEPS + kRing * 32, END = BARS + 24 * 8;
   static_assert(END <= 232448, "shared memory of a block");
 };
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kPartsThreads, 1)
-parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *part, float *whole,
-             int per) {
+parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *whole, int per) {
   using L = PartsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
@@ -65,8 +64,8 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   volatile PartsStep *steps = reinterpret_cast<volatile PartsStep *>(sm + L::STEPS);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + 2, *planned = full + 4,
            *done = planned + kRing, *w_ready = done + kRing, *w_free = w_ready + 1, *s_done = w_ready + 2,
-           *s_free = s_done + 2, *drain = s_free + 2;
-  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 1);
+           *s_free = s_done + 2, *drain = s_free + 2, *staged = drain + 1, *out_free = drain + 2;
+  uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(drain + 3);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 16) tmem_alloc(tmem_sh, 512);
   if (tid == 0) {
@@ -82,6 +81,8 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
     }
     mbar_init(w_ready, 512);
     mbar_init(w_free, 1);
+    mbar_init(staged, 512);
+    mbar_init(out_free, 1);
     mbar_init(drain, 1);
     *failed = 0;
   }
@@ -177,7 +178,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       return ok;
     };
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
+      const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
       // the last segment of a sequence matters to the final state only
       if (sg.last && p.final_state == nullptr) continue;
       const int chunks = (sg.end - sg.begin + C - 1) / C, h = i % p.H;
@@ -217,7 +218,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       if (!wait.warp(planned + rs, step / kRing, SITE_PARTS + 5)) break;
       const int item = steps[rs].item;
       if (item < 0) break;
-      const bool last = steps[rs].last != 0, real = (valid[4 * rs + (r >> 5)] >> (r & 31)) & 1;
+      const bool first = steps[rs].first != 0, last = steps[rs].last != 0, real = (valid[4 * rs + (r >> 5)] >> (r & 31)) & 1;
       const float w = wgt[rs * C + r];
       if (!wait.warp(full + st, step >> 1, SITE_PARTS + 6)) break;
       unsigned char *sk = sm + st * L::STAGE, *sv = sk + L::KT;
@@ -233,6 +234,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
           *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
         }
       if (step > 0 && !wait.warp(w_free, step - 1, SITE_PARTS + 7)) break;
+      if (first && n > 0 && !wait.warp(out_free, n - 1, SITE_PARTS + 9)) break;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int cc = part_of * NC + c;
@@ -249,7 +251,6 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       if (!last) continue;
       if (!wait.warp(s_done + acc, n >> 1, SITE_PARTS + 8)) break;
       fence_after_sync();
-      float *out = part + ((size_t)item * DK + r) * DV + part_of * COLS;
       const uint32_t col = tm + lanes + acc * kCols + part_of * COLS;
       float v[COLS];
       if constexpr (DV == 128) {
@@ -271,13 +272,30 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e]));
       }
-      if (r < DK)
-#pragma unroll
-        for (int e = 0; e < COLS; e += 4) *reinterpret_cast<float4 *>(out + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
       fence_before_sync();
       mbar_arrive(s_free + acc);
+      if (r < DK)      // tiles of 32 columns with the 128-byte swizzle
+#pragma unroll
+        for (int e = 0; e < COLS / 4; ++e) {
+          const int cc = part_of * (COLS / 4) + e;
+          *reinterpret_cast<float4 *>(sm + L::W + row_tile_chunk(r, cc >> 3, cc & 7, DK)) =
+              make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      fence_async_smem();
+      mbar_arrive(staged);
+      if (tid == 0) {
+        if (!wait(staged, n, SITE_PARTS + 4)) break;
+#pragma unroll
+        for (int cb = 0; cb < DV / 32; ++cb)
+          tma_store_3d(&maps.part, smem_u32(sm + L::W) + cb * DK * 128, cb * 32, 0, item * DK);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(out_free);
+      }
+      __syncwarp();
       ++n;
     }
+    if (tid == 0) bulk_wait_all();
   }
   fence_before_sync();
   __syncthreads();
@@ -339,6 +357,9 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   // P overlays A: its columns 32 x .. 32 x + 31 in 32 x .. 32 x + 15
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
   const int G = p.H / p.Hk;
+  // items' segments, loaded an item ahead
+  auto segment = [&](int i) { return i < nitems ? lin::locate(sbase, p.num_seqs, i / p.H) : Segment{}; };
+  Segment next = segment(blockIdx.x);
   int step = 0, ln = 0;      // chunks; those among them whose S goes on to another
 
   if (warp == 17) {
@@ -356,7 +377,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         bulk_wait_read();
       };
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
+        const Segment sg = next;
+        next = segment(i + gridDim.x);
         const int h = i % p.H;
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
@@ -402,7 +424,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       };
       if (blockIdx.x < nitems) issue_a(0);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-        const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
+        const Segment sg = next;
+        next = segment(i + gridDim.x);
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
           const bool last = pos + C >= sg.end, more = !last || i + (int)gridDim.x < nitems;
@@ -455,18 +478,18 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       d = load_decays(p, npos, ns.end, ni % p.H);
       npos += C;
       if (npos >= ns.end && (ni += gridDim.x) < nitems) {
-        ns = lin::locate(p.cu, sbase, p.num_seqs, ni / p.H, per * C);
+        ns = lin::locate(sbase, p.num_seqs, ni / p.H);
         npos = ns.begin;
       }
       return d;
     };
     if (ni < nitems) {
-      ns = lin::locate(p.cu, sbase, p.num_seqs, ni / p.H, per * C);
+      ns = lin::locate(sbase, p.num_seqs, ni / p.H);
       npos = ns.begin;
     }
     RawDecays raw = next();
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
+      const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
         double b[4], total;
@@ -505,7 +528,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
     float *colf = reinterpret_cast<float *>(sm + L::COLF) + (w * (w - 1) / 2 + y) * 32;      // y < w
     bool ok = true;
     for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-      const Segment sg = lin::locate(p.cu, sbase, p.num_seqs, i / p.H, per * C);
+      const Segment sg = next;
+      next = segment(i + gridDim.x);
       const int h = i % p.H;
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
@@ -534,10 +558,10 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         if (!ok) break;
         fence_after_sync();
         if (r < DK) {
-          const float *in = start + ((size_t)i * DK + r) * DV + y * COLS;
           const uint32_t col = tm + lanes + T_S + y * COLS;
           uint32_t v[COLS];
           if (first) {
+            const float *in = start + ((size_t)i * DK + r) * DV + y * COLS;
 #pragma unroll
             for (int e = 0; e < COLS; e += 4)
               *reinterpret_cast<uint4 *>(&v[e]) = __ldcs(reinterpret_cast<const uint4 *>(in + e));
@@ -696,14 +720,14 @@ template <int DK, int DV>
 cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, float *part, float *whole, int per,
                    size_t segs, cudaStream_t s) {
   const size_t items = segs * p.H;
-  if (items > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  if (items * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;      // rows of the states as a tensor map's coordinate
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
   cudaError_t e = cudaFuncSetAttribute(parts_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)PartsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(rows_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RowsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
-  if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, part, whole, per);
+  if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, whole, per);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_linear_chain(p, sbase, part, nullptr, whole, s)) != cudaSuccess) return e;
   if (grid) rows_kernel<DK, DV><<<grid, kRowsThreads, RowsSmem<DK, DV>::END, s>>>(p, maps, sbase, part, per);
@@ -715,7 +739,7 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
 size_t linear_prefill_tc_workspace(const LinearParams &p) {
   using namespace lintc;
   const size_t segs = lin::max_segments(p.N, p.num_seqs, C * segment_chunks(p.N, p.num_seqs, p.H));
-  return lin::table_bytes(p.num_seqs) + lin::align256(segs * p.H * 4) + segs * p.H * (size_t)p.dk * p.dv * 4;
+  return lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4) + segs * p.H * (size_t)p.dk * p.dv * 4;
 }
 
 cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
@@ -724,13 +748,14 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   const size_t segs = p.N > 0 ? lin::max_segments(p.N, p.num_seqs, C * per) : 0;
   unsigned char *w = static_cast<unsigned char *>(p.ws);
   int *sbase = reinterpret_cast<int *>(w);
-  float *whole = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs));
-  float *part = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs) + lin::align256(segs * p.H * 4));
+  float *whole = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs));
+  float *part = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4));
   cudaError_t e = launch_linear_plan(p, sbase, C * per, s);
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&
-                   encode(&maps.v, p.v, p.dv, p.H, p.N) && encode(&maps.o, p.o, p.dv, p.H, p.N)))
+                   encode(&maps.v, p.v, p.dv, p.H, p.N) && encode(&maps.o, p.o, p.dv, p.H, p.N) &&
+                   encode_f32(&maps.part, part, p.dv, segs * p.H * p.dk, p.dk)))
     return cudaErrorNotSupported;
   if (p.dk == 128)
     return p.dv == 128 ? launch<128, 128>(p, maps, sbase, part, whole, per, segs, s)

@@ -241,6 +241,18 @@ inline bool encode(CUtensorMap *map, const void *ptr, int d, int heads, size_t N
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// fp32 [rows][d] in boxes of `box_rows` rows and 32 columns with the 128-byte swizzle.
+inline bool encode_f32(CUtensorMap *map, const void *ptr, int d, size_t rows, int box_rows) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, 1u, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 4, (cuuint64_t)d * 4};
+  const cuuint32_t box[3] = {32u, 1u, (cuuint32_t)box_rows}, one[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(ptr), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline int sm_count() {
   static std::atomic<int> n[64];
   int dev = 0;
