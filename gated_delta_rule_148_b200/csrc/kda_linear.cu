@@ -1,5 +1,6 @@
-// Linear attention with a decay for each head: prefill and its backward pass at fp32
-// accuracy, for any element type and head dimensions (formulas in kda_linear.cuh).
+// Linear attention with a decay for each head: prefill and its backward pass for fp32 inputs (formulas in
+// kda_linear.cuh); the plan of segments, the chain and the sums over shared inputs also for bf16 ones, whose
+// products are in kda_linear_tc.cu and kda_linear_backward_tc.cu.
 //
 // Three steps, all parallel over segments and heads except the short middle one:
 //   parts    each segment's own contribution to the state,  sum_s 2^{b_end - b_s} k_s v_s^T
@@ -83,32 +84,19 @@ __device__ __forceinline__ void each(float (&acc)[MT][NT][4], F f) {
 }
 
 // ------------------------------------------------------------------ tiles
-// Rows [pos0, pos0 + C) of x [N, heads, d], columns [c0, c0 + W) of head `hd`, as fp32 with row
-// stride LD.  Rows past `end` and pads are zeros and are not read.
-template <int W, int LD, bool BF16>
+// Rows [pos0, pos0 + C) of x [N, heads, d], columns [c0, c0 + W) of head `hd`, with row stride LD.  Rows
+// past `end` and pads are zeros and are not read.
+template <int W, int LD>
 __device__ __forceinline__ void load_rows(float *dst, const void *x, int heads, int d, int hd, int c0, int pos0,
                                           int end, const uint8_t *mask) {
-  constexpr int E = BF16 ? 8 : 4, V = W / E;
+  constexpr int V = W / 4;
 #pragma unroll 4
   for (int i = threadIdx.x; i < C * V; i += kThreads) {
-    const int r = i / V, c = (i % V) * E, pos = pos0 + r;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (pos < end && (mask == nullptr || mask[pos] != 0)) {
-      const size_t at = ((size_t)pos * heads + hd) * d + c0 + c;
-      u = BF16 ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(x) + at)
-               : *reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(x) + at);
-    }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float *o = dst + r * LD + c;
-    if (BF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[2 * e] = __uint_as_float(w[e] << 16);
-        o[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    } else {
-      *reinterpret_cast<uint4 *>(o) = u;
-    }
+    const int r = i / V, c = (i % V) * 4, pos = pos0 + r;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pos < end && (mask == nullptr || mask[pos] != 0))
+      u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x) + ((size_t)pos * heads + hd) * d + c0 + c);
+    *reinterpret_cast<float4 *>(dst + r * LD + c) = u;
   }
 }
 
@@ -203,7 +191,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
 
 // ------------------------------------------------------------------ parts
 // Block: segment x head x 64 columns of d_v.  REVERSE: q, do and the rows in reverse.
-template <int DK, bool BF16, bool REVERSE>
+template <int DK, bool REVERSE>
 __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment &sg, int seg, int h, int c0,
                                             float *part, float *whole, float *sm, Decays &dec, int tokens) {
   constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
@@ -216,8 +204,8 @@ __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment
   for (int j = 0; j < chunks; ++j) {
     const int pos0 = sg.begin + (REVERSE ? chunks - 1 - j : j) * C;
     __syncthreads();
-    load_rows<DK, LK, BF16>(sk, REVERSE ? p.q : p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<kSlice, LV, BF16>(sv, REVERSE ? p.d_o : p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    load_rows<DK, LK>(sk, REVERSE ? p.q : p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV>(sv, REVERSE ? p.d_o : p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
     if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
     __syncthreads();
     const float a = dec.whole, *wgt = REVERSE ? dec.from : dec.to;
@@ -231,7 +219,7 @@ __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment
   if (!REVERSE && c0 == 0 && threadIdx.x == 0) whole[(size_t)seg * p.H + h] = keep;
 }
 
-template <int DK, bool BF16>
+template <int DK>
 __global__ void __launch_bounds__(kThreads) parts_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
                                                          float *whole, int tokens) {
   extern __shared__ float sm[];
@@ -241,8 +229,8 @@ __global__ void __launch_bounds__(kThreads) parts_kernel(LinearParams p, const i
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
-  if (blockIdx.y == 0) parts_block<DK, BF16, false>(p, sg, seg, h, c0, part, whole, sm, dec, tokens);
-  else parts_block<DK, BF16, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec, tokens);
+  if (blockIdx.y == 0) parts_block<DK, false>(p, sg, seg, h, c0, part, whole, sm, dec, tokens);
+  else parts_block<DK, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec, tokens);
 }
 template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + kSlice + 4) * 4; }
 
@@ -308,9 +296,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
   for (int j = 0; j < chunks; ++j) {
     const int pos0 = sg.begin + j * C;
     __syncthreads();
-    load_rows<DK, LK, false>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<DK, LK, false>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<kSlice, LV, false>(sv, p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    load_rows<DK, LK>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<DK, LK>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV>(sv, p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
     each(S, [&](int r, int n, float &x) { sS[(m0 * MT + r) * LV + n0 + n] = x; });
     if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
     __syncthreads();
@@ -353,7 +341,7 @@ template <int DK> constexpr size_t rows_smem() {
 //                + sum_{t>=u>s} (q_t.k_s)(do_t.v_s) 2^{b_t-b_s}
 // (what passes over row u: to later rows, from earlier rows, through the chunk, inside it).
 // S and D are taken in halves of 64 rows, one after the other through the same tile.
-template <int DK, int DV, bool BF16>
+template <int DK, int DV>
 struct GradSmem {
   static constexpr int LK = DK + 4, LV = DV + 4, LP = C + 4;
   static constexpr int Q = 0, K = Q + C * LK, V = K + C * LK, O = V + C * LV;
@@ -377,10 +365,10 @@ __device__ __forceinline__ void row_sums(float (&acc)[1][NT][4], float *part, in
   }
 }
 
-template <int DK, int DV, bool BF16>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const int *sbase, const float *start,
                                                         const float *dend, float *gq32, float *gk32, float *gla) {
-  using L = GradSmem<DK, DV, BF16>;
+  using L = GradSmem<DK, DV>;
   constexpr int LK = L::LK, LV = L::LV, LP = L::LP, HALVES = DK / 64, NV = DV / 16;
   extern __shared__ float sm[];
   __shared__ Decays dec;
@@ -393,10 +381,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   const int warp = tid >> 5, m0 = (warp & 3) * 16, wn = warp >> 2, n0 = wn * 32;
   float *sq = sm + L::Q, *sk = sm + L::K, *sv = sm + L::V, *so = sm + L::O, *sP = sm + L::P, *sM = sm + L::M,
         *sS = sm + L::S;
-  load_rows<DK, LK, BF16>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-  load_rows<DK, LK, BF16>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-  load_rows<DV, LV, BF16>(sv, p.v, p.H, DV, h, 0, pos0, sg.end, p.mask);
-  load_rows<DV, LV, BF16>(so, p.d_o, p.H, DV, h, 0, pos0, sg.end, p.mask);
+  load_rows<DK, LK>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+  load_rows<DK, LK>(sk, p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+  load_rows<DV, LV>(sv, p.v, p.H, DV, h, 0, pos0, sg.end, p.mask);
+  load_rows<DV, LV>(so, p.d_o, p.H, DV, h, 0, pos0, sg.end, p.mask);
   if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
   if (tid < 2 * C) r_part[tid] = k_part[tid] = 0.f;
   __syncthreads();
@@ -462,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
       const int pos = pos0 + m0 + r;
       if (pos >= sg.end) return;
       if (gq32) gq32[((size_t)pos * p.H + h) * DK + k0 + n0 + n] = x;
-      else store_elem<BF16>(p.gq, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
+      else store_elem<false>(p.gq, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
     });
     __syncthreads();
     for (int i = tid; i < 64 * DV / 4; i += kThreads) {
@@ -481,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
       const int pos = pos0 + m0 + r;
       if (pos >= sg.end) return;
       if (gk32) gk32[((size_t)pos * p.H + h) * DK + k0 + n0 + n] = x;
-      else store_elem<BF16>(p.gk, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
+      else store_elem<false>(p.gk, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
     });
     gemm3<1, NV, 64>(av, [&](int r, int k) { return sk[(m0 + r) * LK + k0 + k]; },
                      [&](int k, int n) { return sS[k * LV + wn * (DV / 2) + n]; });
@@ -491,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
                   [&](int k, int n) { return so[k * LV + wn * (DV / 2) + n]; });
   each(av, [&](int r, int n, float &x) {
     const int pos = pos0 + m0 + r;
-    if (pos < sg.end) store_elem<BF16>(p.gv, ((size_t)pos * p.H + h) * DV + wn * (DV / 2) + n, x);
+    if (pos < sg.end) store_elem<false>(p.gv, ((size_t)pos * p.H + h) * DV + wn * (DV / 2) + n, x);
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(0xFFFFFFFFu, through, o);
@@ -562,39 +550,51 @@ int segment_chunks(int N, int B, int blocks_per_chunk, int chunk) {
 }
 size_t state_bytes(const LinearParams &p, size_t segs) { return align256(segs * p.H * (size_t)p.dk * p.dv * 4); }
 
-cudaError_t launch_parts_chain(const LinearParams &p, bool bf16, const int *sbase, float *part, float *rpart,
-                               float *whole, size_t segs, int tokens, cudaStream_t s) {
+template <int DK>
+cudaError_t launch_parts(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole, size_t segs,
+                         int tokens, cudaStream_t s) {
   const size_t blocks = segs * p.H * (p.dv / kSlice);
-  if (blocks > 0x7FFFFFFFull || (size_t)p.num_seqs * p.H > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  auto kern = p.dk == 128 ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
-                          : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
-  const size_t smem = p.dk == 128 ? parts_smem<128>() : parts_smem<64>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<parts_kernel<DK>>(parts_smem<DK>());
   if (e != cudaSuccess) return e;
-  if (blocks) kern<<<dim3((unsigned)blocks, rpart ? 2 : 1), kThreads, smem, s>>>(p, sbase, part, rpart, whole, tokens);
-  e = cudaGetLastError();
+  if (blocks)
+    parts_kernel<DK><<<dim3((unsigned)blocks, rpart ? 2 : 1), kThreads, parts_smem<DK>(), s>>>(p, sbase, part, rpart,
+                                                                                            whole, tokens);
+  return cudaGetLastError();
+}
+cudaError_t launch_parts_chain(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole,
+                               size_t segs, int tokens, cudaStream_t s) {
+  const cudaError_t e = p.dk == 128 ? launch_parts<128>(p, sbase, part, rpart, whole, segs, tokens, s)
+                                    : launch_parts<64>(p, sbase, part, rpart, whole, segs, tokens, s);
   if (e != cudaSuccess) return e;
   return launch_linear_chain(p, sbase, part, rpart, whole, s);
 }
 
-template <int DK, int DV, bool BF16>
-cudaError_t launch_grad(const LinearParams &p, const int *sbase, const float *start, const float *dend, float *gq32,
-                        float *gk32, float *gla, size_t segs, cudaStream_t s) {
-  auto kern = grad_kernel<DK, DV, BF16>;
-  const size_t smem = (size_t)GradSmem<DK, DV, BF16>::END * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int DK>
+cudaError_t launch_rows(const LinearParams &p, const int *sbase, const float *start, size_t segs, int tokens,
+                        cudaStream_t s) {
+  const cudaError_t e = allow_smem<rows_kernel<DK>>(rows_smem<DK>());
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(segs * p.H), kThreads, smem, s>>>(p, sbase, start, dend, gq32, gk32, gla);
+  rows_kernel<DK><<<(unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, rows_smem<DK>(), s>>>(p, sbase, start, tokens);
   return cudaGetLastError();
 }
-template <bool BF16>
+
+template <int DK, int DV>
+cudaError_t launch_grad(const LinearParams &p, const int *sbase, const float *start, const float *dend, float *gq32,
+                        float *gk32, float *gla, size_t segs, cudaStream_t s) {
+  constexpr size_t smem = (size_t)GradSmem<DK, DV>::END * 4;
+  const cudaError_t e = allow_smem<grad_kernel<DK, DV>>(smem);
+  if (e != cudaSuccess) return e;
+  grad_kernel<DK, DV><<<(unsigned)(segs * p.H), kThreads, smem, s>>>(p, sbase, start, dend, gq32, gk32, gla);
+  return cudaGetLastError();
+}
 cudaError_t launch_grad_dims(const LinearParams &p, const int *sbase, const float *start, const float *dend,
                              float *gq32, float *gk32, float *gla, size_t segs, cudaStream_t s) {
   if (p.dk == 128)
-    return p.dv == 128 ? launch_grad<128, 128, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
-                       : launch_grad<128, 64, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
-  return p.dv == 128 ? launch_grad<64, 128, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
-                     : launch_grad<64, 64, BF16>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
+    return p.dv == 128 ? launch_grad<128, 128>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
+                       : launch_grad<128, 64>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
+  return p.dv == 128 ? launch_grad<64, 128>(p, sbase, start, dend, gq32, gk32, gla, segs, s)
+                     : launch_grad<64, 64>(p, sbase, start, dend, gq32, gk32, gla, segs, s);
 }
 
 }  // namespace lin
@@ -631,14 +631,9 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4));
   cudaError_t e = launch_linear_plan(p, sbase, tokens, s);
   if (e != cudaSuccess) return e;
-  e = launch_parts_chain(p, bf16, sbase, part, nullptr, whole, segs, tokens, s);
+  e = launch_parts_chain(p, sbase, part, nullptr, whole, segs, tokens, s);
   if (e != cudaSuccess || p.N == 0) return e;
-  auto kern = p.dk == 128 ? rows_kernel<128> : rows_kernel<64>;
-  const size_t smem = p.dk == 128 ? rows_smem<128>() : rows_smem<64>();
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, smem, s>>>(p, sbase, part, tokens);
-  return cudaGetLastError();
+  return p.dk == 128 ? launch_rows<128>(p, sbase, part, segs, tokens, s) : launch_rows<64>(p, sbase, part, segs, tokens, s);
 }
 
 size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
@@ -676,9 +671,9 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
     }
     if (p.decay_head) gla = take((size_t)p.N * p.H * 4);
     if ((e = launch_linear_plan(p, sbase, C, s)) != cudaSuccess) return e;
-    e = launch_parts_chain(p, bf16, sbase, part, rpart, whole, segs, C, s);
+    e = launch_parts_chain(p, sbase, part, rpart, whole, segs, C, s);
     if (e != cudaSuccess) return e;
-    if (p.N > 0) e = launch_grad_dims<false>(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
+    if (p.N > 0) e = launch_grad_dims(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
     if (e != cudaSuccess) return e;
   }
   if (p.N > 0) {

@@ -10,6 +10,8 @@
 // 2^-400 counts as 2^-400: both are 0 against any fp32 value, and the sum keeps its digits.
 #pragma once
 
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -32,6 +34,20 @@ __device__ __forceinline__ const Segment *segment_table(const int *sbase, int nu
 __device__ __forceinline__ Segment locate(const int *sbase, int num_seqs, int seg) {
   const int4 x = __ldg(reinterpret_cast<const int4 *>(segment_table(sbase, num_seqs) + seg));
   return Segment{x.x, x.y, x.z, x.w};
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory: once per device, since the call costs as much as a launch.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 __device__ __forceinline__ double shfl_up_f64(double x, int o) {

@@ -900,24 +900,22 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   float *through = reinterpret_cast<float *>(ws + w.through);
   const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice);
   if (sweeps > 0x7FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  auto fwd = sweep_kernel<DK, DV, false>, rev = sweep_kernel<DK, DV, true>;
-  auto grad = grad_kernel<DK, DV>;
   constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END, grad_smem = GradSmem<DK, DV>::END;
-  cudaError_t e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rev, cudaFuncAttributeMaxDynamicSharedMemorySize, rev_smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem);
+  cudaError_t e = lin::allow_smem<sweep_kernel<DK, DV, false>>(fwd_smem);
+  if (e == cudaSuccess) e = lin::allow_smem<sweep_kernel<DK, DV, true>>(rev_smem);
+  if (e == cudaSuccess) e = lin::allow_smem<grad_kernel<DK, DV>>(grad_smem);
   if (e != cudaSuccess) return e;
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
   if (items > 0) table_kernel<<<(unsigned)((items + 7) / 8), 256, 0, s>>>(p, sbase, tables);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  fwd<<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, tables, nullptr);
+  sweep_kernel<DK, DV, false><<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, tables, nullptr);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  rev<<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, tables, through);
+  sweep_kernel<DK, DV, true><<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, tables, through);
   if ((e = cudaGetLastError()) != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
-  grad<<<grid, kGradThreads, grad_smem, s>>>(p, mg, sbase, through,
+  grad_kernel<DK, DV><<<grid, kGradThreads, grad_smem, s>>>(p, mg, sbase, through,
                                              shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr,
                                              shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr, gla);
   return cudaGetLastError();

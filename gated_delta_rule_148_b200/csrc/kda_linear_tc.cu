@@ -722,10 +722,8 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
   const size_t items = segs * p.H;
   if (items * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;      // rows of the states as a tensor map's coordinate
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
-  cudaError_t e = cudaFuncSetAttribute(parts_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)PartsSmem<DK, DV>::END);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(rows_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RowsSmem<DK, DV>::END);
+  cudaError_t e = lin::allow_smem<parts_kernel<DK, DV>>(PartsSmem<DK, DV>::END);
+  if (e == cudaSuccess) e = lin::allow_smem<rows_kernel<DK, DV>>(RowsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
   if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, whole, per);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

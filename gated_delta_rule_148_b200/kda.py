@@ -199,7 +199,7 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream) -> ctypes.c_void_p:
@@ -207,8 +207,16 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, device: int) -> int:
+    """The stream's handle; the device's current stream without an object made for it."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _check_cuda(name: str, t: Optional[torch.Tensor], dtype=None, shape=None):
     if t is None:
+        return
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the operator has no CPU path)")
@@ -496,28 +504,28 @@ def _linear_common(a, q, k, v, log_alpha, rows: int, same_device=()):
     _check_cuda("q", q, shape=(rows, Hk, dk))
     _check_cuda("k", k, q.dtype, (rows, Hk, dk))
     _check_cuda("v", v, q.dtype, (rows, H, dv))
-    head = decay_layout(log_alpha) == KDA_DECAY_HEAD
-    _check_cuda("log_alpha", log_alpha, torch.float32, (H,) if head else (rows, H))
+    a.decay = decay_layout(log_alpha)
+    _check_cuda("log_alpha", log_alpha, torch.float32, (H,) if a.decay == KDA_DECAY_HEAD else (rows, H))
     a.dtype = _dtype_code(q)
     a.H, a.Hk, a.dk, a.dv = H, Hk, dk, dv
-    a.q, a.k, a.v, a.log_alpha = _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha)
-    a.decay = decay_layout(log_alpha)
+    a.q, a.k, a.v, a.log_alpha = q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr()
     _check_device(q, k, v, log_alpha, *same_device)
     return H, Hk, dk, dv
 
 
 def _check_device(first, *others):
     """All tensors on one device, and that device current: a launch goes to the current one."""
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    if first.device.index != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _workspace(a, name: str, workspace, device):
     """The call's workspace: the caller's, or one of the size that the library states."""
-    nbytes = int(getattr(load(), name + "_workspace_size")(ctypes.byref(a)))
+    nbytes = int(getattr(_lib or load(), name + "_workspace_size")(ctypes.byref(a)))
     if workspace is None:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     a.workspace = _ptr(workspace)
@@ -546,16 +554,18 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha:
     _check_cuda("pad_mask", pad_mask, torch.uint8, (N,))
     _check_cuda("init_state", init_state, torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-    _check_cuda("o", o, q.dtype, (N, H, dv))
-    if final_state is None and want_final_state:
+        o = torch.empty_like(v)
+    else:
+        _check_cuda("o", o, q.dtype, (N, H, dv))
+    if final_state is not None:
+        _check_cuda("final_state", final_state, torch.float32, (B, H, dk, dv))
+    elif want_final_state:
         final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
-    _check_cuda("final_state", final_state, torch.float32, (B, H, dk, dv))
     a.num_seqs, a.total_tokens = B, N
     a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
     a.o, a.final_state = _ptr(o), _ptr(final_state)
     workspace = _workspace(a, "kda_linear_prefill", workspace, q.device)
-    st = load().kda_linear_prefill(ctypes.byref(a), _stream_handle(stream))
+    st = (_lib or load()).kda_linear_prefill(ctypes.byref(a), _raw_stream(stream, q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill")
     return o, final_state
@@ -583,11 +593,12 @@ def linear_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: 
     _check_cuda("mask", mask, torch.uint8, (B,))
     _check_cuda("state", state, torch.float32, (B, H, dk, dv))
     if o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
-    _check_cuda("o", o, q.dtype, (B, H, dv))
+        o = torch.empty_like(v)
+    else:
+        _check_cuda("o", o, q.dtype, (B, H, dv))
     a.B = B
     a.mask, a.state, a.o = _ptr(mask), _ptr(state), _ptr(o)
-    st = load().kda_linear_decode(ctypes.byref(a), _stream_handle(stream))
+    st = (_lib or load()).kda_linear_decode(ctypes.byref(a), _raw_stream(stream, q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_decode")
     return o
@@ -617,7 +628,7 @@ def linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_s
     a.grad_q, a.grad_k, a.grad_v = _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"])
     a.grad_log_alpha, a.grad_init_state = _ptr(g["dlog_alpha"]), _ptr(g["dS0"])
     workspace = _workspace(a, "kda_linear_prefill_backward", workspace, q.device)
-    st = load().kda_linear_prefill_backward(ctypes.byref(a), _stream_handle(stream))
+    st = (_lib or load()).kda_linear_prefill_backward(ctypes.byref(a), _raw_stream(stream, q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill_backward")
     return g
@@ -635,18 +646,16 @@ def _rms_norm(x, weight, residual, eps, out_dtype, group, y, scale, residual_out
     _check_cuda("x", x)
     _check_cuda("weight", weight, torch.float32, (D,))
     _check_cuda("residual", residual, x.dtype, x.shape)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    if residual is None and residual_out is not None:
+    if residual_out is None:
+        residual_out = None if residual is None else torch.empty_like(x)
+    elif residual is None:
         raise ValueError("residual_out needs residual")
-    _check_cuda("residual_out", residual_out, x.dtype, x.shape)
+    else:
+        _check_cuda("residual_out", residual_out, x.dtype, x.shape)
     _check_device(x, weight, residual, y, scale, residual_out)
-    a = RmsNormArgs()
-    a.dtype, a.out_dtype = _dtype_code(x), out_dtype
-    a.rows, a.D, a.eps, a.group = rows, D, float(eps), int(group)
-    a.x, a.residual, a.weight = _ptr(x), _ptr(residual), _ptr(weight)
-    a.y, a.scale, a.residual_out = _ptr(y), _ptr(scale), _ptr(residual_out)
-    st = load().kda_rms_norm(ctypes.byref(a), _stream_handle(stream))
+    a = RmsNormArgs(_dtype_code(x), out_dtype, rows, D, _ptr(x), _ptr(residual), _ptr(weight), eps, group,
+                    _ptr(y), _ptr(scale), _ptr(residual_out))
+    st = (_lib or load()).kda_rms_norm(ctypes.byref(a), _raw_stream(stream, x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm")
     return residual_out
@@ -661,7 +670,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     residual itself."""
     if y is None:
         y = torch.empty_like(x)
-    _check_cuda("y", y, x.dtype, x.shape)
+    else:
+        _check_cuda("y", y, x.dtype, x.shape)
     return y, _rms_norm(x, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out, stream)
 
 
@@ -684,11 +694,13 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         raise ValueError("group must be 0, 32, 64 or 128")
     n = -(-D // group) if group else 1
     if y is None:
-        y = torch.empty(x.shape, dtype=tdt, device=x.device)
+        y = torch.empty_like(x, dtype=tdt)
+    else:
+        _check_cuda("y", y, tdt, x.shape)
     if scale is None:
         scale = torch.empty((*x.shape[:-1], n), dtype=torch.float32, device=x.device)
-    _check_cuda("y", y, tdt, x.shape)
-    _check_cuda("scale", scale, torch.float32, (*x.shape[:-1], n))
+    else:
+        _check_cuda("scale", scale, torch.float32, (*x.shape[:-1], n))
     r = _rms_norm(x, weight, residual, eps, code, group, y, scale, residual_out, stream)
     return y, scale, r
 
@@ -709,7 +721,8 @@ def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: t
     _check_cuda("grad_residual", grad_residual, x.dtype, x.shape)
     if grad_x is None:
         grad_x = torch.empty_like(x)
-    _check_cuda("grad_x", grad_x, x.dtype, x.shape)
+    else:
+        _check_cuda("grad_x", grad_x, x.dtype, x.shape)
     _check_device(x, weight, grad_y, grad_residual, grad_x, workspace)
     grad_weight = torch.empty(D, dtype=torch.float32, device=x.device) if want_grad_weight else None
     a = RmsNormBackwardArgs()
@@ -718,7 +731,7 @@ def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: t
     a.grad_x, a.grad_weight = _ptr(grad_x), _ptr(grad_weight)
     if want_grad_weight:
         workspace = _workspace(a, "kda_rms_norm_backward", workspace, x.device)
-    st = load().kda_rms_norm_backward(ctypes.byref(a), _stream_handle(stream))
+    st = (_lib or load()).kda_rms_norm_backward(ctypes.byref(a), _raw_stream(stream, x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm_backward")
     return grad_x, grad_weight
