@@ -337,7 +337,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   float *whole = reinterpret_cast<float *>(sm + L::WHOLE);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *ready = full + 2, *empty = full + 4, *a_done = full + 6,
            *p_ready = full + 7, *w_ready = full + 8, *qs_done = full + 9, *l_ready = full + 10, *s_done = full + 11,
-           *o_done = full + 12, *drain = full + 13, *o_staged = full + 14;
+           *drain = full + 13, *o_staged = full + 14;
   uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(full + 16);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_sh + 1);
   if (warp == 16) tmem_alloc(tmem_sh, 512);
@@ -406,13 +406,13 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         for (int i = 0; i <= step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
     }
   } else if (warp == 16) {
-    // ---------------- MMAs; a chunk's A goes ahead of Q S, which needs S complete
+    // ---------------- MMAs: P V, Q S, the next chunk's A, then S's update, so that the next P is on its way meanwhile
     if (lane == 0) {
       bool ok = true;
       const uint32_t sw = smem_u32(sm + L::W);
       const uint32_t stage[2] = {smem_u32(sm), smem_u32(sm + L::STAGE)};
       auto issue_a = [&](int x) {            // chunk number x
-        ok = ok && wait(ready + (x & 1), x >> 1, SITE_ROWS + 1);
+        ok = ok && wait(full + (x & 1), x >> 1, SITE_ROWS + 1);
         if (!ok) return;
         fence_after_sync();
         const uint32_t sq = x & 1 ? stage[1] : stage[0];
@@ -433,23 +433,25 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           const uint64_t q = desc_kmajor(sq, C, 0, 0), w = desc_mnmajor(sw, DK, 0, 0), k = desc_mnmajor(sk, C, 0, 0),
                          v = desc_mnmajor(sv, C, 0, 0), hi = desc_mnmajor(sw, C, 0, 0),
                          lo = desc_mnmajor(L::kLoInQ ? sq : smem_u32(sm + L::LO), C, 0, 0);
-          ok = wait(w_ready, step, SITE_ROWS + 3);
-          if (!ok) break;
-          fence_after_sync();
-#pragma unroll
-          for (int s = 0; s < DK / 16; ++s)
-            mma_bf16(tm + T_O1, kmajor_step<C>(q, s), mnmajor_step(w, s), idesc_bf16(128, DV, 0, 1), s > 0);
-          mma_commit(qs_done);
-          ok = wait(p_ready, step, SITE_ROWS + 4);
+          ok = wait(p_ready, step, SITE_ROWS + 3);
           if (!ok) break;
           fence_after_sync();
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
             mma_bf16_ta(tm + T_O2, tm + T_A + 32 * (s >> 1) + 8 * (s & 1), mnmajor_step(v, s), idesc_bf16(128, DV, 0, 1),
                         s > 0);
-          mma_commit(o_done);
+          ok = wait(w_ready, step, SITE_ROWS + 4);
+          if (!ok) break;
+          fence_after_sync();
+#pragma unroll
+          for (int s = 0; s < DK / 16; ++s)
+            mma_bf16(tm + T_O1, kmajor_step<C>(q, s), mnmajor_step(w, s), idesc_bf16(128, DV, 0, 1), s > 0);
+          mma_commit(qs_done);
+          // (if it is there: else S's update, which the loads wait for, goes first)
+          const bool early = more && Waits::test(full + (st ^ 1), ((step + 1) >> 1) & 1);
+          if (early) issue_a(step + 1);
           if (!last) {                       // S += K^T (w V)
-            ok = wait(l_ready, ln++, SITE_ROWS + 5);
+            ok = ok && wait(l_ready, ln++, SITE_ROWS + 5);
             if (!ok) break;
             fence_after_sync();
 #pragma unroll
@@ -461,14 +463,14 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
             mma_commit(s_done);
           }
           mma_commit(empty + st);
-          if (more) issue_a(step + 1);
+          if (more && !early) issue_a(step + 1);
         }
       }
       mma_commit(drain);
       mbar_wait(drain, 0, p.wait_cycles);
     }
   } else if (warp == 18) {
-    // ---------------- decays and rows to clear; the next chunk's decays are loaded a chunk ahead
+    // ---------------- decays; the next chunk's are loaded a chunk ahead
     bool ok = true;
     int ni = blockIdx.x, npos = 0;           // the chunk whose decays are on their way
     Segment ns{};
@@ -496,7 +498,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         uint32_t word;
         const RawDecays now = raw;
         raw = next();
-        const bool clean = scan_decays(now, b, total, word);
+        scan_decays(now, b, total, word);
         // the stage's MMAs are done, and with them the readers of its tables
         if (step >= 2) ok = wait(empty + st, (step >> 1) - 1, SITE_ROWS + 6);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -508,14 +510,6 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           hl[st * C + 4 * lane + e] = make_float2(hi, (float)(b[e] - (double)hi));
         }
         if (lane == 0) whole[st] = ex2((float)total);
-        __syncwarp();
-        ok = wait(full + st, step >> 1, SITE_ROWS + 7);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!clean && ok) {
-          clear_rows<DK>(sm + st * L::STAGE + L::QT, valid + 4 * st);
-          clear_rows<DV>(sm + st * L::STAGE + 2 * L::QT, valid + 4 * st);
-          fence_async_smem();
-        }
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(ready + st);
       }
@@ -534,11 +528,26 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
         const bool first = pos == sg.begin, last = pos + C >= sg.end;
-        ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 8);
+        ok = wait.warp(ready + st, step >> 1, SITE_ROWS + 8) && wait.warp(full + st, step >> 1, SITE_ROWS + 7);
         if (!ok) break;
         const float2 *d = hl + st * C;
         const float2 bt = d[r];
+        const uint32_t cols = valid[4 * st + y];         // P's columns that are real rows
         const bool real = (valid[4 * st + w] >> lane) & 1;
+        unsigned char *tile_k = sm + st * L::STAGE + L::QT, *tile_v = tile_k + L::QT;
+        if (!real) {      // a pad or a row of the next sequence: k and v must not reach S nor o (A's column is masked)
+#pragma unroll
+          for (int e = 0; e < DK / 32; ++e) {
+            const int cc = y * (DK / 32) + e;
+            *reinterpret_cast<uint4 *>(tile_k + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < COLS / 8; ++e) {
+            const int cc = y * (COLS / 8) + e;
+            *reinterpret_cast<uint4 *>(tile_v + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
         const float keep = whole[st], from = ex2(bt.x + bt.y);
         float to, rowf = 0.f;
         {
@@ -551,6 +560,54 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           colf[lane] = ex2((ref.x - bs.x) + (ref.y - bs.y));
         }
         __syncwarp();
+
+        // P's columns 32 y .. 32 y + 31
+        ok = wait.warp(a_done, step, SITE_ROWS + 9);
+        if (!ok) break;
+        fence_after_sync();
+        {
+          const uint32_t col = tm + lanes + T_A + 32 * y;
+          float g[16];
+          if (y > w) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[e] = 0.f;
+          } else {
+            uint32_t a[32];
+            auto mask = [&](uint32_t (&x)[32]) {
+              if (cols != 0xFFFFFFFFu)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = (cols >> e) & 1 ? x[e] : 0u;
+            };
+            tmem_ld32_issue(col, a);
+            if (y < w) {
+              tmem_ld32_wait(a);
+              mask(a);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(colf + e);
+                g[e / 2] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e]) * (rowf * c.x), __uint_as_float(a[e + 1]) * (rowf * c.y)));
+                g[e / 2 + 1] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e + 2]) * (rowf * c.z), __uint_as_float(a[e + 3]) * (rowf * c.w)));
+              }
+            } else {                         // the diagonal: each pair by itself
+              float f[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 bs = d[32 * y + e];
+                f[e] = ex2((bt.x - bs.x) + (bt.y - bs.y));
+              }
+              tmem_ld32_wait(a);
+              mask(a);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) f[e] = e <= lane ? __uint_as_float(a[e]) * f[e] : 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(pack_bf16x2(f[2 * e], f[2 * e + 1]));
+            }
+          }
+          tmem_st16(col, g);
+          tmem_st_wait();
+          fence_before_sync();
+          mbar_arrive(p_ready);
+        }
 
         // S as an operand; S <- 2^{b_C} S
         if (!first) ok = wait.warp(s_done, ln - 1, SITE_ROWS + 12);
@@ -592,50 +649,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         fence_before_sync();
         mbar_arrive(w_ready);
 
-        // P's columns 32 y .. 32 y + 31
-        ok = wait.warp(a_done, step, SITE_ROWS + 9);
-        if (!ok) break;
-        fence_after_sync();
-        {
-          const uint32_t col = tm + lanes + T_A + 32 * y;
-          float g[16];
-          if (y > w) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) g[e] = 0.f;
-          } else {
-            uint32_t a[32];
-            tmem_ld32_issue(col, a);
-            if (y < w) {
-              tmem_ld32_wait(a);
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(colf + e);
-                g[e / 2] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e]) * (rowf * c.x), __uint_as_float(a[e + 1]) * (rowf * c.y)));
-                g[e / 2 + 1] = __uint_as_float(pack_bf16x2(__uint_as_float(a[e + 2]) * (rowf * c.z), __uint_as_float(a[e + 3]) * (rowf * c.w)));
-              }
-            } else {                         // the diagonal: each pair by itself
-              float f[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float2 bs = d[32 * y + e];
-                f[e] = ex2((bt.x - bs.x) + (bt.y - bs.y));
-              }
-              tmem_ld32_wait(a);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] = e <= lane ? __uint_as_float(a[e]) * f[e] : 0.f;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) g[e] = __uint_as_float(pack_bf16x2(f[2 * e], f[2 * e + 1]));
-            }
-          }
-          tmem_st16(col, g);
-          tmem_st_wait();
-          fence_before_sync();
-          mbar_arrive(p_ready);
-        }
-
         // the two parts of w V, once Q S is done
         if (!last) {
-          const unsigned char *sv = sm + st * L::STAGE + 2 * L::QT;
           unsigned char *slo = L::kLoInQ ? sm + st * L::STAGE : sm + L::LO;
           ok = wait.warp(qs_done, step, SITE_ROWS + 14);
           if (!ok) break;
@@ -644,7 +659,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
             const int cc = y * (COLS / 8) + e;
             const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
             float f[8];
-            unpack8(*reinterpret_cast<const uint4 *>(sv + at), f);
+            unpack8(*reinterpret_cast<const uint4 *>(tile_v + at), f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] *= to;
             *reinterpret_cast<uint4 *>(sm + L::W + at) = take_bf16(f);
@@ -656,11 +671,10 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         }
 
         // the output: into v's tile, each thread over the words that it alone has read and the products no longer need
-        ok = wait.warp(o_done, step, SITE_ROWS + 10);
+        ok = wait.warp(qs_done, step, SITE_ROWS + 10);
         if (!ok) break;
         fence_after_sync();
         {
-          unsigned char *tile = sm + st * L::STAGE + 2 * L::QT;
           const bool whole_chunk = pos + C <= sg.end;
           uint16_t *orow = reinterpret_cast<uint16_t *>(p.o) + ((size_t)(pos + r) * p.H + h) * DV;
           uint32_t a[COLS], b[COLS];
@@ -677,11 +691,14 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           }
           float f[COLS];
 #pragma unroll
-          for (int e = 0; e < COLS; ++e) f[e] = real ? fmaf(from, __uint_as_float(a[e]), __uint_as_float(b[e])) : 0.f;
+          for (int e = 0; e < COLS; ++e) f[e] = fmaf(from, __uint_as_float(a[e]), __uint_as_float(b[e]));
+          if (!real)
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) f[e] = 0.f;
 #pragma unroll
           for (int e = 0; e < COLS / 8; ++e) {
             const int cc = y * (COLS / 8) + e;
-            if (whole_chunk) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * e);
+            if (whole_chunk) *reinterpret_cast<uint4 *>(tile_v + row_tile_chunk(r, cc >> 3, cc & 7, C)) = pack8(f + 8 * e);
             else if (pos + r < sg.end) *reinterpret_cast<uint4 *>(orow + 8 * cc) = pack8(f + 8 * e);
           }
           if (whole_chunk) fence_async_smem();

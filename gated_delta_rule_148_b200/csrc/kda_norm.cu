@@ -10,11 +10,15 @@
 //     dw = sum over rows of dy * r * c
 //
 // All of it is bound by HBM: every tensor is read once and written once.  A row belongs to
-// TPR threads (16 lanes of a warp up to 1024 threads), each with VPT vectors of 8 columns
+// TPR threads (8 lanes of a warp up to 1024 threads), each with VPT vectors of 8 columns
 // that stay in registers between the statistic and the output, so there is one pass over
 // the data and the only exchanges are the row sums (shuffles, and one word per warp through
-// shared memory when a row spans warps).  Narrow rows (up to 256 columns) are taken
-// four at a time, so that a thread has four loads in flight instead of one.
+// shared memory when a row spans warps).  What decides the rate is how many bytes a thread has
+// in flight before its first exchange: four 16-byte loads of a tensor (VPT U = 4) in 64
+// registers, so that four blocks of 256 threads share an SM, reach 5.2 - 6.4 TB/s of bf16 from 128 to
+// 8192 columns (a copy: 6.0); one or two loads 3.0 - 4.7, eight loads (two blocks) 2.5 - 4.0.
+// The backward pass keeps dw's columns in registers over all rows of a block and loads the next row
+// while the sums of this one are exchanged: 16384 x 4096 bf16 118 -> 96 us (5.6 TB/s).
 // The statistic, y and the sums of dw are fp32; r is rounded before the statistic, so
 // that the backward pass, which reads the stored r, differentiates what was computed.
 #include <cuda_fp8.h>
@@ -113,6 +117,8 @@ __device__ __forceinline__ void row_reduce(float (&s)[U], float *red) {
 
 constexpr int OUT_SAME = 0, OUT_E4M3 = 1, OUT_I8 = 2;
 __host__ __device__ constexpr int block_threads(int TPR) { return TPR < 256 ? 256 : TPR; }
+// 64 registers a thread for bf16, 128 for fp32, whose loads take twice as many
+__host__ __device__ constexpr int blocks_per_sm(int TPR, bool bf16) { return (bf16 ? 1024 : 512) / block_threads(TPR); }
 
 // 8 scaled values -> 8 bytes.
 template <int OUT>
@@ -137,7 +143,7 @@ __device__ __forceinline__ uint2 pack_bytes(const float (&z)[8]) {
 }
 
 template <int TPR, int VPT, int U, bool BF16, int OUT>
-__global__ void __launch_bounds__(block_threads(TPR), TPR >= 1024 ? 1 : 2) norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(block_threads(TPR), blocks_per_sm(TPR, BF16)) norm_kernel(NormParams p) {
   constexpr int NT = block_threads(TPR), GROUPS = NT / TPR;
   __shared__ float red[U * 32];
   if (device_error_latched(p.err)) return;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR >= 1024 ? 1 : 2) norm_
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         f[u][i][e] = f[u][i][e] * rstd * w[e];
-        if constexpr (OUT != OUT_SAME) top[u] = max_nan(top[u], vec < nvec ? fabsf(f[u][i][e]) : 0.f);
+        if (OUT != OUT_SAME && p.group == 0) top[u] = max_nan(top[u], vec < nvec ? fabsf(f[u][i][e]) : 0.f);
       }
     }
   }
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR >= 1024 ? 1 : 2) norm_
   } else {
     constexpr float kMost = OUT == OUT_E4M3 ? 448.f : 127.f;
     if (p.group == 0) row_reduce<TPR, U, true>(top, red);
-    const int lanes = p.group / 8;       // consecutive lanes of a group (a multiple of 4, at most 16)
+    const int lanes_log = p.group == 128 ? 4 : p.group == 64 ? 3 : 2;       // log2 of a group's consecutive lanes
     const int nscale = p.group ? (p.D + p.group - 1) / p.group : 1;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -234,16 +240,19 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR >= 1024 ? 1 : 2) norm_
           if (vec < nvec)
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[u][i][e]));
-          for (int o = lanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          if (lanes_log >= 4) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+          if (lanes_log >= 3) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+          m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         }
-        const float scale = max_nan(m, kTiny) / kMost, inv = 1.f / scale;
+        const float most = max_nan(m, kTiny), inv = __fdividef(kMost, most);
         if (row < p.rows && vec < nvec) {
           float z[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] = f[u][i][e] * inv;
           reinterpret_cast<uint2 *>(p.y)[(size_t)row * nvec + vec] = pack_bytes<OUT>(z);
-          if (p.group == 0 ? vec == 0 : vec % lanes == 0)
-            p.scale[(size_t)row * nscale + (p.group ? vec / lanes : 0)] = scale;
+          if (p.group == 0 ? vec == 0 : (vec & ((1 << lanes_log) - 1)) == 0)
+            p.scale[(size_t)row * nscale + (p.group ? vec >> lanes_log : 0)] = most / kMost;
         }
       }
     }
@@ -251,10 +260,13 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR >= 1024 ? 1 : 2) norm_
 }
 
 // ---- backward: rows dealt to the blocks in turn; a thread's columns of dw stay in registers
-template <int TPR, int VPT, int U, bool BF16>
-__global__ void __launch_bounds__(block_threads(TPR), TPR >= 512 ? 1 : 2) norm_backward_kernel(NormBackwardParams p) {
+__host__ __device__ constexpr int back_blocks_per_sm(int TPR, bool bf16) { return bf16 && TPR <= 256 ? 2 : 1; }
+
+template <int TPR, int VPT, bool BF16>
+__global__ void __launch_bounds__(block_threads(TPR), back_blocks_per_sm(TPR, BF16)) norm_backward_kernel(NormBackwardParams p) {
   constexpr int NT = block_threads(TPR), GROUPS = NT / TPR;
-  __shared__ float red[2 * U * 32];
+  constexpr bool AHEAD = TPR < 1024;      // the widest rows have no registers for a second one
+  __shared__ float red[2 * 32];
   __shared__ float sum[GROUPS > 1 ? GROUPS * TPR * VPT * 8 : 1];
   if (device_error_latched(p.err)) return;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -270,60 +282,59 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR >= 512 ? 1 : 2) norm_b
     }
   }
   const float inv_d = 1.f / (float)p.D;
-  const long long step = (long long)gridDim.x * (GROUPS * U);
-  for (long long base = (long long)blockIdx.x * (GROUPS * U); base < p.rows; base += step) {
-    Raw<BF16> rx[U][VPT], ry[U][VPT], rg[U][VPT];
-    float s[2 * U];
+  const long long step = (long long)gridDim.x * GROUPS;
+  Raw<BF16> nx[VPT], ny[VPT], ng[VPT];
+  auto fetch = [&](long long row) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long row = base + grp + (long long)u * GROUPS;
+    for (int i = 0; i < VPT; ++i) {
+      const int vec = t + i * TPR;
+      const size_t at = (size_t)row * nvec + vec;
+      const bool in = row < p.rows && vec < nvec;
+      nx[i] = in ? load8<BF16>(p.x, at) : Raw<BF16>{};
+      ny[i] = in ? load8<BF16>(p.dy, at) : Raw<BF16>{};
+      if (p.dr) ng[i] = in ? load8<BF16>(p.dr, at) : Raw<BF16>{};
+    }
+  };
+  const long long first = (long long)blockIdx.x * GROUPS;
+  if (AHEAD) fetch(first + grp);
+  for (long long base = first; base < p.rows; base += step) {      // the block's rows; each thread comes along to the last
+    const long long row = base + grp;
+    if (!AHEAD) fetch(row);
+    Raw<BF16> cx[VPT], cy[VPT], cg[VPT];
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int vec = t + i * TPR;
-        const size_t at = (size_t)row * nvec + vec;
-        const bool in = row < p.rows && vec < nvec;
-        rx[u][i] = in ? load8<BF16>(p.x, at) : Raw<BF16>{};
-        ry[u][i] = in ? load8<BF16>(p.dy, at) : Raw<BF16>{};
-        if (p.dr) rg[u][i] = in ? load8<BF16>(p.dr, at) : Raw<BF16>{};
+    for (int i = 0; i < VPT; ++i) {
+      cx[i] = nx[i];
+      cy[i] = ny[i];
+      cg[i] = ng[i];
+      float x[8], y[8];
+      unpack8<BF16>(cx[i], x);
+      unpack8<BF16>(cy[i], y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[0] = fmaf(x[e], x[e], s[0]);
+        s[1] = fmaf(x[e], y[e] * w[i][e], s[1]);
       }
     }
+    if (AHEAD) fetch(row + step);
+    row_reduce<TPR, 2, false>(s, red);
+    const float rstd = rsqrtf(s[0] * inv_d + p.eps);
+    const float back = rstd * rstd * (s[1] * inv_d);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      s[u] = s[U + u] = 0.f;
+    for (int i = 0; i < VPT; ++i) {
+      const int vec = t + i * TPR;
+      if (row >= p.rows || vec >= nvec) continue;
+      float x[8], y[8], g[8];
+      unpack8<BF16>(cx[i], x);
+      unpack8<BF16>(cy[i], y);
+      if (p.dr) unpack8<BF16>(cg[i], g);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float x[8], y[8];
-        unpack8<BF16>(rx[u][i], x);
-        unpack8<BF16>(ry[u][i], y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[u] = fmaf(x[e], x[e], s[u]);
-          s[U + u] = fmaf(x[e], y[e] * w[i][e], s[U + u]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        dw[i][e] = fmaf(y[e], x[e] * rstd, dw[i][e]);
+        const float d = rstd * fmaf(-x[e], back, y[e] * w[i][e]);
+        y[e] = p.dr ? d + g[e] : d;
       }
-    }
-    row_reduce<TPR, 2 * U, false>(s, red);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long row = base + grp + (long long)u * GROUPS;
-      const float rstd = rsqrtf(s[u] * inv_d + p.eps);
-      const float back = rstd * rstd * (s[U + u] * inv_d);
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int vec = t + i * TPR;
-        if (row >= p.rows || vec >= nvec) continue;
-        float x[8], y[8], g[8];
-        unpack8<BF16>(rx[u][i], x);
-        unpack8<BF16>(ry[u][i], y);
-        if (p.dr) unpack8<BF16>(rg[u][i], g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dw[i][e] = fmaf(y[e], x[e] * rstd, dw[i][e]);
-          const float d = rstd * fmaf(-x[e], back, y[e] * w[i][e]);
-          y[e] = p.dr ? d + g[e] : d;
-        }
-        store8<BF16>(p.dx, (size_t)row * nvec + vec, pack8<BF16>(y));
-      }
+      store8<BF16>(p.dx, (size_t)row * nvec + vec, pack8<BF16>(y));
     }
   }
   if (p.part == nullptr) return;
@@ -373,33 +384,36 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int pa
   }
 }
 
-template <int TPR, int VPT, int U>
+template <int TPR, int VPT, int U, bool SAME = true>
 cudaError_t launch(const NormParams &p, bool bf16, int out, cudaStream_t s) {
   constexpr int NT = block_threads(TPR);
   const long long per = (long long)(NT / TPR) * U;
   const unsigned grid = (unsigned)((p.rows + per - 1) / per);
-  if (bf16) {
-    if (out == OUT_SAME) norm_kernel<TPR, VPT, U, true, OUT_SAME><<<grid, NT, 0, s>>>(p);
-    else if (out == OUT_E4M3) norm_kernel<TPR, VPT, U, true, OUT_E4M3><<<grid, NT, 0, s>>>(p);
+  if (out == OUT_SAME) {
+    if constexpr (SAME) {
+      if (bf16) norm_kernel<TPR, VPT, U, true, OUT_SAME><<<grid, NT, 0, s>>>(p);
+      else norm_kernel<TPR, VPT, U, false, OUT_SAME><<<grid, NT, 0, s>>>(p);
+    }
+  } else if (bf16) {
+    if (out == OUT_E4M3) norm_kernel<TPR, VPT, U, true, OUT_E4M3><<<grid, NT, 0, s>>>(p);
     else norm_kernel<TPR, VPT, U, true, OUT_I8><<<grid, NT, 0, s>>>(p);
   } else {
-    if (out == OUT_SAME) norm_kernel<TPR, VPT, U, false, OUT_SAME><<<grid, NT, 0, s>>>(p);
-    else if (out == OUT_E4M3) norm_kernel<TPR, VPT, U, false, OUT_E4M3><<<grid, NT, 0, s>>>(p);
+    if (out == OUT_E4M3) norm_kernel<TPR, VPT, U, false, OUT_E4M3><<<grid, NT, 0, s>>>(p);
     else norm_kernel<TPR, VPT, U, false, OUT_I8><<<grid, NT, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
 
-constexpr int kMaxParts = 148 * 4;      // rows of partial sums at most
+constexpr int kMaxParts = 148 * 2;      // rows of partial sums at most: as many blocks as run at a time
 
-template <int TPR, int VPT, int U>
+template <int TPR, int VPT>
 cudaError_t launch_back(const NormBackwardParams &p, bool bf16, cudaStream_t s) {
   constexpr int NT = block_threads(TPR);
-  const long long per = (long long)(NT / TPR) * U, need = (p.rows + per - 1) / per;
-  const long long cap = TPR >= 1024 ? kMaxParts / 4 : TPR == 512 ? kMaxParts / 2 : kMaxParts;
+  const long long per = NT / TPR, need = (p.rows + per - 1) / per;
+  const long long cap = (long long)kMaxParts / 2 * back_blocks_per_sm(TPR, bf16);
   const unsigned grid = (unsigned)(need < cap ? need : cap);
-  if (bf16) norm_backward_kernel<TPR, VPT, U, true><<<grid, NT, 0, s>>>(p);
-  else norm_backward_kernel<TPR, VPT, U, false><<<grid, NT, 0, s>>>(p);
+  if (bf16) norm_backward_kernel<TPR, VPT, true><<<grid, NT, 0, s>>>(p);
+  else norm_backward_kernel<TPR, VPT, false><<<grid, NT, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part == nullptr) return e;
   norm_dw_kernel<<<(unsigned)((p.D + 31) / 32), dim3(32, 32), 0, s>>>(p.part, (int)grid, p.D, p.dw, p.err);
@@ -413,20 +427,26 @@ size_t norm_backward_workspace(long long rows, int D) {
   return (size_t)parts * (size_t)D * 4;
 }
 
-// Threads per row: the smallest count that holds the row in one vector of 8 columns each
-// (two from 4096 columns, where more threads only add exchanges).
+// Threads per row so that a thread holds four vectors of 8 columns (of two rows where a row has no more than
+// 128 threads of two), from the measurements above.
 cudaError_t launch_norm(const NormParams &p, bool bf16, int out, cudaStream_t s) {
   using namespace norm;
   if (p.rows == 0) return cudaSuccess;
   const int nvec = p.D / 8;
-  if (nvec <= 16) return launch<16, 1, 4>(p, bf16, out, s);
-  if (nvec <= 32) return launch<32, 1, 4>(p, bf16, out, s);
-  if (nvec <= 64) return launch<64, 1, 2>(p, bf16, out, s);
-  if (nvec <= 128) return launch<128, 1, 2>(p, bf16, out, s);
-  if (nvec <= 256) return launch<256, 1, 1>(p, bf16, out, s);
-  if (nvec <= 512) return launch<256, 2, 1>(p, bf16, out, s);
-  if (nvec <= 1024) return launch<512, 2, 1>(p, bf16, out, s);
-  return launch<1024, 2, 1>(p, bf16, out, s);
+  if (nvec <= 16 && out == OUT_SAME) {      // without groups of 16 lanes: fewer exchanges; 5.9 against 5.2 TB/s
+    const unsigned grid = (unsigned)((p.rows + 63) / 64);
+    if (bf16) norm_kernel<8, 2, 2, true, OUT_SAME><<<grid, 256, 0, s>>>(p);
+    else norm_kernel<8, 2, 2, false, OUT_SAME><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  if (nvec <= 16) return launch<16, 1, 4, false>(p, bf16, out, s);
+  if (nvec <= 32) return launch<16, 2, 2>(p, bf16, out, s);
+  if (nvec <= 64) return launch<32, 2, 2>(p, bf16, out, s);
+  if (nvec <= 128) return launch<32, 4, 1>(p, bf16, out, s);
+  if (nvec <= 256) return launch<128, 2, 2>(p, bf16, out, s);
+  if (nvec <= 512) return launch<128, 4, 1>(p, bf16, out, s);
+  if (nvec <= 1024) return launch<256, 4, 1>(p, bf16, out, s);
+  return launch<512, 4, 1>(p, bf16, out, s);
 }
 
 cudaError_t launch_norm_backward(const NormBackwardParams &p, bool bf16, cudaStream_t s) {
@@ -434,14 +454,14 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, bool bf16, cudaStr
   if (p.rows == 0)
     return p.dw ? cudaMemsetAsync(p.dw, 0, (size_t)p.D * 4, s) : cudaSuccess;
   const int nvec = p.D / 8;
-  if (nvec <= 16) return launch_back<16, 1, 2>(p, bf16, s);
-  if (nvec <= 32) return launch_back<32, 1, 2>(p, bf16, s);
-  if (nvec <= 64) return launch_back<64, 1, 1>(p, bf16, s);
-  if (nvec <= 128) return launch_back<128, 1, 1>(p, bf16, s);
-  if (nvec <= 256) return launch_back<256, 1, 1>(p, bf16, s);
-  if (nvec <= 512) return launch_back<256, 2, 1>(p, bf16, s);
-  if (nvec <= 1024) return launch_back<512, 2, 1>(p, bf16, s);
-  return launch_back<1024, 2, 1>(p, bf16, s);
+  if (nvec <= 16) return launch_back<8, 2>(p, bf16, s);
+  if (nvec <= 32) return launch_back<16, 2>(p, bf16, s);
+  if (nvec <= 64) return launch_back<32, 2>(p, bf16, s);
+  if (nvec <= 128) return launch_back<64, 2>(p, bf16, s);
+  if (nvec <= 256) return launch_back<128, 2>(p, bf16, s);
+  if (nvec <= 512) return launch_back<256, 2>(p, bf16, s);
+  if (nvec <= 1024) return launch_back<512, 2>(p, bf16, s);
+  return launch_back<1024, 2>(p, bf16, s);
 }
 
 }  // namespace kda
