@@ -18,7 +18,7 @@
 //           TMEM over A.  E, F and U are scaled in TMEM, where the second products add to them; on
 //           the way the row sums q.E and k.F give the decays' gradients, in fp32.
 // The grad kernel is a persistent block per SM: a load/store warp, an MMA thread, a warp that
-// prepares decays and clears rows that are pads or belong to the next sequence, and four warpgroups.
+// prepares decays, and four warpgroups.
 #include "kda_linear_tc.cuh"
 
 namespace kda {
@@ -532,7 +532,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
                      xk[2] = {desc_kmajor(sx, DK, 0, 0), desc_kmajor(sx + L::X1, DK, 0, 0)}, mk = desc_kmajor(smm, C, 0, 0), mm = desc_mnmajor(smm, C, 0, 0);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
         const uint32_t T_V = tm + t_v(it), T_Q = tm + t_q(it);
-        ok = wait(ready, it, SITE_GRAD + 6);
+        ok = wait(full, it, SITE_GRAD + 6);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll
@@ -603,7 +603,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       mbar_wait(drain, 0, p.wait_cycles);
     }
   } else if (warp == 18) {
-    // ---------------- decays and rows to clear
+    // ---------------- decays
     bool ok = true;
     RawDecays raw{};
     auto next = [&](int i) {
@@ -618,7 +618,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       uint32_t word;
       const RawDecays now = raw;
       next(i + gridDim.x);
-      const bool clean = scan_decays(now, b, total, word);
+      scan_decays(now, b, total, word);
       if (it > 0) ok = wait.warp(tab_free, it - 1, SITE_GRAD + 16);
       if (!ok) break;
       if ((lane & 7) == 0) valid[lane >> 3] = word;
@@ -626,15 +626,6 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       for (int e = 0; e < 4; ++e) {
         const float hi = (float)b[e];
         hl[4 * lane + e] = make_float2(hi, (float)(b[e] - (double)hi));
-      }
-      __syncwarp();
-      ok = wait.warp(full, it, SITE_GRAD + 17);
-      if (!clean && ok) {
-        clear_rows<DK>(sm + L::Q, valid);
-        clear_rows<DK>(sm + L::K, valid);
-        clear_rows<DV>(sm + L::V, valid);
-        clear_rows<DV>(sm + L::O, valid);
-        fence_async_smem();
       }
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(ready);
@@ -650,9 +641,26 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
       const int h = i % p.H, pos = sg.begin;
       const int rows = sg.end - pos;
       const uint32_t T_V = tm + lanes + t_v(it), T_Q = tm + lanes + t_q(it);
-      ok = wait.warp(ready, it, SITE_GRAD + 18);
+      ok = wait.warp(ready, it, SITE_GRAD + 18) && wait.warp(full, it, SITE_GRAD + 17);
       if (!ok) break;
       const float2 br = hl[r];
+      const uint32_t cols = valid[y];                  // of the warp's columns: the real rows
+      const bool real = (valid[w] >> lane) & 1;
+      if (!real) {      // a pad or a row of the next sequence: q, k and grad_o must not reach other rows (sums of whole rows are
+                        // masked where they are used)
+#pragma unroll
+        for (int e = 0; e < DK / 32; ++e) {
+          const int cc = y * (DK / 32) + e;
+          const uint32_t at = row_tile_chunk(r, cc >> 3, cc & 7, C);
+          *reinterpret_cast<uint4 *>(sm + L::Q + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sm + L::K + at) = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < DV / 32; ++e) {
+          const int cc = y * (DV / 32) + e;
+          *reinterpret_cast<uint4 *>(sm + L::O + row_tile_chunk(r, cc >> 3, cc & 7, C)) = make_uint4(0, 0, 0, 0);
+        }
+      }
       float fac;      // E's rows are scaled by 2^{b_t}, F's and U's by 2^{b_C - b_s}
       {
         const float2 be = hl[C - 1];
@@ -682,6 +690,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4 *>(mt + row_tile_chunk(r, y >> 1, 4 * (y & 1) + c, C)) = make_uint4(0, 0, 0, 0);
       } else {
+        const uint32_t on_cols = real ? cols : 0u;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           float a[16], g[16];
@@ -702,9 +711,9 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const bool on = y > w || 16 * z + e + x >= lane;      // t >= s
+              const bool on = (y > w || 16 * z + e + x >= lane) && ((on_cols >> (16 * z + e + x)) & 1);      // t >= s
               a[e + x] = on ? a[e + x] * d[x] : 0.f;
-              f[16 * z + e + x] = a[e + x] * g[e + x];
+              f[16 * z + e + x] = on ? a[e + x] * g[e + x] : 0.f;
               g[e + x] = on ? g[e + x] * d[x] : 0.f;
             }
           }
@@ -728,7 +737,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         float acc = 0.f;
 #pragma unroll
         for (int e = 31; e >= 0; --e) {
-          acc += (y > w || e >= lane) ? f[e] : 0.f;
+          acc += f[e];
           f[e] = (y > w || e > lane) ? acc : 0.f;
         }
         if (y > w) before = exclusive_sum(acc);
@@ -768,6 +777,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         tmem_st_wait();
         fence_before_sync();
         mbar_arrive(y ? f_scaled : e_scaled);
+        if (!real) dot = 0.f;
         // over the rows from this one on (q.E) or before this one (k.F): to the third warpgroup, in TMEM beside P
         const float sum = y ? exclusive_sum(dot) : suffix_sum(dot);
         if (lane == (y ? 31 : 0)) sums[4 * y + w] = y ? sum + dot : sum;
@@ -815,7 +825,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           for (int x = w + 1; x < 4; ++x) g += sums[x];
           for (int x = 0; x < w; ++x) g += sums[4 + x];
           // one decay per head: [H, N] for the sum that follows
-          if (r < rows) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = ((valid[w] >> lane) & 1) ? g : 0.f;
+          if (r < rows) gla[p.decay_head ? (size_t)h * p.N + pos + r : (size_t)(pos + r) * p.H + h] = real ? g : 0.f;
           fence_before_sync();
           mbar_arrive(tab_free);
         }
@@ -828,6 +838,9 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           if (32 * x >= cols) break;
           float f[32];
           tmem_ld32(col + 32 * x, f);
+          if (!real)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = 0.f;
           if (row32 != nullptr) {
             if (r < rows)
 #pragma unroll

@@ -133,17 +133,6 @@ struct Waits {
   }
 };
 
-// Zeroes the rows of a [128][D] tile that are not set in valid (one warp).
-template <int D>
-__device__ __forceinline__ void clear_rows(unsigned char *tile, const uint32_t *valid) {
-  const int lane = threadIdx.x & 31;
-  for (int w = 0; w < C / 32; ++w)
-    for (uint32_t pads = ~valid[w]; pads != 0; pads &= pads - 1) {
-      const int r = 32 * w + __ffs((int)pads) - 1;
-      if (lane < D / 8) *reinterpret_cast<uint4 *>(tile + row_tile_chunk(r, lane >> 3, lane & 7, C)) = make_uint4(0, 0, 0, 0);
-    }
-}
-
 // A chunk's decays, one warp: lane's rows 4 lane .. 4 lane + 3.  Loading is apart from summing, so that the
 // next chunk's values are on their way while this one's are used.
 struct RawDecays {
