@@ -21,10 +21,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs), and behind them each segment's
-// sequence, rows [begin, end) and whether it is the sequence's last.
+// Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs); behind them the segments in the order
+// in which blocks take them: number (their states' place, in the sequences' order), rows [begin, end) and whether a
+// segment is its sequence's last.
 struct alignas(16) Segment {
-  int b, begin, end, last;
+  int id, begin, end, last;
 };
 inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
 inline size_t table_bytes(int B, size_t segs) { return align256((size_t)(B + 1) * 4) + align256(segs * sizeof(Segment)); }

@@ -947,7 +947,7 @@ cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float
   *gq32 = shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr;
   *gk32 = shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr;
   *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
-  cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, s);
+  cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, 1, 1, 1, s);
   if (e != cudaSuccess) return e;
   GradMaps mg{};
   SweepMaps mf{}, mr{};

@@ -28,6 +28,12 @@ struct Maps {
   CUtensorMap q, k, v, o, part;
 };
 
+// A block's n-th item (segment x H + h): there and back over the blocks, so that the blocks with the longest item of one
+// round take the shortest of the next.
+__device__ __forceinline__ int item_of(int n) {
+  return n * (int)gridDim.x + (int)(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 // ============================================================ parts
 // A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
 // weights; the others follow.  It goes from a segment's last chunk to its first and stops once every
@@ -54,7 +60,7 @@ struct PartsSmem {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kPartsThreads, 1)
-parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *whole, int per) {
+parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *whole) {
   using L = PartsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
@@ -177,7 +183,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
       ok = __all_sync(0xFFFFFFFFu, ok);
       return ok;
     };
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+    for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
       const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
       // the last segment of a sequence matters to the final state only
       if (sg.last && p.final_state == nullptr) continue;
@@ -201,10 +207,10 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
         if ((lane & 7) == 0) valid[4 * rs + (lane >> 3)] = word;
         after += total;
         const bool last = j == 0 || after < -151.0;
-        publish(i, sg.begin + j * C, h, j == chunks - 1, last);
+        publish(sg.id * p.H + h, sg.begin + j * C, h, j == chunks - 1, last);
         if (last) break;
       }
-      if (lane == 0) whole[i] = ex2((float)after);
+      if (lane == 0) whole[sg.id * p.H + h] = ex2((float)after);
     }
     if (ok && reserve()) publish(-1, 0, 0, false, false);
   } else {
@@ -326,7 +332,7 @@ struct RowsSmem {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kRowsThreads, 1)
-rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, const float *start, int per) {
+rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, const float *start) {
   using L = RowsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   if (device_error_latched(p.err)) return;
@@ -359,7 +365,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   const int G = p.H / p.Hk;
   // items' segments, loaded an item ahead
   auto segment = [&](int i) { return i < nitems ? lin::locate(sbase, p.num_seqs, i / p.H) : Segment{}; };
-  Segment next = segment(blockIdx.x);
+  Segment next = segment(item_of(0));
   int step = 0, ln = 0;      // chunks; those among them whose S goes on to another
 
   if (warp == 17) {
@@ -376,9 +382,9 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         bulk_commit();
         bulk_wait_read();
       };
-      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+      for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
         const Segment sg = next;
-        next = segment(i + gridDim.x);
+        next = segment(item_of(n_i + 1));
         const int h = i % p.H;
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
@@ -422,13 +428,13 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           mma_bf16(tm + T_A, kmajor_step<C>(q, s), kmajor_step<C>(k, s), idesc_bf16(128, C, 0, 0), s > 0);
         mma_commit(a_done);
       };
-      if (blockIdx.x < nitems) issue_a(0);
-      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+      if (item_of(0) < nitems) issue_a(0);
+      for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
         const Segment sg = next;
-        next = segment(i + gridDim.x);
+        next = segment(item_of(n_i + 1));
         for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
           const int st = step & 1;
-          const bool last = pos + C >= sg.end, more = !last || i + (int)gridDim.x < nitems;
+          const bool last = pos + C >= sg.end, more = !last || item_of(n_i + 1) < nitems;
           const uint32_t sq = st ? stage[1] : stage[0], sk = sq + L::QT, sv = sk + L::QT;
           const uint64_t q = desc_kmajor(sq, C, 0, 0), w = desc_mnmajor(sw, DK, 0, 0), k = desc_mnmajor(sk, C, 0, 0),
                          v = desc_mnmajor(sv, C, 0, 0), hi = desc_mnmajor(sw, C, 0, 0),
@@ -472,14 +478,14 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   } else if (warp == 18) {
     // ---------------- decays; the next chunk's are loaded a chunk ahead
     bool ok = true;
-    int ni = blockIdx.x, npos = 0;           // the chunk whose decays are on their way
+    int nk = 0, ni = item_of(0), npos = 0;   // the chunk whose decays are on their way
     Segment ns{};
     auto next = [&]() {
       RawDecays d{};
       if (ni >= nitems) return d;
       d = load_decays(p, npos, ns.end, ni % p.H);
       npos += C;
-      if (npos >= ns.end && (ni += gridDim.x) < nitems) {
+      if (npos >= ns.end && (ni = item_of(++nk)) < nitems) {
         ns = lin::locate(sbase, p.num_seqs, ni / p.H);
         npos = ns.begin;
       }
@@ -490,7 +496,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       npos = ns.begin;
     }
     RawDecays raw = next();
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+    for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
       const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
@@ -521,9 +527,9 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     float *colf = reinterpret_cast<float *>(sm + L::COLF) + (w * (w - 1) / 2 + y) * 32;      // y < w
     bool ok = true;
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+    for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
       const Segment sg = next;
-      next = segment(i + gridDim.x);
+      next = segment(item_of(n_i + 1));
       const int h = i % p.H;
       for (int pos = sg.begin; pos < sg.end && ok; pos += C, ++step) {
         const int st = step & 1;
@@ -618,7 +624,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
           const uint32_t col = tm + lanes + T_S + y * COLS;
           uint32_t v[COLS];
           if (first) {
-            const float *in = start + ((size_t)i * DK + r) * DV + y * COLS;
+            const float *in = start + (((size_t)sg.id * p.H + h) * DK + r) * DV + y * COLS;
 #pragma unroll
             for (int e = 0; e < COLS; e += 4)
               *reinterpret_cast<uint4 *>(&v[e]) = __ldcs(reinterpret_cast<const uint4 *>(in + e));
@@ -716,25 +722,24 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
 }
 
 // ============================================================ host
-// Chunks in a segment: the count with the shortest expected run, in chunk times: rounds of items over the
-// SMs, each item `per` chunks and about two more (fill of the pipeline, its state in and out).
-int segment_chunks(int N, int B, int H) {
+// The fewest chunks in a segment that the plan may take: half of what sequences of equal length would have, in rounds of
+// segments over the SMs with two chunks' time for each segment's beginning and end.  It bounds the workspace.
+int least_chunks(int N, int B, int H) {
   int best = 1;
   double cost = 1e300;
   for (int per = 1; per <= 32; ++per) {
     const double items = ((double)N / (C * per) + 0.5 * B) * H;
-    const double rounds = std::ceil(items / 148.0);
-    const double c = rounds * (per + 2.0);
+    const double c = std::ceil(items / 148.0) * (per + 2.0);
     if (c < cost * 0.999) {
       cost = c;
       best = per;
     }
   }
-  return best;
+  return (best + 1) / 2;
 }
 
 template <int DK, int DV>
-cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, float *part, float *whole, int per,
+cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, float *part, float *whole,
                    size_t segs, cudaStream_t s) {
   const size_t items = segs * p.H;
   if (items * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;      // rows of the states as a tensor map's coordinate
@@ -742,10 +747,10 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
   cudaError_t e = lin::allow_smem<parts_kernel<DK, DV>>(PartsSmem<DK, DV>::END);
   if (e == cudaSuccess) e = lin::allow_smem<rows_kernel<DK, DV>>(RowsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
-  if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, whole, per);
+  if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, whole);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_linear_chain(p, sbase, part, nullptr, whole, s)) != cudaSuccess) return e;
-  if (grid) rows_kernel<DK, DV><<<grid, kRowsThreads, RowsSmem<DK, DV>::END, s>>>(p, maps, sbase, part, per);
+  if (grid) rows_kernel<DK, DV><<<grid, kRowsThreads, RowsSmem<DK, DV>::END, s>>>(p, maps, sbase, part);
   return cudaGetLastError();
 }
 
@@ -753,19 +758,19 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
 
 size_t linear_prefill_tc_workspace(const LinearParams &p) {
   using namespace lintc;
-  const size_t segs = lin::max_segments(p.N, p.num_seqs, C * segment_chunks(p.N, p.num_seqs, p.H));
+  const size_t segs = lin::max_segments(p.N, p.num_seqs, C * least_chunks(p.N, p.num_seqs, p.H));
   return lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4) + segs * p.H * (size_t)p.dk * p.dv * 4;
 }
 
 cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   using namespace lintc;
-  const int per = segment_chunks(p.N, p.num_seqs, p.H);
+  const int per = least_chunks(p.N, p.num_seqs, p.H);
   const size_t segs = p.N > 0 ? lin::max_segments(p.N, p.num_seqs, C * per) : 0;
   unsigned char *w = static_cast<unsigned char *>(p.ws);
   int *sbase = reinterpret_cast<int *>(w);
   float *whole = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs));
   float *part = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4));
-  cudaError_t e = launch_linear_plan(p, sbase, C * per, s);
+  cudaError_t e = launch_linear_plan(p, sbase, C, per, 64, sm_count(), s);
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&
@@ -773,10 +778,10 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
                    encode_f32(&maps.part, part, p.dv, segs * p.H * p.dk, p.dk)))
     return cudaErrorNotSupported;
   if (p.dk == 128)
-    return p.dv == 128 ? launch<128, 128>(p, maps, sbase, part, whole, per, segs, s)
-                       : launch<128, 64>(p, maps, sbase, part, whole, per, segs, s);
-  return p.dv == 128 ? launch<64, 128>(p, maps, sbase, part, whole, per, segs, s)
-                     : launch<64, 64>(p, maps, sbase, part, whole, per, segs, s);
+    return p.dv == 128 ? launch<128, 128>(p, maps, sbase, part, whole, segs, s)
+                       : launch<128, 64>(p, maps, sbase, part, whole, segs, s);
+  return p.dv == 128 ? launch<64, 128>(p, maps, sbase, part, whole, segs, s)
+                     : launch<64, 64>(p, maps, sbase, part, whole, segs, s);
 }
 
 }  // namespace kda
