@@ -497,13 +497,14 @@ def _linear_common(a, q, k, v, log_alpha, rows: int, same_device=()):
     """Checks what the linear-attention calls share and fills those fields of ``a``."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q and v must be [rows, heads, dim]")
-    N, Hk, dk = q.shape
-    H, dv = v.shape[1:]
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    N, Hk, dk = qs
+    _, H, dv = vs
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError(f"the value heads ({H}) must be a multiple of the query/key heads ({Hk})")
-    _check_cuda("q", q, shape=(rows, Hk, dk))
-    _check_cuda("k", k, q.dtype, (rows, Hk, dk))
-    _check_cuda("v", v, q.dtype, (rows, H, dv))
+    _check_cuda("q", q, None, (rows, Hk, dk))
+    _check_cuda("k", k, dt, qs)
+    _check_cuda("v", v, dt, (rows, H, dv))
     a.decay = decay_layout(log_alpha)
     _check_cuda("log_alpha", log_alpha, torch.float32, (H,) if a.decay == KDA_DECAY_HEAD else (rows, H))
     a.dtype = _dtype_code(q)
@@ -523,12 +524,20 @@ def _check_device(first, *others):
         raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _workspace(a, name: str, workspace, device):
-    """The call's workspace: the caller's, or one of the size that the library states."""
-    nbytes = int(getattr(_lib or load(), name + "_workspace_size")(ctypes.byref(a)))
+_workspace_sizes = {}
+
+
+def _workspace(a, name: str, sizes, workspace, like):
+    """The call's workspace: the caller's, or one of the size that the library states for these ``sizes``."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    a.workspace = _ptr(workspace)
+        nbytes = _workspace_sizes.get((name, sizes))
+        if nbytes is None:
+            nbytes = int(getattr(_lib or load(), name + "_workspace_size")(ctypes.byref(a)))
+            if len(_workspace_sizes) >= 4096:
+                _workspace_sizes.clear()
+            _workspace_sizes[(name, sizes)] = nbytes
+        workspace = like.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
 
@@ -560,11 +569,11 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha:
     if final_state is not None:
         _check_cuda("final_state", final_state, torch.float32, (B, H, dk, dv))
     elif want_final_state:
-        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        final_state = log_alpha.new_empty((B, H, dk, dv))
     a.num_seqs, a.total_tokens = B, N
     a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
     a.o, a.final_state = _ptr(o), _ptr(final_state)
-    workspace = _workspace(a, "kda_linear_prefill", workspace, q.device)
+    workspace = _workspace(a, "kda_linear_prefill", (a.dtype, B, N, H, Hk, dk, dv), workspace, q)
     st = (_lib or load()).kda_linear_prefill(ctypes.byref(a), _raw_stream(stream, q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill")
@@ -621,13 +630,13 @@ def linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_s
     _check_cuda("grad_final_state", grad_final_state, torch.float32, (B, H, dk, dv))
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
          "dlog_alpha": torch.empty_like(log_alpha),
-         "dS0": torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device) if want_grad_init_state else None}
+         "dS0": log_alpha.new_empty((B, H, dk, dv)) if want_grad_init_state else None}
     a.num_seqs, a.total_tokens = B, N
     a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
     a.grad_o, a.grad_final_state = _ptr(grad_o), _ptr(grad_final_state)
     a.grad_q, a.grad_k, a.grad_v = _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"])
     a.grad_log_alpha, a.grad_init_state = _ptr(g["dlog_alpha"]), _ptr(g["dS0"])
-    workspace = _workspace(a, "kda_linear_prefill_backward", workspace, q.device)
+    workspace = _workspace(a, "kda_linear_prefill_backward", (a.dtype, B, N, H, Hk, dk, dv, a.decay), workspace, q)
     st = (_lib or load()).kda_linear_prefill_backward(ctypes.byref(a), _raw_stream(stream, q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill_backward")
@@ -641,8 +650,7 @@ def _norm_rows(x: torch.Tensor) -> Tuple[int, int]:
     return (x.numel() // D if D else 0), D
 
 
-def _rms_norm(x, weight, residual, eps, out_dtype, group, y, scale, residual_out, stream):
-    rows, D = _norm_rows(x)
+def _rms_norm(x, rows, D, weight, residual, eps, out_dtype, group, y, scale, residual_out, stream):
     _check_cuda("x", x)
     _check_cuda("weight", weight, torch.float32, (D,))
     _check_cuda("residual", residual, x.dtype, x.shape)
@@ -653,8 +661,8 @@ def _rms_norm(x, weight, residual, eps, out_dtype, group, y, scale, residual_out
     else:
         _check_cuda("residual_out", residual_out, x.dtype, x.shape)
     _check_device(x, weight, residual, y, scale, residual_out)
-    a = RmsNormArgs(_dtype_code(x), out_dtype, rows, D, _ptr(x), _ptr(residual), _ptr(weight), eps, group,
-                    _ptr(y), _ptr(scale), _ptr(residual_out))
+    a = RmsNormArgs(_dtype_code(x), out_dtype, rows, D, x.data_ptr(), _ptr(residual), _ptr(weight), eps, group,
+                    y.data_ptr(), _ptr(scale), _ptr(residual_out))
     st = (_lib or load()).kda_rms_norm(ctypes.byref(a), _raw_stream(stream, x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm")
@@ -668,11 +676,12 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     residual is given.  x [.., D] bf16 or fp32, D a multiple of 8 up to 16384; weight [D] fp32
     or None (ones).  Returns (y, r), r None without a residual; residual_out may be the
     residual itself."""
+    rows, D = _norm_rows(x)
     if y is None:
         y = torch.empty_like(x)
     else:
         _check_cuda("y", y, x.dtype, x.shape)
-    return y, _rms_norm(x, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out, stream)
+    return y, _rms_norm(x, rows, D, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out, stream)
 
 
 _BYTE_TYPES = {"e4m3": (KDA_E4M3, torch.float8_e4m3fn), "int8": (KDA_I8, torch.int8)}
@@ -689,7 +698,7 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     if quant not in _BYTE_TYPES:
         raise ValueError(f"quant must be one of {sorted(_BYTE_TYPES)}, got {quant!r}")
     code, tdt = _BYTE_TYPES[quant]
-    _, D = _norm_rows(x)
+    rows, D = _norm_rows(x)
     if group < 0:
         raise ValueError("group must be 0, 32, 64 or 128")
     n = -(-D // group) if group else 1
@@ -698,10 +707,10 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     else:
         _check_cuda("y", y, tdt, x.shape)
     if scale is None:
-        scale = torch.empty((*x.shape[:-1], n), dtype=torch.float32, device=x.device)
+        scale = x.new_empty((*x.shape[:-1], n), dtype=torch.float32)
     else:
         _check_cuda("scale", scale, torch.float32, (*x.shape[:-1], n))
-    r = _rms_norm(x, weight, residual, eps, code, group, y, scale, residual_out, stream)
+    r = _rms_norm(x, rows, D, weight, residual, eps, code, group, y, scale, residual_out, stream)
     return y, scale, r
 
 
@@ -724,13 +733,13 @@ def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: t
     else:
         _check_cuda("grad_x", grad_x, x.dtype, x.shape)
     _check_device(x, weight, grad_y, grad_residual, grad_x, workspace)
-    grad_weight = torch.empty(D, dtype=torch.float32, device=x.device) if want_grad_weight else None
+    grad_weight = x.new_empty(D, dtype=torch.float32) if want_grad_weight else None
     a = RmsNormBackwardArgs()
     a.dtype, a.rows, a.D, a.eps = _dtype_code(x), rows, D, float(eps)
     a.x, a.weight, a.grad_y, a.grad_residual = _ptr(x), _ptr(weight), _ptr(grad_y), _ptr(grad_residual)
     a.grad_x, a.grad_weight = _ptr(grad_x), _ptr(grad_weight)
     if want_grad_weight:
-        workspace = _workspace(a, "kda_rms_norm_backward", workspace, x.device)
+        workspace = _workspace(a, "kda_rms_norm_backward", (a.dtype, rows, D), workspace, x)
     st = (_lib or load()).kda_rms_norm_backward(ctypes.byref(a), _raw_stream(stream, x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm_backward")
