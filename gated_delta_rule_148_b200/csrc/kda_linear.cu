@@ -18,7 +18,9 @@ namespace kda {
 namespace lin {
 
 constexpr int C = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;       // a chunk's outputs are a chain of short steps: 16 warps hide each other's latency
+                                   // (8 warps: gradients of 33 x 8 chunks of 64 x 128 in 93 instead of 80 us)
+constexpr int kPartThreads = 256;   // many small blocks side by side: 8 warps each split fewer operands twice (27 / 34 us)
 constexpr int kSlice = 64;          // d_v columns of a block in the parts and prefill rows kernels
 
 // ------------------------------------------------------------------ 3xTF32 products
@@ -86,12 +88,12 @@ __device__ __forceinline__ void each(float (&acc)[MT][NT][4], F f) {
 // ------------------------------------------------------------------ tiles
 // Rows [pos0, pos0 + C) of x [N, heads, d], columns [c0, c0 + W) of head `hd`, with row stride LD.  Rows
 // past `end` and pads are zeros and are not read.
-template <int W, int LD>
+template <int W, int LD, int T = kThreads>
 __device__ __forceinline__ void load_rows(float *dst, const void *x, int heads, int d, int hd, int c0, int pos0,
                                           int end, const uint8_t *mask) {
   constexpr int V = W / 4;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < C * V; i += kThreads) {
+  for (int i = threadIdx.x; i < C * V; i += T) {
     const int r = i / V, c = (i % V) * 4, pos = pos0 + r;
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
     if (pos < end && (mask == nullptr || mask[pos] != 0))
@@ -266,8 +268,8 @@ __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment
   for (int j = 0; j < chunks; ++j) {
     const int pos0 = sg.begin + (REVERSE ? chunks - 1 - j : j) * C;
     __syncthreads();
-    load_rows<DK, LK>(sk, REVERSE ? p.q : p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
-    load_rows<kSlice, LV>(sv, REVERSE ? p.d_o : p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
+    load_rows<DK, LK, kPartThreads>(sk, REVERSE ? p.q : p.k, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
+    load_rows<kSlice, LV, kPartThreads>(sv, REVERSE ? p.d_o : p.v, p.H, p.dv, h, c0, pos0, sg.end, p.mask);
     if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
     __syncthreads();
     const float a = dec.whole, *wgt = REVERSE ? dec.from : dec.to;
@@ -282,7 +284,7 @@ __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kThreads) parts_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
+__global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
                                                          float *whole, int tokens) {
   extern __shared__ float sm[];
   __shared__ Decays dec;
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *s
 
 // ------------------------------------------------------------------ prefill rows
 template <int DK>
-__global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const int *sbase, const float *start, int tokens) {
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(LinearParams p, const int *sbase, const float *start, int tokens) {
   constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
   extern __shared__ float sm[];
   __shared__ Decays dec;
@@ -350,8 +352,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
   const int hk = h / (p.H / p.Hk);
-  const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16, n0 = (warp >> 2) * 32;
-  float S[MT][4][4];                 // rows MT m0 .., columns n0 .. of the state
+  const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16, n0 = (warp >> 2) * 16;
+  float S[MT][2][4];                 // rows MT m0 .., columns n0 .. of the state
   const float *in = start + ((size_t)seg * p.H + h) * DK * p.dv + c0;
   each(S, [&](int r, int n, float &x) { x = in[(size_t)(m0 * MT + r) * p.dv + n0 + n]; });
   const int chunks = (sg.end - sg.begin + C - 1) / C;
@@ -364,21 +366,21 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
     each(S, [&](int r, int n, float &x) { sS[(m0 * MT + r) * LV + n0 + n] = x; });
     if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
     __syncthreads();
-    float o[1][4][4], A[1][4][4];
+    float o[1][2][4], A[1][2][4];
     zero(A);
     if (n0 <= m0 + 15)               // else above the diagonal
-      gemm3<1, 4, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+      gemm3<1, 2, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
                       [&](int k, int n) { return sk[(n0 + n) * LK + k]; });
     each(A, [&](int r, int n, float &x) {
       const int t = m0 + r, s = n0 + n;
       sP[t * LV + s] = s <= t ? x * pair_decay(dec, t, s) : 0.f;
     });
     zero(o);
-    gemm3<1, 4, DK>(o, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+    gemm3<1, 2, DK>(o, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
                     [&](int k, int n) { return sS[k * LV + n0 + n]; });
     each(o, [&](int r, int, float &x) { x *= dec.from[m0 + r]; });
     __syncthreads();
-    gemm3<1, 4, C>(o, [&](int r, int k) { return sP[(m0 + r) * LV + k]; },
+    gemm3<1, 2, C>(o, [&](int r, int k) { return sP[(m0 + r) * LV + k]; },
                    [&](int k, int n) { return sv[k * LV + n0 + n]; });
     each(o, [&](int r, int n, float &x) {
       const int pos = pos0 + m0 + r;
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(LinearParams p, const in
     });
     if (j + 1 < chunks) {
       each(S, [&](int, int, float &x) { x *= dec.whole; });
-      gemm3<MT, 4, C>(S, [&](int r, int k) { return sk[k * LK + m0 * MT + r] * dec.to[k]; },
+      gemm3<MT, 2, C>(S, [&](int r, int k) { return sk[k * LK + m0 * MT + r] * dec.to[k]; },
                       [&](int k, int n) { return sv[k * LV + n0 + n]; });
     }
   }
@@ -410,7 +412,7 @@ struct GradSmem {
   static constexpr int P = O + C * LV, M = P + C * LP, S = M + C * LP, END = S + C * (LV > LP ? LV : LP);
 };
 
-// x[row] += sum of f's values over the warp's columns of the row, kept per warp column in part[2][C].
+// x[row] += sum of f's values over the warp's columns of the row, kept per warp column in part[4][C].
 template <int NT, class F>
 __device__ __forceinline__ void row_sums(float (&acc)[1][NT][4], float *part, int m0, int wn, F f) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
@@ -431,16 +433,16 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const int *sbase, const float *start,
                                                         const float *dend, float *gq32, float *gk32, float *gla) {
   using L = GradSmem<DK, DV>;
-  constexpr int LK = L::LK, LV = L::LV, LP = L::LP, HALVES = DK / 64, NV = DV / 16;
+  constexpr int LK = L::LK, LV = L::LV, LP = L::LP, HALVES = DK / 64, NV = DV / 32;
   extern __shared__ float sm[];
   __shared__ Decays dec;
-  __shared__ float r_part[2 * C], k_part[2 * C], pair_sum[C], red[kThreads / 32];
+  __shared__ float r_part[4 * C], k_part[4 * C], pair_sum[C], red[kThreads / 32];
   if (device_error_latched(p.err)) return;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
   const int hk = h / (p.H / p.Hk), pos0 = sg.begin, tid = threadIdx.x;
-  const int warp = tid >> 5, m0 = (warp & 3) * 16, wn = warp >> 2, n0 = wn * 32;
+  const int warp = tid >> 5, m0 = (warp & 3) * 16, wn = warp >> 2, n0 = wn * 16;
   float *sq = sm + L::Q, *sk = sm + L::K, *sv = sm + L::V, *so = sm + L::O, *sP = sm + L::P, *sM = sm + L::M,
         *sS = sm + L::S;
   load_rows<DK, LK>(sq, p.q, p.Hk, DK, hk, 0, pos0, sg.end, p.mask);
@@ -448,16 +450,16 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   load_rows<DV, LV>(sv, p.v, p.H, DV, h, 0, pos0, sg.end, p.mask);
   load_rows<DV, LV>(so, p.d_o, p.H, DV, h, 0, pos0, sg.end, p.mask);
   if (warp == 0) chunk_decays(dec, p, pos0, sg.end, h);
-  if (tid < 2 * C) r_part[tid] = k_part[tid] = 0.f;
+  if (tid < 4 * C) r_part[tid] = k_part[tid] = 0.f;
   __syncthreads();
   {
-    float A[1][4][4], G[1][4][4];
+    float A[1][2][4], G[1][2][4];
     zero(A);
     zero(G);
     if (n0 <= m0 + 15) {
-      gemm3<1, 4, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
+      gemm3<1, 2, DK>(A, [&](int r, int k) { return sq[(m0 + r) * LK + k]; },
                       [&](int k, int n) { return sk[(n0 + n) * LK + k]; });
-      gemm3<1, 4, DV>(G, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
+      gemm3<1, 2, DV>(G, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
                       [&](int k, int n) { return sv[(n0 + n) * LV + k]; });
     }
     each(G, [&](int r, int n, float &x) {
@@ -500,13 +502,13 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
       *reinterpret_cast<float4 *>(sS + r * LV + c) = x;
     }
     __syncthreads();
-    float acc[1][4][4];
+    float acc[1][2][4];
     zero(acc);
-    gemm3<1, 4, DV>(acc, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
+    gemm3<1, 2, DV>(acc, [&](int r, int k) { return so[(m0 + r) * LV + k]; },
                     [&](int k, int n) { return sS[(n0 + n) * LV + k]; });
     each(acc, [&](int r, int, float &x) { x *= dec.from[m0 + r]; });
     row_sums(acc, r_part, m0, wn, [&](int r, int n, float x) { return x * sq[(m0 + r) * LK + k0 + n0 + n]; });
-    gemm3<1, 4, C>(acc, [&](int r, int k) { return sM[(m0 + r) * LP + k]; },
+    gemm3<1, 2, C>(acc, [&](int r, int k) { return sM[(m0 + r) * LP + k]; },
                    [&](int k, int n) { return sk[k * LK + k0 + n0 + n]; });
     each(acc, [&](int r, int n, float &x) {
       const int pos = pos0 + m0 + r;
@@ -521,11 +523,11 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
     }
     __syncthreads();
     zero(acc);
-    gemm3<1, 4, DV>(acc, [&](int r, int k) { return sv[(m0 + r) * LV + k]; },
+    gemm3<1, 2, DV>(acc, [&](int r, int k) { return sv[(m0 + r) * LV + k]; },
                     [&](int k, int n) { return sS[(n0 + n) * LV + k]; });
     each(acc, [&](int r, int, float &x) { x *= dec.to[m0 + r]; });
     row_sums(acc, k_part, m0, wn, [&](int r, int n, float x) { return x * sk[(m0 + r) * LK + k0 + n0 + n]; });
-    gemm3<1, 4, C>(acc, [&](int r, int k) { return sM[k * LP + m0 + r]; },
+    gemm3<1, 2, C>(acc, [&](int r, int k) { return sM[k * LP + m0 + r]; },
                    [&](int k, int n) { return sq[k * LK + k0 + n0 + n]; });
     each(acc, [&](int r, int n, float &x) {
       const int pos = pos0 + m0 + r;
@@ -534,14 +536,14 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
       else store_elem<false>(p.gk, ((size_t)pos * p.H + h) * DK + k0 + n0 + n, x);
     });
     gemm3<1, NV, 64>(av, [&](int r, int k) { return sk[(m0 + r) * LK + k0 + k]; },
-                     [&](int k, int n) { return sS[k * LV + wn * (DV / 2) + n]; });
+                     [&](int k, int n) { return sS[k * LV + wn * (DV / 4) + n]; });
   }
   each(av, [&](int r, int, float &x) { x *= dec.to[m0 + r]; });
   gemm3<1, NV, C>(av, [&](int r, int k) { return sP[k * LP + m0 + r]; },
-                  [&](int k, int n) { return so[k * LV + wn * (DV / 2) + n]; });
+                  [&](int k, int n) { return so[k * LV + wn * (DV / 4) + n]; });
   each(av, [&](int r, int n, float &x) {
     const int pos = pos0 + m0 + r;
-    if (pos < sg.end) store_elem<false>(p.gv, ((size_t)pos * p.H + h) * DV + wn * (DV / 2) + n, x);
+    if (pos < sg.end) store_elem<false>(p.gv, ((size_t)pos * p.H + h) * DV + wn * (DV / 4) + n, x);
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(0xFFFFFFFFu, through, o);
@@ -550,8 +552,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   if (tid < C && pos0 + tid < sg.end) {
     float x = 0.f, r = 0.f, k = 0.f;
     for (int i = 0; i < kThreads / 32; ++i) x += red[i];
-    for (int t = C - 1; t >= tid; --t) r += r_part[t] + r_part[C + t];
-    for (int s = 0; s < tid; ++s) k += k_part[s] + k_part[C + s];
+    for (int t = C - 1; t >= tid; --t) r += (r_part[t] + r_part[C + t]) + (r_part[2 * C + t] + r_part[3 * C + t]);
+    for (int s = 0; s < tid; ++s) k += (k_part[s] + k_part[C + s]) + (k_part[2 * C + s] + k_part[3 * C + s]);
     const bool pad = p.mask != nullptr && p.mask[pos0 + tid] == 0;
     const float g = pad ? 0.f : pair_sum[tid] + r + k + dec.whole * x;
     // one decay per head: [H, N] for the sum that follows
@@ -620,7 +622,7 @@ cudaError_t launch_parts(const LinearParams &p, const int *sbase, float *part, f
   const cudaError_t e = allow_smem<parts_kernel<DK>>(parts_smem<DK>());
   if (e != cudaSuccess) return e;
   if (blocks)
-    parts_kernel<DK><<<dim3((unsigned)blocks, rpart ? 2 : 1), kThreads, parts_smem<DK>(), s>>>(p, sbase, part, rpart,
+    parts_kernel<DK><<<dim3((unsigned)blocks, rpart ? 2 : 1), kPartThreads, parts_smem<DK>(), s>>>(p, sbase, part, rpart,
                                                                                             whole, tokens);
   return cudaGetLastError();
 }
