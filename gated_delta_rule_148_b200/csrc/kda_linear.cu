@@ -140,26 +140,32 @@ __device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
 // Checks cu_seqlens (nothing else runs if it is invalid), takes the number of chunks in a segment, lo .. hi, and fills
 // the segment table, longest segments first.  In the time of a chunk on one SM: a segment costs its chunks and about a half
 // more (its state in and out), and its share of the state half of up to six chunks (a share ends where the decays
-// are 0 in fp32).  Measured with 1, 2, .. 64 chunks on 131072 tokens and on a batch of 63 to 4099 tokens: the
-// best of both, 1.13 ms (32 chunks) and 116 us (16).  The lengths are known here only.
+// are 0 in fp32).  The longest run over the SMs is no shorter than the mean, nor than r + 1 times the segment in place
+// r x SMs, since one SM has r + 1 of the segments up to there.  Against the best of 1, 2, .. 64 chunks, measured one by
+// one, the count so taken costs 0 to 5 % more on nine batches of 2048 to 32768 tokens and on 131072 tokens.  The
+// lengths are known here only.
 constexpr int kMaxPer = 64;
 constexpr int kCached = 1024;      // sequences whose tables fit in shared memory
 __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int chunk, int lo, int hi, int sms) {
-  __shared__ int tot[32], carry, bad, slot[kMaxPer + 1], s_cu[kCached + 1], s_base[kCached + 1];
+  __shared__ int tot[32], carry, bad, most, slot[kMaxPer + 1], s_cu[kCached + 1], s_base[kCached + 1];
+  __shared__ int lengths[32][kMaxPer + 1];
   __shared__ unsigned best;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  if (tid == 0) { carry = 0; bad = 0; best = 0xFFFFFFFFu; }
+  if (tid == 0) { carry = 0; bad = 0; most = lo; best = 0xFFFFFFFFu; }
   if (tid <= kMaxPer) slot[tid] = 0;
   __syncthreads();
   if (device_error_latched(p.err)) return;
   const bool cached = p.num_seqs <= kCached;
-  int wrong = 0;
+  int wrong = 0, top = 0;
   for (int i = tid; i <= p.num_seqs; i += 1024) {
-    const int c = p.cu[i];
+    const int c = p.cu[i], d = i > 0 ? p.cu[i - 1] : 0;
     if (cached) s_cu[i] = c;
-    if (c < 0 || c > p.N || (i == 0 && c != 0) || (i == p.num_seqs && c != p.N) || (i > 0 && p.cu[i - 1] > c)) wrong = 1;
+    if (c < 0 || c > p.N || (i == 0 && c != 0) || (i == p.num_seqs && c != p.N) || d > c) wrong = 1;
+    top = max(top, c - d);
   }
   if (wrong) atomicOr(&bad, 1);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (lane == 0 && top > 0) atomicMax(&most, (top + chunk - 1) / chunk);
   __syncthreads();
   if (bad) {
     if (tid == 0) atomicOr(p.err, ERR_BIT_CHECK);
@@ -167,21 +173,33 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
   }
   const int *cu = cached ? s_cu : p.cu, *base = cached ? s_base : sbase;
   auto chunks = [&](int b) { return (cu[b + 1] - cu[b] + chunk - 1) / chunk; };
+  hi = min(hi, most);      // chunks of the longest sequence (lo at least)
   if (hi > lo) {
     for (int per = lo + w; per <= hi; per += 32) {      // a warp for each count
-      int all = 0, segs = 0, full = 0;
+      for (int n = lane; n <= kMaxPer; n += 32) lengths[w][n] = 0;
+      __syncwarp();
+      int all = 0, segs = 0;
       for (int b = lane; b < p.num_seqs; b += 32) {
-        const int n = chunks(b), f = n / per;
+        const int n = chunks(b), f = n / per, rest = n - f * per;
         all += n;
-        full += f;
-        segs += f + (n > f * per);
+        segs += f + (rest > 0);
+        if (f > 0) atomicAdd(&lengths[w][per], f);
+        if (rest > 0) atomicAdd(&lengths[w][rest], 1);
       }
+      __syncwarp();
       all = __reduce_add_sync(0xFFFFFFFFu, all);
       segs = __reduce_add_sync(0xFFFFFFFFu, segs);
-      full = __reduce_add_sync(0xFFFFFFFFu, full);
-      const float heads = (float)p.H / (float)sms;
-      const float mean = ((float)all + 0.5f * (float)segs) * heads, longest = ceilf((float)full * heads) * ((float)per + 0.5f);
-      const float cost = fmaxf(mean, longest) + ceilf((float)segs * heads) * 0.5f * (float)min(per, 6);
+      const int at = lane * sms / p.H;                  // this lane: r = lane
+      int place = 0, longest = 0;
+#pragma unroll 8
+      for (int n = per; n > 0; --n) {
+        place += lengths[w][n];
+        longest = longest == 0 && place > at ? n : longest;
+      }
+      const float heads = (float)p.H / (float)sms, mean = ((float)all + 0.5f * (float)segs) * heads;
+      int run = (lane + 1) * (longest > 0 ? 2 * longest + 1 : 0);      // in halves of a chunk
+      run = __reduce_max_sync(0xFFFFFFFFu, run);
+      const float cost = fmaxf(mean, 0.5f * (float)run) + ceilf((float)segs * heads) * 0.5f * (float)min(per, 6);
       // quarters of a chunk's time in 24 bits, then the count
       if (lane == 0) atomicMin(&best, (unsigned)fminf(4.f * cost, 16e6f) << 8 | (unsigned)per);
     }
@@ -237,13 +255,16 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
     atomicAdd(&slot[n], 1);
   }
   __syncthreads();
-  if (tid == 0) {
-    int at = 0;
-    for (int n = kMaxPer; n > 0; --n) {
-      const int c = slot[n];
-      slot[n] = at;
-      at += c;
+  if (w == 0) {      // places of the lengths, from the longest: lane's are kMaxPer - 2 lane and the one before it
+    const int a = slot[kMaxPer - 2 * lane], b = slot[kMaxPer - 2 * lane - 1];
+    int x = a + b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
     }
+    slot[kMaxPer - 2 * lane] = x - a - b;
+    slot[kMaxPer - 2 * lane - 1] = x - b;
   }
   __syncthreads();
   for (int i = tid; i < segs; i += 1024) {
