@@ -182,6 +182,31 @@ cudaError_t launch_norm(const NormParams &p, bool bf16, int out, cudaStream_t s)
 size_t norm_backward_workspace(long long rows, int D);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, bool bf16, cudaStream_t s);
 
+// ---------------------------------------------------------------- a call's kernels, one after another
+// A kernel launched with launch_next may be placed on the SMs while the one before it still runs (its launch then costs
+// nothing); it begins with after_previous(), which returns when that kernel is complete and its writes are visible.
+// A call's first kernel is launched plainly, so that calls do not overlap.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A &&...args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- helpers
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
   return __uint_as_float(((unsigned)h) << 16);

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
   if (tid == 0) { carry = 0; bad = 0; most = lo; best = 0xFFFFFFFFu; }
   if (tid <= kMaxPer) slot[tid] = 0;
   __syncthreads();
+  let_next_start();
   if (device_error_latched(p.err)) return;
   const bool cached = p.num_seqs <= kCached;
   int wrong = 0, top = 0;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, con
                                                          float *whole, int tokens) {
   extern __shared__ float sm[];
   __shared__ Decays dec;
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
@@ -324,6 +326,7 @@ template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + k
 // z = 0 forwards from init_state, 1 backwards from the final state's gradient.
 __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
                                                     const float *whole) {
+  after_previous();
   if (device_error_latched(p.err)) return;
   const bool back = blockIdx.z != 0;
   const size_t bh = blockIdx.x, per = (size_t)p.dk * p.dv;
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(Linear
   extern __shared__ float sm[];
   __shared__ Decays dec;
   float *sq = sm, *sk = sq + C * LK, *sv = sk + C * LK, *sS = sv + C * LV, *sP = sS + DK * LV;
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
@@ -458,6 +462,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   extern __shared__ float sm[];
   __shared__ Decays dec;
   __shared__ float r_part[4 * C], k_part[4 * C], pair_sum[C], red[kThreads / 32];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
   if (seg >= sbase[p.num_seqs]) return;
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
 // dq, dk of a key head: the value heads' fp32 gradients added in order.  Thread: 4 columns.
 template <bool BF16>
 __global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float *gq32, const float *gk32) {
+  after_previous();
   if (device_error_latched(p.err)) return;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = p.dk / 4;
   if (i >= (size_t)p.N * p.Hk * per) return;
@@ -608,6 +614,7 @@ __global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float 
 // The gradient of a head's constant log_alpha: the sum over the tokens, in 64 bits and a fixed order.
 __global__ void __launch_bounds__(1024) head_decay_kernel(LinearParams p, const float *gla) {
   __shared__ double s[32];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int h = blockIdx.x;
   double a = 0.0;
@@ -642,10 +649,9 @@ cudaError_t launch_parts(const LinearParams &p, const int *sbase, float *part, f
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<parts_kernel<DK>>(parts_smem<DK>());
   if (e != cudaSuccess) return e;
-  if (blocks)
-    parts_kernel<DK><<<dim3((unsigned)blocks, rpart ? 2 : 1), kPartThreads, parts_smem<DK>(), s>>>(p, sbase, part, rpart,
-                                                                                            whole, tokens);
-  return cudaGetLastError();
+  if (blocks == 0) return cudaSuccess;
+  return launch_next(parts_kernel<DK>, dim3((unsigned)blocks, rpart ? 2 : 1), kPartThreads, parts_smem<DK>(), s, p, sbase,
+                     part, rpart, whole, tokens);
 }
 cudaError_t launch_parts_chain(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole,
                                size_t segs, int tokens, cudaStream_t s) {
@@ -660,8 +666,8 @@ cudaError_t launch_rows(const LinearParams &p, const int *sbase, const float *st
                         cudaStream_t s) {
   const cudaError_t e = allow_smem<rows_kernel<DK>>(rows_smem<DK>());
   if (e != cudaSuccess) return e;
-  rows_kernel<DK><<<(unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, rows_smem<DK>(), s>>>(p, sbase, start, tokens);
-  return cudaGetLastError();
+  return launch_next(rows_kernel<DK>, (unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, rows_smem<DK>(), s, p, sbase,
+                     start, tokens);
 }
 
 template <int DK, int DV>
@@ -670,8 +676,7 @@ cudaError_t launch_grad(const LinearParams &p, const int *sbase, const float *st
   constexpr size_t smem = (size_t)GradSmem<DK, DV>::END * 4;
   const cudaError_t e = allow_smem<grad_kernel<DK, DV>>(smem);
   if (e != cudaSuccess) return e;
-  grad_kernel<DK, DV><<<(unsigned)(segs * p.H), kThreads, smem, s>>>(p, sbase, start, dend, gq32, gk32, gla);
-  return cudaGetLastError();
+  return launch_next(grad_kernel<DK, DV>, (unsigned)(segs * p.H), kThreads, smem, s, p, sbase, start, dend, gq32, gk32, gla);
 }
 cudaError_t launch_grad_dims(const LinearParams &p, const int *sbase, const float *start, const float *dend,
                              float *gq32, float *gk32, float *gla, size_t segs, cudaStream_t s) {
@@ -692,8 +697,8 @@ cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int chunk, int
 cudaError_t launch_linear_chain(const LinearParams &p, const int *sbase, float *part, float *rpart, const float *whole,
                                 cudaStream_t s) {
   const unsigned nx = (unsigned)(p.dk * p.dv / 1024);
-  lin::chain_kernel<<<dim3((unsigned)(p.num_seqs * p.H), nx, rpart ? 2 : 1), 256, 0, s>>>(p, sbase, part, rpart, whole);
-  return cudaGetLastError();
+  return launch_next(lin::chain_kernel, dim3((unsigned)(p.num_seqs * p.H), nx, rpart ? 2 : 1), 256, 0, s, p, sbase, part,
+                     rpart, whole);
 }
 
 size_t linear_prefill_workspace(const LinearParams &p, bool bf16) {
@@ -765,13 +770,12 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
     if (shared) {
       const size_t n = ((size_t)p.N * p.Hk * (p.dk / 4) + 255) / 256;
       if (n > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-      if (bf16) share_kernel<true><<<dim3((unsigned)n, 2), 256, 0, s>>>(p, gq32, gk32);
-      else share_kernel<false><<<dim3((unsigned)n, 2), 256, 0, s>>>(p, gq32, gk32);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = bf16 ? launch_next(share_kernel<true>, dim3((unsigned)n, 2), 256, 0, s, p, gq32, gk32)
+               : launch_next(share_kernel<false>, dim3((unsigned)n, 2), 256, 0, s, p, gq32, gk32);
+      if (e != cudaSuccess) return e;
     }
   }
-  if (p.decay_head) head_decay_kernel<<<(unsigned)p.H, 1024, 0, s>>>(p, gla);
-  return cudaGetLastError();
+  return p.decay_head ? launch_next(head_decay_kernel, (unsigned)p.H, 1024, 0, s, p, gla) : cudaSuccess;
 }
 
 }  // namespace kda

@@ -39,6 +39,7 @@ struct Table {
 };
 
 __global__ void __launch_bounds__(256) table_kernel(LinearParams p, const int *sbase, Table *tables) {
+  after_previous();
   if (device_error_latched(p.err)) return;
   const size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= (size_t)sbase[p.num_seqs] * p.H) return;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kSweepThreads, 1)
 sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const Table *tables, float *through) {
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
@@ -375,6 +377,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
             float *gk32, float *gla) {
   using L = GradSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
@@ -919,19 +922,18 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   if (e == cudaSuccess) e = lin::allow_smem<grad_kernel<DK, DV>>(grad_smem);
   if (e != cudaSuccess) return e;
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
-  if (items > 0) table_kernel<<<(unsigned)((items + 7) / 8), 256, 0, s>>>(p, sbase, tables);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  sweep_kernel<DK, DV, false><<<(unsigned)sweeps, kSweepThreads, fwd_smem, s>>>(p, mf, sbase, tables, nullptr);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  sweep_kernel<DK, DV, true><<<(unsigned)sweeps, kSweepThreads, rev_smem, s>>>(p, mr, sbase, tables, through);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.N == 0) return e;
+  if (items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
+  if (e == cudaSuccess)
+    e = launch_next(sweep_kernel<DK, DV, false>, (unsigned)sweeps, kSweepThreads, fwd_smem, s, p, mf, sbase, tables, nullptr);
+  if (e == cudaSuccess)
+    e = launch_next(sweep_kernel<DK, DV, true>, (unsigned)sweeps, kSweepThreads, rev_smem, s, p, mr, sbase, tables, through);
+  if (e != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
-  grad_kernel<DK, DV><<<grid, kGradThreads, grad_smem, s>>>(p, mg, sbase, through,
-                                             shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr,
-                                             shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr, gla);
-  return cudaGetLastError();
+  return launch_next(grad_kernel<DK, DV>, grid, kGradThreads, grad_smem, s, p, mg, sbase, through,
+                     shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr,
+                     shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr, gla);
 }
 
 }  // namespace lintc

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kPartsThreads, 1)
 parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *whole) {
   using L = PartsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, const float *start) {
   using L = RowsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
+  after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
@@ -747,11 +749,11 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
   cudaError_t e = lin::allow_smem<parts_kernel<DK, DV>>(PartsSmem<DK, DV>::END);
   if (e == cudaSuccess) e = lin::allow_smem<rows_kernel<DK, DV>>(RowsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
-  if (grid) parts_kernel<DK, DV><<<grid, kPartsThreads, PartsSmem<DK, DV>::END, s>>>(p, maps, sbase, whole);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = launch_linear_chain(p, sbase, part, nullptr, whole, s)) != cudaSuccess) return e;
-  if (grid) rows_kernel<DK, DV><<<grid, kRowsThreads, RowsSmem<DK, DV>::END, s>>>(p, maps, sbase, part);
-  return cudaGetLastError();
+  if (grid) e = launch_next(parts_kernel<DK, DV>, grid, kPartsThreads, PartsSmem<DK, DV>::END, s, p, maps, sbase, whole);
+  if (e == cudaSuccess) e = launch_linear_chain(p, sbase, part, nullptr, whole, s);
+  if (e == cudaSuccess && grid)
+    e = launch_next(rows_kernel<DK, DV>, grid, kRowsThreads, RowsSmem<DK, DV>::END, s, p, maps, sbase, part);
+  return e;
 }
 
 }  // namespace lintc

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(block_threads(TPR), back_blocks_per_sm(TPR, BF
   constexpr bool AHEAD = TPR < 1024;      // the widest rows have no registers for a second one
   __shared__ float red[2 * 32];
   __shared__ float sum[GROUPS > 1 ? GROUPS * TPR * VPT * 8 : 1];
+  let_next_start();
   if (device_error_latched(p.err)) return;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int nvec = p.D / 8;
@@ -369,6 +370,7 @@ __global__ void __launch_bounds__(block_threads(TPR), back_blocks_per_sm(TPR, BF
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int parts, int D, float *dw,
                                                        const unsigned *err) {
   __shared__ float s[32][33];
+  after_previous();
   if (device_error_latched(err)) return;
   const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
   float a = 0.f;
@@ -416,8 +418,7 @@ cudaError_t launch_back(const NormBackwardParams &p, bool bf16, cudaStream_t s) 
   else norm_backward_kernel<TPR, VPT, false><<<grid, NT, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part == nullptr) return e;
-  norm_dw_kernel<<<(unsigned)((p.D + 31) / 32), dim3(32, 32), 0, s>>>(p.part, (int)grid, p.D, p.dw, p.err);
-  return cudaGetLastError();
+  return launch_next(norm_dw_kernel, (unsigned)((p.D + 31) / 32), dim3(32, 32), 0, s, p.part, (int)grid, p.D, p.dw, p.err);
 }
 
 }  // namespace norm
