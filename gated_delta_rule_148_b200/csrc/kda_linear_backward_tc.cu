@@ -161,10 +161,10 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
           ++states;
         }
       }
-      if (!ok) {      // loads in flight land before the block ends
-        for (int i = 0; i < loaded; ++i) mbar_wait(full + i % kSweepStages, (i / kSweepStages) & 1, 2000000);
-        for (int i = 0; i < states; ++i) mbar_wait(s_full + (i & 1), (i >> 1) & 1, 2000000);
-      }
+      // loads in flight land before the block ends, whoever gave up
+      for (int i = loaded > kSweepStages ? loaded - kSweepStages : 0; i < loaded; ++i)
+        mbar_wait(full + i % kSweepStages, (i / kSweepStages) & 1, kDrainCycles);
+      for (int i = states > 2 ? states - 2 : 0; i < states; ++i) mbar_wait(s_full + (i & 1), (i >> 1) & 1, kDrainCycles);
     }
   } else if (warp == 8) {
     if (lane == 0) {
@@ -185,7 +185,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         mma_commit(done + sl);
       }
       mma_commit(drain);
-      mbar_wait(drain, 0, p.wait_cycles);
+      mbar_wait(drain, 0, kDrainCycles);
     }
   } else if (warp == 10) {
     if (lane == 0) {
@@ -517,11 +517,11 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         store_v();
       }
       bulk_wait_all();
-      if (!ok)      // loads in flight (of this item and the one before) land before the block ends
-        for (int x = 0; x < 10; ++x) {
-          uint64_t *bar = x < 2 ? full : x_full + (x >> 1) - 1;
-          mbar_wait(bar, (it + 1 + x) & 1, 2000000);
-        }
+      // loads in flight (the last item's, and those of one begun) land before the block ends, whoever gave up
+      for (int i = it > 0 ? it - 1 : 0; i < it + !ok; ++i) {
+        mbar_wait(full, i & 1, kDrainCycles);
+        for (int x = 0; x < 4; ++x) mbar_wait(x_full + x, i & 1, kDrainCycles);
+      }
     }
   } else if (warp == 16) {
     // ---------------- MMAs
@@ -604,7 +604,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
         mma_commit(dv_done);
       }
       mma_commit(drain);
-      mbar_wait(drain, 0, p.wait_cycles);
+      mbar_wait(drain, 0, kDrainCycles);
     }
   } else if (warp == 18) {
     // ---------------- decays

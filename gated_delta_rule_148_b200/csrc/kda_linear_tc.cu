@@ -22,7 +22,7 @@ namespace kda {
 namespace lintc {
 
 // Wait sites reported with a timeout.
-enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 51 };
+enum : unsigned { SITE_PARTS = 41, SITE_ROWS = 55 };
 
 struct Maps {
   CUtensorMap q, k, v, o, part;
@@ -156,10 +156,10 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
           ++n;
         }
       }
-      if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i < loaded; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+      // loads in flight land before the block ends, whoever gave up
+      for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, kDrainCycles);
       mma_commit(drain);
-      mbar_wait(drain, 0, p.wait_cycles);
+      mbar_wait(drain, 0, kDrainCycles);
     }
   } else if (warp == 17) {
     // ---------------- the plan
@@ -290,16 +290,19 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
         }
       fence_async_smem();
       mbar_arrive(staged);
+      bool gone = true;
       if (tid == 0) {
-        if (!wait(staged, n, SITE_PARTS + 4)) break;
+        gone = wait(staged, n, SITE_PARTS + 10);
+        if (gone) {
 #pragma unroll
-        for (int cb = 0; cb < DV / 32; ++cb)
-          tma_store_3d(&maps.part, smem_u32(sm + L::W) + cb * DK * 128, cb * 32, 0, item * DK);
-        bulk_commit();
-        bulk_wait_read();
-        mbar_arrive(out_free);
+          for (int cb = 0; cb < DV / 32; ++cb)
+            tma_store_3d(&maps.part, smem_u32(sm + L::W) + cb * DK * 128, cb * 32, 0, item * DK);
+          bulk_commit();
+          bulk_wait_read();
+          mbar_arrive(out_free);
+        }
       }
-      __syncwarp();
+      if (!__all_sync(0xFFFFFFFFu, gone)) break;
       ++n;
     }
     if (tid == 0) bulk_wait_all();
@@ -410,8 +413,8 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
       }
       for (int x = step > 2 ? step - 2 : 0; x < step; ++x) store(x & 1, x);
       bulk_wait_all();
-      if (!ok)      // loads in flight land before the block ends
-        for (int i = 0; i <= step; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, 2000000);
+      // loads in flight (a begun chunk's too) land before the block ends, whoever gave up
+      for (int i = step > 2 ? step - 2 : 0; i < step + !ok; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, kDrainCycles);
     }
   } else if (warp == 16) {
     // ---------------- MMAs: P V, Q S, the next chunk's A, then S's update, so that the next P is on its way meanwhile
@@ -475,7 +478,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
         }
       }
       mma_commit(drain);
-      mbar_wait(drain, 0, p.wait_cycles);
+      mbar_wait(drain, 0, kDrainCycles);
     }
   } else if (warp == 18) {
     // ---------------- decays; the next chunk's are loaded a chunk ahead

@@ -16,6 +16,7 @@ using namespace tc;
 using lin::Segment;
 
 constexpr int C = 128;      // rows of a chunk
+constexpr long long kDrainCycles = 2000000;      // for what is in flight when a block ends
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");

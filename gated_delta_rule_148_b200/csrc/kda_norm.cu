@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(block_threads(TPR), blocks_per_sm(TPR, BF16)) 
           m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
           m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         }
-        const float most = max_nan(m, kTiny), inv = __fdividef(kMost, most);
+        const float most = max_nan(m, kTiny), inv = kMost / most;
         if (row < p.rows && vec < nvec) {
           float z[8];
 #pragma unroll

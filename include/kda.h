@@ -349,7 +349,9 @@ kda_status kda_prefill_backward(const kda_backward_args *args, void *stream);
  *                overlap on the GPU need workspaces of their own.
  * Numerics: products of bf16 inputs are accumulated in fp32; for o the weights
  * q.k a..a and the state are rounded to bf16 once as operands; final_state keeps fp32
- * accuracy.  fp32 inputs keep fp32 accuracy throughout.
+ * accuracy.  fp32 inputs keep fp32 accuracy throughout.  Decays below 2^-126 count as 0.
+ * The batch's lengths decide how its sequences are cut into segments, and with that the
+ * order of the sums; the same lengths give the same bits.
  */
 typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1 } kda_decay;
 
@@ -421,6 +423,9 @@ kda_status kda_linear_decode(const kda_linear_decode_args *args, void *stream);
  *   workspace        kda_linear_prefill_backward_workspace_size() bytes, 256-byte aligned.
  * Sums over shared heads and tokens are taken in a fixed order: the same call gives
  * the same bits.
+ * Numerics with bf16 inputs: on the way to grad_q, grad_k and grad_v the weights, the
+ * states and their gradients are rounded to bf16 once as operands; grad_log_alpha and
+ * grad_init_state take them as two and three bf16 parts (2^-16, 2^-24).
  */
 typedef struct {
   kda_dtype dtype;
@@ -468,7 +473,8 @@ kda_status kda_linear_prefill_backward(const kda_linear_backward_args *args, voi
  *                group of that many columns (the last may be short).
  *   scale        8-bit output: fp32 [rows, 1] or [rows, ceil(D / group)]:
  *                max(max|y|, 2^-100) / 448 (e4m3) or / 127 (int8), and the stored value is
- *                y / scale rounded to nearest even.  A NaN in a group makes its scale NaN.
+ *                y / scale (as y times the reciprocal of scale, both in fp32) rounded to nearest
+ *                even.  A NaN in a group makes its scale NaN.
  *   residual_out [rows, D] r, or NULL; needs residual; may be the same pointer as residual.
  * Outputs may not otherwise overlap an input or each other.  Allocates nothing.
  */
@@ -534,8 +540,8 @@ kda_status kda_get_device_status(void *stream);
  *                or written out of bounds and the call's outputs are left
  *                unspecified.
  *   wait_cycles  the limit, in SM clock cycles, of every bounded wait in later
- *                prefill calls; <= 0 restores the default (about 2 s).
- * Process-wide and read at each kda_prefill call; meant for tests only.
+ *                prefill and linear-attention calls; <= 0 restores the default (about 2 s).
+ * Process-wide and read at each call; meant for tests only.
  * Returns KDA_ERR_INVALID_ARG for an unknown fault bit.
  */
 #define KDA_FAULT_STARVE_STATE_LOADS 1
@@ -552,7 +558,9 @@ kda_status kda_debug_set_fault(int fault, long long wait_cycles);
  * release (loading side); single-kernel tensor-core prefill: 21-26 (its six
  * waits in program order); chunks of 128 / 256: the state pass uses 11-14 as
  * above (11 any item tile) and 16 for the U_v block, the merge kernels 31
- * (operand loads), 32 and 33 (their two product groups).
+ * (operand loads), 32 and 33 (their two product groups); linear attention in bf16:
+ * 41-51 a segment's share of the state, 55-69 a segment's outputs, 71-80 the backward
+ * pass's states, 91-117 its gradients.
  */
 int kda_debug_timeout_site(void *stream);
 

@@ -317,3 +317,40 @@ def test_offsets_past_31_bits():
     step = 2 * (lib.F32 + 2 * lib.HALF_BF16)
     assert ((o[N - tail:].float() - o2.float()).abs() <= step * mo + 1e-30).all()
     assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_short_sequences_and_a_long_one(dtype):
+    """More sequences than the plan keeps in shared memory, most of them empty or a few tokens long."""
+    lengths = [i % 4 for i in range(1100)] + [900]
+    c = lib.case(12, lengths, 1, 1, 64, 64, dtype)
+    _check_prefill(c)
+    _check_backward(c)
+
+
+@pytest.mark.parametrize("lengths", [[3300, 260, 2000, 129, 1, 0, 700], [128 * 9, 128 * 9 + 1, 128 * 8 - 1]], ids=["mixed", "near"])
+def test_segments_of_mixed_lengths(lengths):
+    """Segments of several chunks, taken longest first: each state lands where it belongs, and twice the same bits."""
+    c = lib.case(13, lengths, 16, 4, 128, 64, "bf16", pads=0.05)
+    o, s = _check_prefill(lib.spoil_pads(c))
+    o2, s2 = _prefill(c)
+    assert torch.equal(o, o2) and torch.equal(s, s2)
+
+
+def test_waits_that_run_out_are_reported():
+    """A limit shorter than any load: the call returns, its status says so, and the next calls are whole."""
+    c = lib.case(14, [500, 300], 4, 2, 128, 128, "bf16")
+    d = lib.to_cuda(c)
+    kda.debug_set_fault(0, 50)
+    try:
+        kda.linear_prefill(d["q"], d["k"], d["v"], d["log_alpha"], d["cu_seqlens"], init_state=d["init_state"])
+        assert kda.get_device_status() == kda.KDA_ERR_DEVICE_TIMEOUT
+        assert 41 <= kda.debug_timeout_site() <= 69
+        kda.linear_prefill_backward(d["q"], d["k"], d["v"], d["log_alpha"], d["cu_seqlens"], d["grad_o"],
+                                    init_state=d["init_state"])
+        assert kda.get_device_status() == kda.KDA_ERR_DEVICE_TIMEOUT
+        assert 71 <= kda.debug_timeout_site() <= 117
+    finally:
+        kda.debug_set_fault(0, 0)
+    _check_prefill(c)
+    _check_backward(c)

@@ -1,8 +1,8 @@
 """GPU parity of the RMS norm (residual, 8-bit outputs, backward) against 64-bit formulas.
 
-Bounds, relative to the value: fp32 arithmetic has a sum of D squares in a tree of D / 8 threads (at
-most 8 * 2 + 10 roundings of positive terms), rsqrt (2 units), three products: below 32 roundings of 2^-24, so
-F32 = 2^-19; a bf16 output adds 2^-8, e4m3 2^-4 (2^-10 absolute below 2^-6), int8 1/2 a unit."""
+Bounds, relative to the value: fp32 arithmetic has a sum of D squares, up to 32 in a thread and a tree over
+the threads (at most 32 + 10 roundings of positive terms, halved by the root), rsqrt (2 units), three products: below
+32 roundings of 2^-24, so F32 = 2^-19; a bf16 output adds 2^-8, e4m3 2^-4 (2^-10 absolute below 2^-6), int8 1/2 a unit."""
 import pytest
 import torch
 
@@ -154,3 +154,14 @@ def test_leading_dimensions_captured_call_and_many_rows():
     big[-1, ::2] = 3.0
     y, _ = kda.rms_norm(big, None, eps=0.0, y=big.new_empty(rows, 1024))
     assert torch.all(y[:-1] == 1) and torch.equal(y[-1], kda.rms_norm(big[-1:].contiguous(), None, eps=0.0)[0][0])
+
+
+@pytest.mark.parametrize("quant", ["e4m3", "int8"])
+def test_bytes_of_values_near_the_type_s_ends(quant):
+    """Outputs near fp32's largest and near 2^-100: the top of each group is stored as the type's largest value."""
+    top = 448.0 if quant == "e4m3" else 127.0
+    x = torch.ones(3, 64, device="cuda")
+    for size in (2.5e38, 1.0, 2.0 ** -99):
+        y8, scale, _ = kda.rms_norm_quant(x, torch.full((64,), size, device="cuda"), eps=0.0, quant=quant, group=32)
+        assert torch.all(y8.float() == top)
+        assert torch.allclose(scale.double(), torch.tensor(size / top, dtype=torch.float64, device="cuda"), rtol=2.0 ** -21, atol=0.0)
