@@ -143,10 +143,12 @@ __device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
 // are 0 in fp32).  The longest run over the SMs is no shorter than the mean, nor than r + 1 times the segment in place
 // r x SMs, since one SM has r + 1 of the segments up to there.  Against the best of 1, 2, .. 64 chunks, measured one by
 // one, the count so taken costs 0 to 5 % more on nine batches of 2048 to 32768 tokens and on 131072 tokens.  The
-// lengths are known here only.
+// lengths are known here only.  order (may be null): the sequences from the longest to the shortest (unsorted beyond
+// those whose tables fit in shared memory).
 constexpr int kMaxPer = 64;
 constexpr int kCached = 1024;      // sequences whose tables fit in shared memory
-__global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int chunk, int lo, int hi, int sms) {
+__global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int chunk, int lo, int hi, int sms,
+                                                    int *order) {
   __shared__ int tot[32], carry, bad, most, slot[kMaxPer + 1], s_cu[kCached + 1], s_base[kCached + 1];
   __shared__ int lengths[32][kMaxPer + 1];
   __shared__ unsigned best;
@@ -245,6 +247,19 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
     n = (s.end - s.begin + chunk - 1) / chunk;
     return s;
   };
+  if (order != nullptr)
+    for (int b = tid; b < p.num_seqs; b += 1024) {
+      int place = b;
+      if (cached) {
+        const int n = cu[b + 1] - cu[b];
+        place = 0;
+        for (int i = 0; i < p.num_seqs; ++i) {
+          const int m = cu[i + 1] - cu[i];
+          place += m > n || (m == n && i < b);
+        }
+      }
+      order[place] = b;
+    }
   if (per == 1) {
     int n;
     for (int i = tid; i < segs; i += 1024) table[i] = find(i, n);
@@ -689,8 +704,9 @@ cudaError_t launch_grad_dims(const LinearParams &p, const int *sbase, const floa
 
 }  // namespace lin
 
-cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int chunk, int lo, int hi, int sms, cudaStream_t s) {
-  lin::plan_kernel<<<1, 1024, 0, s>>>(p, sbase, chunk, lo, hi < lin::kMaxPer ? hi : lin::kMaxPer, sms);
+cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int chunk, int lo, int hi, int sms, int *order,
+                               cudaStream_t s) {
+  lin::plan_kernel<<<1, 1024, 0, s>>>(p, sbase, chunk, lo, hi < lin::kMaxPer ? hi : lin::kMaxPer, sms, order);
   return cudaGetLastError();
 }
 
@@ -719,7 +735,7 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   int *sbase = reinterpret_cast<int *>(w);
   float *whole = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs));
   float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4));
-  cudaError_t e = launch_linear_plan(p, sbase, tokens, 1, 1, 1, s);
+  cudaError_t e = launch_linear_plan(p, sbase, tokens, 1, 1, 1, nullptr, s);
   if (e != cudaSuccess) return e;
   e = launch_parts_chain(p, sbase, part, nullptr, whole, segs, tokens, s);
   if (e != cudaSuccess || p.N == 0) return e;
@@ -760,7 +776,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
       gk32 = take((size_t)p.N * p.H * p.dk * 4);
     }
     if (p.decay_head) gla = take((size_t)p.N * p.H * 4);
-    if ((e = launch_linear_plan(p, sbase, C, 1, 1, 1, s)) != cudaSuccess) return e;
+    if ((e = launch_linear_plan(p, sbase, C, 1, 1, 1, nullptr, s)) != cudaSuccess) return e;
     e = launch_parts_chain(p, sbase, part, rpart, whole, segs, C, s);
     if (e != cudaSuccess) return e;
     if (p.N > 0) e = launch_grad_dims(p, sbase, part, rpart, gq32, gk32, gla, segs, s);

@@ -85,14 +85,14 @@ struct SweepMaps {
 
 template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
-sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const Table *tables, float *through) {
+sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const int *order, const Table *tables, float *through) {
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
-  const int c0 = (int)(blockIdx.x % SL) * kSlice, h = (int)(blockIdx.x / SL % p.H), b = (int)(blockIdx.x / SL / p.H);
+  const int c0 = (int)(blockIdx.x % SL) * kSlice, h = (int)(blockIdx.x / SL % p.H), b = order[blockIdx.x / SL / p.H];
   const int begin = p.cu[b], end = p.cu[b + 1], n = (end - begin + C - 1) / C, chunk0 = sbase[b];
   // the last chunk's product matters to the gradient of the initial state only
   const int n_mma = REVERSE && p.g_init != nullptr ? n : n - 1;
@@ -848,8 +848,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
           if (row32 != nullptr) {
             if (r < rows)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4 *>(row32 + 32 * x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+              for (int e = 0; e < 32; e += 8) store_8(row32 + 32 * x + e, f + e);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -887,7 +886,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
 
 // ============================================================ host
 struct BackwardWorkspace {
-  size_t sbase, through, tables, s, d, gq32, gk32, gla, bytes;
+  size_t sbase, order, through, tables, s, d, gq32, gk32, gla, bytes;
 };
 inline BackwardWorkspace backward_layout(const LinearParams &p) {
   const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
@@ -898,6 +897,7 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
     return at;
   };
   w.sbase = take(lin::table_bytes(p.num_seqs, chunks));
+  w.order = take((size_t)p.num_seqs * 4);
   w.through = take(chunks * p.H * (p.dv / 8) * 4);
   w.tables = take(chunks * p.H * sizeof(Table));
   w.s = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
@@ -913,7 +913,7 @@ template <int DK, int DV>
 cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const SweepMaps &mr, const GradMaps &mg,
                             const BackwardWorkspace &w, size_t items, cudaStream_t s) {
   unsigned char *ws = static_cast<unsigned char *>(p.ws);
-  const int *sbase = reinterpret_cast<const int *>(ws + w.sbase);
+  const int *sbase = reinterpret_cast<const int *>(ws + w.sbase), *order = reinterpret_cast<const int *>(ws + w.order);
   float *through = reinterpret_cast<float *>(ws + w.through);
   const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice);
   if (sweeps > 0x7FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
@@ -925,9 +925,9 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
   if (items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, false>, (unsigned)sweeps, kSweepThreads, fwd_smem, s, p, mf, sbase, tables, nullptr);
+    e = launch_next(sweep_kernel<DK, DV, false>, (unsigned)sweeps, kSweepThreads, fwd_smem, s, p, mf, sbase, order, tables, nullptr);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, true>, (unsigned)sweeps, kSweepThreads, rev_smem, s, p, mr, sbase, tables, through);
+    e = launch_next(sweep_kernel<DK, DV, true>, (unsigned)sweeps, kSweepThreads, rev_smem, s, p, mr, sbase, order, tables, through);
   if (e != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
@@ -950,7 +950,8 @@ cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float
   *gq32 = shared ? reinterpret_cast<float *>(ws + w.gq32) : nullptr;
   *gk32 = shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr;
   *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
-  cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, 1, 1, 1, s);
+  cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, 1, 1, 1,
+                                     reinterpret_cast<int *>(ws + w.order), s);
   if (e != cudaSuccess) return e;
   GradMaps mg{};
   SweepMaps mf{}, mr{};

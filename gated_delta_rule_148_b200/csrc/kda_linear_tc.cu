@@ -775,7 +775,7 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   int *sbase = reinterpret_cast<int *>(w);
   float *whole = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs));
   float *part = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4));
-  cudaError_t e = launch_linear_plan(p, sbase, C, per, 64, sm_count(), s);
+  cudaError_t e = launch_linear_plan(p, sbase, C, per, 64, sm_count(), nullptr, s);
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&

@@ -99,6 +99,12 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, float (&x)[2]) {
   x[1] = __uint_as_float(r[1]);
 }
 
+// 8 floats (32 bytes, a whole sector) to global memory.
+__device__ __forceinline__ void store_8(float *p, const float *f) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]) : "memory");
+}
+
 // Bounded waits of one block.  After one has run out every role leaves its loop; the waits of the
 // others then end too.
 struct Waits {
