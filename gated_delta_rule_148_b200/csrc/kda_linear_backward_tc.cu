@@ -87,18 +87,38 @@ struct SweepMaps {
 
 template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
-sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const int *order, const Table *tables, float *through) {
+sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const int *order,
+             const Table *tables, float *through) {
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
-  const int c0 = (int)(blockIdx.x % SL) * kSlice, h = (int)(blockIdx.x / SL % p.H), b = order[blockIdx.x / SL / p.H];
-  const int begin = p.cu[b], end = p.cu[b + 1], n = (end - begin + C - 1) / C, chunk0 = sbase[b];
-  // the last chunk's product matters to the gradient of the initial state only
-  const int n_mma = REVERSE && p.g_init != nullptr ? n : n - 1;
-  auto at = [&](int j) { return REVERSE ? n - 1 - j : j; };      // chunk of step j
+  const int nitems = p.num_seqs * p.H * SL;
+  // a block's items one after the other; the next one's rows are looked up an item ahead
+  struct Item {
+    int b, h, c0, begin, n, chunk0;
+  };
+  auto look_up = [&](int k) {
+    const int i = item_of(k);
+    Item x{};
+    if (i < nitems) {
+      x.c0 = i % SL * kSlice;
+      x.h = i / SL % p.H;
+      x.b = order[i / SL / p.H];
+      x.begin = p.cu[x.b];
+      x.n = (p.cu[x.b + 1] - x.begin + C - 1) / C;
+      x.chunk0 = sbase[x.b];
+    }
+    return x;
+  };
+  Item next = look_up(0);
+  // products: the last chunk's matters to the gradient of the initial state only
+  auto products = [&](const Item &x) { return REVERSE && p.g_init != nullptr ? x.n : x.n - 1; };
+  auto at = [&](const Item &x, int j) { return REVERSE ? x.n - 1 - j : j; };      // chunk of step j
+  // first row of a step's first part in the state tiles
+  auto tile_row = [&](const Item &x, int j) { return (int)((((size_t)(x.chunk0 + at(x, j)) * p.H + x.h) * 2) * DK); };
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::BARS), *empty = full + kSweepStages, *w_ready = empty + kSweepStages,
@@ -129,38 +149,41 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   fence_after_sync();
   const uint32_t tm = *tmem_sh;
   const Waits wait{p.wait_cycles, p.err, p.site, failed};
-  const int hk = h / (p.H / p.Hk);
-  const Table *table = tables + (size_t)chunk0 * p.H + h;
-  // first row of a step's first part in the state tiles
-  auto tile_row = [&](int j) { return (int)((((size_t)(chunk0 + at(j)) * p.H + h) * 2) * DK); };
-
   if (warp == 9) {
     if (lane == 0) {
       bool ok = true;
       int loaded = 0, states = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int st = j % kSweepStages;
-        if (j < n_mma) {
-          if (j >= kSweepStages) ok = wait(empty + st, j / kSweepStages - 1, SITE_SWEEP);
-          if (!ok) break;
-          mbar_arrive_expect_tx(full + st, L::STAGE + C * 4 + 16);
-          const uint32_t dst = smem_u32(sm + st * L::STAGE);
-          const Table &t = table[(size_t)at(j) * p.H];
-          bulk_load(wgt + st * C, REVERSE ? t.from : t.to, C * 4, full + st);
-          bulk_load(valid + st * 4, t.valid, 16, full + st);
+      for (int k = 0; item_of(k) < nitems && ok; ++k) {
+        const Item x = next;
+        next = look_up(k + 1);
+        const int n_mma = products(x), hk = x.h / (p.H / p.Hk);
+        const Table *table = tables + (size_t)x.chunk0 * p.H + x.h;
+        for (int j = 0; j < x.n && ok; ++j) {
+          const int pos = x.begin + at(x, j) * C;
+          if (j < n_mma) {
+            const int st = loaded % kSweepStages;
+            if (loaded >= kSweepStages) ok = wait(empty + st, loaded / kSweepStages - 1, SITE_SWEEP);
+            if (!ok) break;
+            mbar_arrive_expect_tx(full + st, L::STAGE + C * 4 + 16);
+            const uint32_t dst = smem_u32(sm + st * L::STAGE);
+            const Table &t = table[(size_t)at(x, j) * p.H];
+            bulk_load(wgt + st * C, REVERSE ? t.from : t.to, C * 4, full + st);
+            bulk_load(valid + st * 4, t.valid, 16, full + st);
 #pragma unroll
-          for (int kb = 0; kb < DK / 64; ++kb) tma_load_3d(dst + kb * C * 128, &maps.k, kb * 64, hk, begin + at(j) * C, full + st);
-          tma_load_3d(dst + L::KT, &maps.v, c0, h, begin + at(j) * C, full + st);
-          ++loaded;
-        }
-        if constexpr (REVERSE) {
-          if (j >= 2) ok = wait(s_free + (j & 1), (j >> 1) - 1, SITE_SWEEP + 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(s_full + (j & 1), 2 * L::XT);
+            for (int kb = 0; kb < DK / 64; ++kb) tma_load_3d(dst + kb * C * 128, &maps.k, kb * 64, hk, pos, full + st);
+            tma_load_3d(dst + L::KT, &maps.v, x.c0, x.h, pos, full + st);
+            ++loaded;
+          }
+          if constexpr (REVERSE) {
+            const int sl = states & 1;
+            if (states >= 2) ok = wait(s_free + sl, (states >> 1) - 1, SITE_SWEEP + 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(s_full + sl, 2 * L::XT);
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            tma_load_3d(smem_u32(sm + L::IN + ((j & 1) * 2 + x) * L::XT), &maps.s, c0, 0, tile_row(j) + x * DK, s_full + (j & 1));
-          ++states;
+            for (int y = 0; y < 2; ++y)
+              tma_load_3d(smem_u32(sm + L::IN + (sl * 2 + y) * L::XT), &maps.s, x.c0, 0, tile_row(x, j) + y * DK, s_full + sl);
+            ++states;
+          }
         }
       }
       // loads in flight land before the block ends, whoever gave up
@@ -171,33 +194,46 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   } else if (warp == 8) {
     if (lane == 0) {
       bool ok = true;
-      for (int j = 0; j < n_mma && ok; ++j) {
-        const int st = j % kSweepStages, sl = j & 1;
-        if (j >= 2) ok = wait(acc_free + sl, (j >> 1) - 1, SITE_SWEEP + 2);
-        ok = ok && wait(w_ready + sl, j >> 1, SITE_SWEEP + 3);
-        if (!ok) break;
-        fence_after_sync();
-        const uint64_t k = desc_mnmajor(smem_u32(sm + st * L::STAGE), C, 0, 0),
-                       v = sdesc(smem_u32(sm + L::W + sl * 3 * L::VT), L::VT, 512, 4);
+      int m = 0;
+      for (int k = 0; item_of(k) < nitems && ok; ++k) {
+        const Item x = next;
+        next = look_up(k + 1);
+        for (int j = 0; j < products(x) && ok; ++j, ++m) {
+          const int st = m % kSweepStages, sl = m & 1;
+          if (m >= 2) ok = wait(acc_free + sl, (m >> 1) - 1, SITE_SWEEP + 2);
+          ok = ok && wait(w_ready + sl, m >> 1, SITE_SWEEP + 3);
+          if (!ok) break;
+          fence_after_sync();
+          const uint64_t kd = desc_mnmajor(smem_u32(sm + st * L::STAGE), C, 0, 0),
+                         vd = sdesc(smem_u32(sm + L::W + sl * 3 * L::VT), L::VT, 512, 4);
 #pragma unroll
-        for (int s = 0; s < C / 16; ++s)
-          mma_bf16(tm + sl * 128, mnmajor_step(k, s), v + (uint32_t)(s * 16 * 64 >> 4),
-                   idesc_bf16(128, 3 * kSlice, 1, 1), s > 0);
-        mma_commit(empty + st);
-        mma_commit(done + sl);
+          for (int s = 0; s < C / 16; ++s)
+            mma_bf16(tm + sl * 128, mnmajor_step(kd, s), vd + (uint32_t)(s * 16 * 64 >> 4),
+                     idesc_bf16(128, 3 * kSlice, 1, 1), s > 0);
+          mma_commit(empty + st);
+          mma_commit(done + sl);
+        }
       }
       mma_commit(drain);
       mbar_wait(drain, 0, kDrainCycles);
     }
   } else if (warp == 10) {
     if (lane == 0) {
-      for (int j = 0; j < n; ++j) {
-        if (!wait(staged, j, SITE_SWEEP + 8)) break;
+      bool ok = true;
+      int out = 0;
+      for (int k = 0; item_of(k) < nitems && ok; ++k) {
+        const Item x = next;
+        next = look_up(k + 1);
+        for (int j = 0; j < x.n && ok; ++j, ++out) {
+          ok = wait(staged, out, SITE_SWEEP + 8);
+          if (!ok) break;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) tma_store_3d(&maps.out, smem_u32(sm + L::OUT + x * L::XT), c0, 0, tile_row(j) + x * DK);
-        bulk_commit();
-        bulk_wait_read();
-        mbar_arrive(out_free);
+          for (int y = 0; y < 2; ++y)
+            tma_store_3d(&maps.out, smem_u32(sm + L::OUT + y * L::XT), x.c0, 0, tile_row(x, j) + y * DK);
+          bulk_commit();
+          bulk_wait_read();
+          mbar_arrive(out_free);
+        }
       }
       bulk_wait_all();
     }
@@ -205,110 +241,127 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
     // ---------------- w V (thread: row of the chunk)
     const int r = tid;
     bool ok = true;
-    for (int j = 0; j < n_mma && ok; ++j) {
-      const int sl = j & 1, st = j % kSweepStages;
-      ok = wait.warp(full + st, j / kSweepStages, SITE_SWEEP + 4);
-      if (!ok) break;
-      const bool real = (valid[4 * st + warp] >> lane) & 1;
-      const float w = wgt[st * C + r];
-      unsigned char *sk = sm + st * L::STAGE;
-      uint4 u[4];
+    int m = 0;
+    for (int k = 0; item_of(k) < nitems && ok; ++k) {
+      const Item x = next;
+      next = look_up(k + 1);
+      for (int j = 0; j < products(x) && ok; ++j, ++m) {
+        const int sl = m & 1, st = m % kSweepStages;
+        ok = wait.warp(full + st, m / kSweepStages, SITE_SWEEP + 4);
+        if (!ok) break;
+        const bool real = (valid[4 * st + warp] >> lane) & 1;
+        const float w = wgt[st * C + r];
+        unsigned char *sk = sm + st * L::STAGE;
+        uint4 u[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        u[c] = real ? *reinterpret_cast<const uint4 *>(sk + L::KT + slice_at(r, c)) : make_uint4(0, 0, 0, 0);
-      if (!real)
+        for (int c = 0; c < 4; ++c)
+          u[c] = real ? *reinterpret_cast<const uint4 *>(sk + L::KT + slice_at(r, c)) : make_uint4(0, 0, 0, 0);
+        if (!real)
 #pragma unroll
-        for (int c = 0; c < DK / 8; ++c)
-          *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
-      if (j >= 2) ok = wait.warp(done + sl, (j >> 1) - 1, SITE_SWEEP + 5);
-      if (!ok) break;
-      unsigned char *sw = sm + L::W + sl * 3 * L::VT;
+          for (int c = 0; c < DK / 8; ++c)
+            *reinterpret_cast<uint4 *>(sk + row_tile_chunk(r, c >> 3, c & 7, C)) = make_uint4(0, 0, 0, 0);
+        if (m >= 2) ok = wait.warp(done + sl, (m >> 1) - 1, SITE_SWEEP + 5);
+        if (!ok) break;
+        unsigned char *sw = sm + L::W + sl * 3 * L::VT;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f[8];
-        unpack8(u[c], f);
+        for (int c = 0; c < 4; ++c) {
+          float f[8];
+          unpack8(u[c], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= w;
+          for (int e = 0; e < 8; ++e) f[e] *= w;
 #pragma unroll
-        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint4 *>(sw + x * L::VT + slice_at(r, c)) = take_bf16(f);
+          for (int y = 0; y < 3; ++y) *reinterpret_cast<uint4 *>(sw + y * L::VT + slice_at(r, c)) = take_bf16(f);
+        }
+        fence_async_smem();
+        mbar_arrive(w_ready + sl);
       }
-      fence_async_smem();
-      mbar_arrive(w_ready + sl);
     }
   } else {
     // ---------------- the state (thread: its row)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float *in = REVERSE ? p.d_final : p.init_state;
-    const size_t own = (((size_t)b * p.H + h) * DK + r) * DV + c0;
-    float S[kSlice];
-#pragma unroll
-    for (int e = 0; e < kSlice; ++e) S[e] = 0.f;
-    if (in != nullptr && r < DK)
-#pragma unroll
-      for (int e = 0; e < kSlice; e += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(in + own + e);
-        S[e] = f.x; S[e + 1] = f.y; S[e + 2] = f.z; S[e + 3] = f.w;
-      }
     bool ok = true;
-    float next = n > 0 ? table[(size_t)at(0) * p.H].whole : 0.f;
-    for (int j = 0; j < n && ok; ++j) {
-      const int sl = j & 1;
-      const float a = next;
-      if (j + 1 < n) next = table[(size_t)at(j + 1) * p.H].whole;
-      if (j > 0) ok = wait.warp(out_free, j - 1, SITE_SWEEP + 9);
-      if (!ok) break;
-      if (r < DK)
+    int out = 0, m = 0;
+    for (int k = 0; item_of(k) < nitems && ok; ++k) {
+      const Item x = next;
+      next = look_up(k + 1);
+      const int n_mma = products(x);
+      const float *whole = &tables[(size_t)(x.chunk0 + at(x, 0)) * p.H + x.h].whole;
+      const ptrdiff_t hop = (REVERSE ? -1 : 1) * (ptrdiff_t)p.H * (ptrdiff_t)(sizeof(Table) / 4);
+      const size_t own = (((size_t)x.b * p.H + x.h) * DK + r) * DV + x.c0;
+      float S[kSlice];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float f[8];
+      for (int e = 0; e < kSlice; ++e) S[e] = 0.f;
+      if (in != nullptr && r < DK)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = S[8 * c + e];
-          *reinterpret_cast<uint4 *>(sm + L::OUT + slice_at(r, c)) = take_bf16(f);
-          *reinterpret_cast<uint4 *>(sm + L::OUT + L::XT + slice_at(r, c)) = take_bf16(f);
+        for (int e = 0; e < kSlice; e += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(in + own + e);
+          S[e] = f.x; S[e + 1] = f.y; S[e + 2] = f.z; S[e + 3] = f.w;
         }
-      fence_async_smem();
-      mbar_arrive(staged);
-      if constexpr (REVERSE) {
-        ok = wait.warp(s_full + sl, j >> 1, SITE_SWEEP + 6);
+      float ahead = x.n > 0 ? *whole : 0.f;
+      for (int j = 0; j < x.n && ok; ++j, ++out) {
+        const int sl = out & 1;
+        const float a = ahead;
+        whole += hop;
+        if (j + 1 < x.n) ahead = *whole;
+        if (out > 0) ok = wait.warp(out_free, out - 1, SITE_SWEEP + 9);
         if (!ok) break;
-        const unsigned char *t = sm + L::IN + sl * 2 * L::XT;
-        float dot = 0.f;
         if (r < DK)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float f[8], g[8];
-            unpack8(*reinterpret_cast<const uint4 *>(t + slice_at(r, c)), f);
-            unpack8(*reinterpret_cast<const uint4 *>(t + L::XT + slice_at(r, c)), g);
+            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(f[e] + g[e], S[8 * c + e], dot);
+            for (int e = 0; e < 8; ++e) f[e] = S[8 * c + e];
+            *reinterpret_cast<uint4 *>(sm + L::OUT + slice_at(r, c)) = take_bf16(f);
+            *reinterpret_cast<uint4 *>(sm + L::OUT + L::XT + slice_at(r, c)) = take_bf16(f);
           }
-        mbar_arrive(s_free + sl);
+        fence_async_smem();
+        mbar_arrive(staged);
+        if constexpr (REVERSE) {
+          ok = wait.warp(s_full + sl, out >> 1, SITE_SWEEP + 6);
+          if (!ok) break;
+          const unsigned char *t = sm + L::IN + sl * 2 * L::XT;
+          float dot = 0.f;
+          if (r < DK)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-        if (lane == 0) through[(((size_t)(chunk0 + at(j)) * p.H + h) * SL + c0 / kSlice) * 4 + (warp & 3)] = dot;
+            for (int c = 0; c < 4; ++c) {
+              float f[8], g[8];
+              unpack8(*reinterpret_cast<const uint4 *>(t + slice_at(r, c)), f);
+              unpack8(*reinterpret_cast<const uint4 *>(t + L::XT + slice_at(r, c)), g);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dot = fmaf(f[e] + g[e], S[8 * c + e], dot);
+            }
+          mbar_arrive(s_free + sl);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+          if (lane == 0)
+            through[(((size_t)(x.chunk0 + at(x, j)) * p.H + x.h) * SL + x.c0 / kSlice) * 4 + (warp & 3)] = dot;
+        }
+        if (j >= n_mma) continue;
+        ok = wait.warp(done + (m & 1), m >> 1, SITE_SWEEP + 7);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t col = tm + lanes + (m & 1) * 128;
+        uint32_t u[32], v[32], w[32];
+        tmem_ld32_issue(col, u);
+        tmem_ld32_issue(col + 32, v);
+        tmem_ld32_issue(col + 64, w);
+        tmem_ld32_wait(u);
+        tmem_ld32_wait(v);
+        tmem_ld32_wait(w);
+        fence_before_sync();
+        mbar_arrive(acc_free + (m & 1));
+        ++m;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          S[e] = fmaf(a, S[e], __uint_as_float(u[e]) + (__uint_as_float(v[e]) + __uint_as_float(w[e])));
       }
-      if (j >= n_mma) continue;
-      ok = wait.warp(done + sl, j >> 1, SITE_SWEEP + 7);
-      if (!ok) break;
-      fence_after_sync();
-      uint32_t x[32], y[32], z[32];
-      tmem_ld32_issue(tm + lanes + sl * 128, x);
-      tmem_ld32_issue(tm + lanes + sl * 128 + 32, y);
-      tmem_ld32_issue(tm + lanes + sl * 128 + 64, z);
-      tmem_ld32_wait(x);
-      tmem_ld32_wait(y);
-      tmem_ld32_wait(z);
-      fence_before_sync();
-      mbar_arrive(acc_free + sl);
+      if (REVERSE && p.g_init != nullptr && ok && r < DK)
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        S[e] = fmaf(a, S[e], __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e])));
+        for (int e = 0; e < kSlice; e += 4)
+          *reinterpret_cast<float4 *>(p.g_init + own + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
-    if (REVERSE && p.g_init != nullptr && ok && r < DK)
-#pragma unroll
-      for (int e = 0; e < kSlice; e += 4)
-        *reinterpret_cast<float4 *>(p.g_init + own + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
   }
   fence_before_sync();
   __syncthreads();
@@ -918,18 +971,19 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   const int *sbase = reinterpret_cast<const int *>(ws + w.sbase), *order = reinterpret_cast<const int *>(ws + w.order);
   float *through = reinterpret_cast<float *>(ws + w.through);
   const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice);
-  if (sweeps > 0x7FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  if (sweeps > 0x3FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END, grad_smem = GradSmem<DK, DV>::END;
   cudaError_t e = lin::allow_smem<sweep_kernel<DK, DV, false>>(fwd_smem);
   if (e == cudaSuccess) e = lin::allow_smem<sweep_kernel<DK, DV, true>>(rev_smem);
   if (e == cudaSuccess) e = lin::allow_smem<grad_kernel<DK, DV>>(grad_smem);
   if (e != cudaSuccess) return e;
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
+  const unsigned sweep_grid = (unsigned)(sweeps < (size_t)sm_count() ? sweeps : (size_t)sm_count());
   if (items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, false>, (unsigned)sweeps, kSweepThreads, fwd_smem, s, p, mf, sbase, order, tables, nullptr);
+    e = launch_next(sweep_kernel<DK, DV, false>, sweep_grid, kSweepThreads, fwd_smem, s, p, mf, sbase, order, tables, nullptr);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, true>, (unsigned)sweeps, kSweepThreads, rev_smem, s, p, mr, sbase, order, tables, through);
+    e = launch_next(sweep_kernel<DK, DV, true>, sweep_grid, kSweepThreads, rev_smem, s, p, mr, sbase, order, tables, through);
   if (e != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;

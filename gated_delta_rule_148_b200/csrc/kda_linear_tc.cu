@@ -32,12 +32,6 @@ struct Maps {
   CUtensorMap q, k, v, o, part;
 };
 
-// A block's n-th item (segment x H + h): there and back over the blocks, so that the blocks with the longest item of one
-// round take the shortest of the next.
-__device__ __forceinline__ int item_of(int n) {
-  return n * (int)gridDim.x + (int)(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
-
 // ============================================================ parts
 // A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
 // weights; the others follow.  It goes from a segment's last chunk to its first and stops once every
@@ -134,7 +128,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
         const int st = step & 1, rs = step % kRing, acc = n & 1;
         const bool first = steps[rs].first != 0, last = steps[rs].last != 0;
         if (first && n >= 2) ok = ok && wait(s_free + acc, (n >> 1) - 1, SITE_PARTS + 2);
-        ok = ok && wait(w_ready, step, SITE_PARTS + 3);
+        ok = ok && wait(full + st, step >> 1, SITE_PARTS + 3) && wait(w_ready, step, SITE_PARTS + 3);
         if (!ok) break;
         fence_after_sync();
         const uint32_t d = tm + acc * kCols;

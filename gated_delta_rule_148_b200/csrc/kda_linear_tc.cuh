@@ -187,6 +187,12 @@ __device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], 
   return __all_sync(0xFFFFFFFFu, d.bits == 0xFu);
 }
 
+// A block's n-th item of a list: there and back over the blocks, so that the blocks with the longest item of one
+// round take the shortest of the next.
+__device__ __forceinline__ int item_of(int n) {
+  return n * (int)gridDim.x + (int)(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 // 8 bf16 of a 16-byte word as floats.
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
   const uint32_t a[4] = {u.x, u.y, u.z, u.w};
