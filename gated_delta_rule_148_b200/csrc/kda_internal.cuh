@@ -166,6 +166,9 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
 // bf16 inputs: tensor-core kernels (kda_linear_tc.cu).
 size_t linear_prefill_tc_workspace(const LinearParams &p);
 cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s);
+// States at the segments' starts (part) and their gradients at the segments' ends (rpart).
+cudaError_t launch_linear_segment_states_tc(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole,
+                                            size_t segs, cudaStream_t s);
 // ... of the backward pass (kda_linear_backward_tc.cu); where the caller's sums over shared inputs find their
 // terms: dq, dk per value head (null if none is shared), the decays' gradients per token.
 size_t linear_backward_tc_workspace(const LinearParams &p);

@@ -145,7 +145,6 @@ __device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
 // one, the count so taken costs 0 to 5 % more on nine batches of 2048 to 32768 tokens and on 131072 tokens.  The
 // lengths are known here only.  order (may be null): the sequences from the longest to the shortest (unsorted beyond
 // those whose tables fit in shared memory).
-constexpr int kMaxPer = 64;
 constexpr int kCached = 1024;      // sequences whose tables fit in shared memory
 __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int chunk, int lo, int hi, int sms,
                                                     int *order) {
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
     s.id = i;
     s.begin = cu[a] + (i - base[a]) * tokens;
     s.end = min(e, s.begin + tokens);
-    s.last = s.begin + tokens >= e;
+    s.of = a << 1 | (s.begin + tokens >= e ? 1 : 0);
     n = (s.end - s.begin + chunk - 1) / chunk;
     return s;
   };

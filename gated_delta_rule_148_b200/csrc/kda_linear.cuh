@@ -22,11 +22,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs); behind them the segments in the order
-// in which blocks take them: number (their states' place, in the sequences' order), rows [begin, end) and whether a
-// segment is its sequence's last.
+// in which blocks take them: number (their states' place, in the sequences' order), rows [begin, end), and the sequence
+// with a bit that tells its last segment.
 struct alignas(16) Segment {
-  int id, begin, end, last;
+  int id, begin, end, of;
+  __device__ __forceinline__ bool last() const { return of & 1; }
+  __device__ __forceinline__ int seq() const { return of >> 1; }
 };
+// Chunks in a segment at most, where segments have more than one: the plan counts the lengths in shared memory.
+constexpr int kMaxPer = 64;
 inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
 inline size_t table_bytes(int B, size_t segs) { return align256((size_t)(B + 1) * 4) + align256(segs * sizeof(Segment)); }
 __device__ __forceinline__ const Segment *segment_table(const int *sbase, int num_seqs) {

@@ -6,7 +6,8 @@
 //           head through all chunks:  S <- 2^{b_C} S + K^T (w V), w_s = 2^{b_C - b_s}, with
 //           S in registers (fp32), w V split into three bf16 parts (24 bits).  The products do not
 //           depend on S, so the chain from chunk to chunk is one multiply-add per element, and four
-//           blocks of a head keep it parallel for few heads.  D: the same from the last chunk to
+//           blocks of a head keep it parallel for few heads; for fewer still, segments of a sequence
+//           are swept from states of their own (sweep_chunks).  D: the same from the last chunk to
 //           the first over q, grad_o with w_t = 2^{b_t}; it also takes <S, D> of each chunk.
 //           Both are stored as two bf16 parts (16 bits), the form in which the next step's
 //           products read them.
@@ -88,17 +89,18 @@ struct SweepMaps {
 template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kSweepThreads, 1)
 sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const int *order,
-             const Table *tables, float *through) {
+             const int *segments, const float *start, const Table *tables, float *through) {
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
-  const int nitems = p.num_seqs * p.H * SL;
+  // whole sequences from the longest, or (segments) parts of them from the states in start
+  const int nitems = (segments ? segments[p.num_seqs] : p.num_seqs) * p.H * SL;
   // a block's items one after the other; the next one's rows are looked up an item ahead
   struct Item {
-    int b, h, c0, begin, n, chunk0;
+    int b, h, c0, begin, n, chunk0;      // b: sequence, or segment
   };
   auto look_up = [&](int k) {
     const int i = item_of(k);
@@ -106,16 +108,25 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
     if (i < nitems) {
       x.c0 = i % SL * kSlice;
       x.h = i / SL % p.H;
-      x.b = order[i / SL / p.H];
-      x.begin = p.cu[x.b];
-      x.n = (p.cu[x.b + 1] - x.begin + C - 1) / C;
-      x.chunk0 = sbase[x.b];
+      if (segments != nullptr) {
+        const Segment sg = lin::locate(segments, p.num_seqs, i / SL / p.H);
+        x.b = sg.id;
+        x.begin = sg.begin;
+        x.n = (sg.end - sg.begin + C - 1) / C;
+        x.chunk0 = sbase[sg.seq()] + (sg.begin - p.cu[sg.seq()]) / C;
+      } else {
+        x.b = order[i / SL / p.H];
+        x.begin = p.cu[x.b];
+        x.n = (p.cu[x.b + 1] - x.begin + C - 1) / C;
+        x.chunk0 = sbase[x.b];
+      }
     }
     return x;
   };
   Item next = look_up(0);
   // products: the last chunk's matters to the gradient of the initial state only
-  auto products = [&](const Item &x) { return REVERSE && p.g_init != nullptr ? x.n : x.n - 1; };
+  const bool to_init = REVERSE && segments == nullptr && p.g_init != nullptr;
+  auto products = [&](const Item &x) { return to_init ? x.n : x.n - 1; };
   auto at = [&](const Item &x, int j) { return REVERSE ? x.n - 1 - j : j; };      // chunk of step j
   // first row of a step's first part in the state tiles
   auto tile_row = [&](const Item &x, int j) { return (int)((((size_t)(x.chunk0 + at(x, j)) * p.H + x.h) * 2) * DK); };
@@ -280,7 +291,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
     // ---------------- the state (thread: its row)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const float *in = REVERSE ? p.d_final : p.init_state;
+    const float *in = segments ? start : REVERSE ? p.d_final : p.init_state;
     bool ok = true;
     int out = 0, m = 0;
     for (int k = 0; item_of(k) < nitems && ok; ++k) {
@@ -357,7 +368,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
         for (int e = 0; e < 32; ++e)
           S[e] = fmaf(a, S[e], __uint_as_float(u[e]) + (__uint_as_float(v[e]) + __uint_as_float(w[e])));
       }
-      if (REVERSE && p.g_init != nullptr && ok && r < DK)
+      if (to_init && ok && r < DK)
 #pragma unroll
         for (int e = 0; e < kSlice; e += 4)
           *reinterpret_cast<float4 *>(p.g_init + own + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
@@ -940,12 +951,33 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
 }
 
 // ============================================================ host
+// Chunks in a segment of the sweeps, or 0 to sweep whole sequences.  Few sequences and heads leave SMs idle: then segments,
+// about one for each SM, are swept from states computed like the prefill's, in both directions.  A step of both sweeps
+// takes 1.8 us and the states with their four more launches 36 to 57 us, so it takes 25 steps less to be worth it; the host
+// knows the mean length only, which the longest sequence's steps are no fewer than.  Whole -> segments, d_k = d_v = 128:
+// one head of 2048, 4096, 8192, 32768 tokens 63 -> 67, 92 -> 68, 150 -> 74, 547 -> 116 us; 4 heads of 4096, 8192
+// 97 -> 85, 175 -> 114 us; 8 of 2048, 4096, 8192 67 -> 85, 113 -> 114, 201 -> 159 us; 16 of 4096, 8192 139 -> 160,
+// 239 -> 232 us; 8 heads of two times 2048 82 -> 116 us.
+inline int sweep_chunks(const LinearParams &p) {
+  constexpr int kSms = 148, kWorth = 25;
+  const long long lanes = (long long)p.H * (p.dv / kSlice), chunks = ((long long)p.N + C - 1) / C;
+  if (p.num_seqs == 0 || lanes > kSms) return 0;
+  const long long segs = kSms / lanes;
+  long long per = (chunks + segs - 1) / segs;
+  if (per < 2) per = 2;
+  if (per > lin::kMaxPer) per = lin::kMaxPer;
+  return chunks >= (per + kWorth) * p.num_seqs ? (int)per : 0;
+}
+
 struct BackwardWorkspace {
-  size_t sbase, order, through, tables, s, d, gq32, gk32, gla, bytes;
+  int per;      // chunks in a segment of the sweeps; 0: whole sequences
+  size_t segs, sbase, order, seg_base, part, rpart, whole, through, tables, s, d, gq32, gk32, gla, bytes;
 };
 inline BackwardWorkspace backward_layout(const LinearParams &p) {
   const size_t chunks = lin::max_segments(p.N, p.num_seqs, C);
   BackwardWorkspace w{};
+  w.per = sweep_chunks(p);
+  w.segs = w.per ? lin::max_segments(p.N, p.num_seqs, C * w.per) : 0;
   auto take = [&](size_t n) {
     const size_t at = w.bytes;
     w.bytes += lin::align256(n);
@@ -953,6 +985,12 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
   };
   w.sbase = take(lin::table_bytes(p.num_seqs, chunks));
   w.order = take((size_t)p.num_seqs * 4);
+  if (w.per) {
+    w.seg_base = take(lin::table_bytes(p.num_seqs, w.segs));
+    w.part = take(w.segs * p.H * (size_t)p.dk * p.dv * 4);
+    w.rpart = take(w.segs * p.H * (size_t)p.dk * p.dv * 4);
+    w.whole = take(w.segs * p.H * 4);
+  }
   w.through = take(chunks * p.H * (p.dv / 8) * 4);
   w.tables = take(chunks * p.H * sizeof(Table));
   w.s = take(chunks * p.H * (size_t)p.dk * p.dv * 4);
@@ -970,7 +1008,7 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   unsigned char *ws = static_cast<unsigned char *>(p.ws);
   const int *sbase = reinterpret_cast<const int *>(ws + w.sbase), *order = reinterpret_cast<const int *>(ws + w.order);
   float *through = reinterpret_cast<float *>(ws + w.through);
-  const size_t sweeps = (size_t)p.num_seqs * p.H * (DV / kSlice);
+  const size_t sweeps = (w.per ? w.segs : (size_t)p.num_seqs) * p.H * (DV / kSlice);
   if (sweeps > 0x3FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END, grad_smem = GradSmem<DK, DV>::END;
   cudaError_t e = lin::allow_smem<sweep_kernel<DK, DV, false>>(fwd_smem);
@@ -979,11 +1017,22 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   if (e != cudaSuccess) return e;
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
   const unsigned sweep_grid = (unsigned)(sweeps < (size_t)sm_count() ? sweeps : (size_t)sm_count());
-  if (items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
+  const int *segments = nullptr;
+  const float *part = nullptr, *rpart = nullptr;
+  if (w.per) {
+    segments = reinterpret_cast<const int *>(ws + w.seg_base);
+    float *a = reinterpret_cast<float *>(ws + w.part), *b = reinterpret_cast<float *>(ws + w.rpart);
+    e = launch_linear_segment_states_tc(p, segments, a, b, reinterpret_cast<float *>(ws + w.whole), w.segs, s);
+    part = a;
+    rpart = b;
+  }
+  if (e == cudaSuccess && items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, false>, sweep_grid, kSweepThreads, fwd_smem, s, p, mf, sbase, order, tables, nullptr);
+    e = launch_next(sweep_kernel<DK, DV, false>, sweep_grid, kSweepThreads, fwd_smem, s, p, mf, sbase, order, segments, part,
+                    tables, nullptr);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, true>, sweep_grid, kSweepThreads, rev_smem, s, p, mr, sbase, order, tables, through);
+    e = launch_next(sweep_kernel<DK, DV, true>, sweep_grid, kSweepThreads, rev_smem, s, p, mr, sbase, order, segments, rpart,
+                    tables, through);
   if (e != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
@@ -1008,6 +1057,8 @@ cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float
   *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, 1, 1, 1,
                                      reinterpret_cast<int *>(ws + w.order), s);
+  if (e == cudaSuccess && w.per)
+    e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.seg_base), C, w.per, w.per, 1, nullptr, s);
   if (e != cudaSuccess) return e;
   GradMaps mg{};
   SweepMaps mf{}, mr{};

@@ -4,7 +4,8 @@
 //   parts   a segment's contribution to the state, sum_s w_s k_s v_s^T with w_s = 2^{b_end - b_s}:
 //           the chunks of a segment from the last to the first, so that w needs no second
 //           look at the decays, all accumulated in TMEM:  S += K^T (w V).  w V is split into
-//           three bf16 parts (24 bits), so the states keep fp32 accuracy.
+//           three bf16 parts (24 bits), so the states keep fp32 accuracy.  REVERSE: the same over q and grad_o from a
+//           segment's first chunk on, w_t = 2^{b_t}: its share of the state's gradient at its start.
 //   chain   states at the segments' starts (chain_kernel, kda_linear.cu)
 //   rows    per chunk  A = Q K^T,  P = A o 2^{b_t - b_s} (bf16, TMEM),  O1 = Q S,  O2 = P V,
 //           o = 2^{b_t} O1 + O2,  S <- 2^{b_C} S + K^T (w V), w V in two bf16 parts (2^-17: it only
@@ -34,7 +35,7 @@ struct Maps {
 
 // ============================================================ parts
 // A ring of four steps: the preparing warp decides which chunk of which segment comes next and writes its
-// weights; the others follow.  It goes from a segment's last chunk to its first and stops once every
+// weights; the others follow.  It goes from a segment's last chunk to its first (or back) and stops once every
 // weight that is left is 0 in fp32 (decays of 2^-151 and less): those rows are not read, their share is 0.
 constexpr int kPartsThreads = 16 * 32 + 64;     // four warpgroups, a TMA + MMA warp, a preparing warp
 constexpr int kRing = 4;
@@ -56,7 +57,7 @@ struct PartsSmem {
   static_assert(END <= 232448, "shared memory of a block");
 };
 
-template <int DK, int DV>
+template <int DK, int DV, bool REVERSE>
 __global__ void __launch_bounds__(kPartsThreads, 1)
 parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase, float *whole) {
   using L = PartsSmem<DK, DV>;
@@ -184,32 +185,34 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
     };
     for (int n_i = 0, i; (i = item_of(n_i)) < nitems && ok; ++n_i) {
       const Segment sg = lin::locate(sbase, p.num_seqs, i / p.H);
-      // the last segment of a sequence matters to the final state only
-      if (sg.last && p.final_state == nullptr) continue;
+      // the last segment of a sequence matters to the final state only (the first to the initial state's gradient)
+      if (REVERSE ? p.g_init == nullptr && sg.begin == p.cu[sg.seq()] : p.final_state == nullptr && sg.last()) continue;
       const int chunks = (sg.end - sg.begin + C - 1) / C, h = i % p.H;
-      double after = 0.0;
-      RawDecays raw = load_decays(p, sg.begin + (chunks - 1) * C, sg.end, h);
-      for (int j = chunks - 1; j >= 0; --j) {
+      double past = 0.0;                     // log2 of the decay over the chunks taken
+      auto at = [&](int x) { return sg.begin + (REVERSE ? x : chunks - 1 - x) * C; };
+      RawDecays raw = load_decays(p, at(0), sg.end, h);
+      for (int x = 0; x < chunks; ++x) {
         const RawDecays now = raw;
-        if (j > 0) raw = load_decays(p, sg.begin + (j - 1) * C, sg.end, h);
+        if (x + 1 < chunks) raw = load_decays(p, at(x + 1), sg.end, h);
         double b[4], total;
         uint32_t word;
         scan_decays(now, b, total, word);
         if (!reserve()) break;
         const int rs = step % kRing;
         float4 w;
-        w.x = ex2((float)(after + (total - b[0])));
-        w.y = ex2((float)(after + (total - b[1])));
-        w.z = ex2((float)(after + (total - b[2])));
-        w.w = ex2((float)(after + (total - b[3])));
+        w.x = ex2((float)(past + (REVERSE ? b[0] : total - b[0])));
+        w.y = ex2((float)(past + (REVERSE ? b[1] : total - b[1])));
+        w.z = ex2((float)(past + (REVERSE ? b[2] : total - b[2])));
+        w.w = ex2((float)(past + (REVERSE ? b[3] : total - b[3])));
         reinterpret_cast<float4 *>(wgt + rs * C)[lane] = w;
         if ((lane & 7) == 0) valid[4 * rs + (lane >> 3)] = word;
-        after += total;
-        const bool last = j == 0 || after < -151.0;
-        publish(sg.id * p.H + h, sg.begin + j * C, h, j == chunks - 1, last);
+        past += total;
+        const bool last = x == chunks - 1 || past < -151.0;
+        publish(sg.id * p.H + h, at(x), h, x == 0, last);
         if (last) break;
       }
-      if (lane == 0) whole[sg.id * p.H + h] = ex2((float)after);
+      // both directions' sums round apart: a segment's factor has one writer
+      if (lane == 0 && (!REVERSE || sg.last())) whole[sg.id * p.H + h] = ex2((float)past);
     }
     if (ok && reserve()) publish(-1, 0, 0, false, false);
   } else {
@@ -747,13 +750,26 @@ cudaError_t launch(const LinearParams &p, const Maps &maps, const int *sbase, fl
   const size_t items = segs * p.H;
   if (items * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;      // rows of the states as a tensor map's coordinate
   const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
-  cudaError_t e = lin::allow_smem<parts_kernel<DK, DV>>(PartsSmem<DK, DV>::END);
+  cudaError_t e = lin::allow_smem<parts_kernel<DK, DV, false>>(PartsSmem<DK, DV>::END);
   if (e == cudaSuccess) e = lin::allow_smem<rows_kernel<DK, DV>>(RowsSmem<DK, DV>::END);
   if (e != cudaSuccess) return e;
-  if (grid) e = launch_next(parts_kernel<DK, DV>, grid, kPartsThreads, PartsSmem<DK, DV>::END, s, p, maps, sbase, whole);
+  if (grid) e = launch_next(parts_kernel<DK, DV, false>, grid, kPartsThreads, PartsSmem<DK, DV>::END, s, p, maps, sbase, whole);
   if (e == cudaSuccess) e = launch_linear_chain(p, sbase, part, nullptr, whole, s);
   if (e == cudaSuccess && grid)
     e = launch_next(rows_kernel<DK, DV>, grid, kRowsThreads, RowsSmem<DK, DV>::END, s, p, maps, sbase, part);
+  return e;
+}
+
+template <int DK, int DV>
+cudaError_t launch_shares(const LinearParams &p, const Maps &fwd, const Maps &rev, const int *sbase, float *whole,
+                          size_t items, cudaStream_t s) {
+  if (items * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
+  constexpr int smem = PartsSmem<DK, DV>::END;
+  cudaError_t e = lin::allow_smem<parts_kernel<DK, DV, false>>(smem);
+  if (e == cudaSuccess) e = lin::allow_smem<parts_kernel<DK, DV, true>>(smem);
+  if (e == cudaSuccess) e = launch_next(parts_kernel<DK, DV, false>, grid, kPartsThreads, smem, s, p, fwd, sbase, whole);
+  if (e == cudaSuccess) e = launch_next(parts_kernel<DK, DV, true>, grid, kPartsThreads, smem, s, p, rev, sbase, whole);
   return e;
 }
 
@@ -785,6 +801,25 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
                        : launch<128, 64>(p, maps, sbase, part, whole, segs, s);
   return p.dv == 128 ? launch<64, 128>(p, maps, sbase, part, whole, segs, s)
                      : launch<64, 64>(p, maps, sbase, part, whole, segs, s);
+}
+
+cudaError_t launch_linear_segment_states_tc(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole,
+                                            size_t segs, cudaStream_t s) {
+  using namespace lintc;
+  Maps fwd{}, rev{};
+  const size_t rows = segs * p.H * p.dk;
+  if (!(encode(&fwd.k, p.k, p.dk, p.Hk, p.N) && encode(&fwd.v, p.v, p.dv, p.H, p.N) &&
+        encode_f32(&fwd.part, part, p.dv, rows, p.dk) && encode(&rev.k, p.q, p.dk, p.Hk, p.N) &&
+        encode(&rev.v, p.d_o, p.dv, p.H, p.N) && encode_f32(&rev.part, rpart, p.dv, rows, p.dk)))
+    return cudaErrorNotSupported;
+  cudaError_t e;
+  if (p.dk == 128)
+    e = p.dv == 128 ? launch_shares<128, 128>(p, fwd, rev, sbase, whole, segs * p.H, s)
+                    : launch_shares<128, 64>(p, fwd, rev, sbase, whole, segs * p.H, s);
+  else
+    e = p.dv == 128 ? launch_shares<64, 128>(p, fwd, rev, sbase, whole, segs * p.H, s)
+                    : launch_shares<64, 64>(p, fwd, rev, sbase, whole, segs * p.H, s);
+  return e != cudaSuccess ? e : launch_linear_chain(p, sbase, part, rpart, whole, s);
 }
 
 }  // namespace kda

@@ -337,6 +337,39 @@ def test_segments_of_mixed_lengths(lengths):
     assert torch.equal(o, o2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("lengths,H,Hk,dk,dv,kw", [
+    ([3600], 1, 1, 128, 128, dict(state=False)),
+    ([9000, 1, 0, 5000], 2, 1, 64, 128, dict(pads=0.05)),
+    ([14 * 256 + 1], 2, 2, 128, 64, dict(decay="head")),
+    ([4300], 1, 1, 64, 64, dict(la_scale=20.0, pads=0.3)),
+], ids=["no_states", "mixed", "one_row_over", "strong_decays"])
+def test_backward_of_few_long_heads(lengths, H, Hk, dk, dv, kw):
+    """Few heads of long sequences: parts of them are swept from states of their own, twice with the same bits."""
+    c = lib.case(15, lengths, H, Hk, dk, dv, "bf16", **kw)
+    if c["pad_mask"] is not None:
+        lib.spoil_pads(c)
+    g = _check_backward(c)
+    again = _backward(c)
+    assert all(torch.equal(g[n], again[n]) for n in g)
+    less = _backward(c, want_grad_init_state=False)
+    assert less["dS0"] is None
+    assert all(torch.equal(g[n], less[n]) for n in ("dq", "dk", "dv", "dlog_alpha"))
+
+
+def test_backward_of_few_long_heads_with_waits_that_run_out():
+    c = lib.case(16, [4096], 1, 1, 128, 128, "bf16")
+    d = lib.to_cuda(c)
+    kda.debug_set_fault(0, 50)
+    try:
+        kda.linear_prefill_backward(d["q"], d["k"], d["v"], d["log_alpha"], d["cu_seqlens"], d["grad_o"],
+                                    init_state=d["init_state"])
+        assert kda.get_device_status() == kda.KDA_ERR_DEVICE_TIMEOUT
+        assert 41 <= kda.debug_timeout_site() <= 117
+    finally:
+        kda.debug_set_fault(0, 0)
+    _check_backward(c)
+
+
 def test_waits_that_run_out_are_reported():
     """A limit shorter than any load: the call returns, its status says so, and the next calls are whole."""
     c = lib.case(14, [500, 300], 4, 2, 128, 128, "bf16")
