@@ -86,7 +86,7 @@ struct SweepMaps {
   CUtensorMap k, v, s, out;      // REVERSE: q, grad_o, the states of the sweep before; the tiles written
 };
 
-template <int DK, int DV, bool REVERSE>
+template <int DK, int DV, bool REVERSE, bool CUT>
 __global__ void __launch_bounds__(kSweepThreads, 1)
 sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *sbase, const int *order,
              const int *segments, const float *start, const Table *tables, float *through) {
@@ -96,8 +96,8 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   if (device_error_latched(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
-  // whole sequences from the longest, or (segments) parts of them from the states in start
-  const int nitems = (segments ? segments[p.num_seqs] : p.num_seqs) * p.H * SL;
+  // whole sequences from the longest, or (CUT) segments of them from the states in start
+  const int nitems = (CUT ? segments[p.num_seqs] : p.num_seqs) * p.H * SL;
   // a block's items one after the other; the next one's rows are looked up an item ahead
   struct Item {
     int b, h, c0, begin, n, chunk0;      // b: sequence, or segment
@@ -108,7 +108,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
     if (i < nitems) {
       x.c0 = i % SL * kSlice;
       x.h = i / SL % p.H;
-      if (segments != nullptr) {
+      if constexpr (CUT) {
         const Segment sg = lin::locate(segments, p.num_seqs, i / SL / p.H);
         x.b = sg.id;
         x.begin = sg.begin;
@@ -125,7 +125,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   };
   Item next = look_up(0);
   // products: the last chunk's matters to the gradient of the initial state only
-  const bool to_init = REVERSE && segments == nullptr && p.g_init != nullptr;
+  const bool to_init = REVERSE && !CUT && p.g_init != nullptr;
   auto products = [&](const Item &x) { return to_init ? x.n : x.n - 1; };
   auto at = [&](const Item &x, int j) { return REVERSE ? x.n - 1 - j : j; };      // chunk of step j
   // first row of a step's first part in the state tiles
@@ -291,7 +291,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
     // ---------------- the state (thread: its row)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const float *in = segments ? start : REVERSE ? p.d_final : p.init_state;
+    const float *in = CUT ? start : REVERSE ? p.d_final : p.init_state;
     bool ok = true;
     int out = 0, m = 0;
     for (int k = 0; item_of(k) < nitems && ok; ++k) {
@@ -957,16 +957,19 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
 // knows the mean length only, which the longest sequence's steps are no fewer than.  Whole -> segments, d_k = d_v = 128:
 // one head of 2048, 4096, 8192, 32768 tokens 63 -> 67, 92 -> 68, 150 -> 74, 547 -> 116 us; 4 heads of 4096, 8192
 // 97 -> 85, 175 -> 114 us; 8 of 2048, 4096, 8192 67 -> 85, 113 -> 114, 201 -> 159 us; 16 of 4096, 8192 139 -> 160,
-// 239 -> 232 us; 8 heads of two times 2048 82 -> 116 us.
+// 239 -> 232 us; 8 heads of two times 2048 82 -> 116 us; 2 heads of 262144 4.22 -> 0.67 ms, 16 of 65536 1.56 -> 1.27 ms.
+// 32 heads have no SM for a second segment: two of 64 chunks made 16384 tokens slower, 600 -> 690 us.
 inline int sweep_chunks(const LinearParams &p) {
   constexpr int kSms = 148, kWorth = 25;
   const long long lanes = (long long)p.H * (p.dv / kSlice), chunks = ((long long)p.N + C - 1) / C;
-  if (p.num_seqs == 0 || lanes > kSms) return 0;
+  if (p.num_seqs == 0 || lanes > kSms / 2) return 0;      // no SM for a second segment
   const long long segs = kSms / lanes;
   long long per = (chunks + segs - 1) / segs;
   if (per < 2) per = 2;
   if (per > lin::kMaxPer) per = lin::kMaxPer;
-  return chunks >= (per + kWorth) * p.num_seqs ? (int)per : 0;
+  // an SM's steps: more than one segment's where the plan's longest segment leaves more segments than SMs
+  const long long steps = per * (((chunks + per - 1) / per * lanes + kSms - 1) / kSms);
+  return chunks >= (steps + kWorth) * p.num_seqs ? (int)per : 0;
 }
 
 struct BackwardWorkspace {
@@ -1002,6 +1005,23 @@ inline BackwardWorkspace backward_layout(const LinearParams &p) {
   return w;
 }
 
+template <int DK, int DV, bool CUT>
+cudaError_t launch_sweeps(const LinearParams &p, const SweepMaps &mf, const SweepMaps &mr, const int *sbase, const int *order,
+                          const int *segments, const float *part, const float *rpart, const Table *tables, float *through,
+                          size_t items, cudaStream_t s) {
+  constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END;
+  cudaError_t e = lin::allow_smem<sweep_kernel<DK, DV, false, CUT>>(fwd_smem);
+  if (e == cudaSuccess) e = lin::allow_smem<sweep_kernel<DK, DV, true, CUT>>(rev_smem);
+  const unsigned grid = (unsigned)(items < (size_t)sm_count() ? items : (size_t)sm_count());
+  if (e == cudaSuccess)
+    e = launch_next(sweep_kernel<DK, DV, false, CUT>, grid, kSweepThreads, fwd_smem, s, p, mf, sbase, order, segments, part,
+                    tables, nullptr);
+  if (e == cudaSuccess)
+    e = launch_next(sweep_kernel<DK, DV, true, CUT>, grid, kSweepThreads, rev_smem, s, p, mr, sbase, order, segments, rpart,
+                    tables, through);
+  return e;
+}
+
 template <int DK, int DV>
 cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const SweepMaps &mr, const GradMaps &mg,
                             const BackwardWorkspace &w, size_t items, cudaStream_t s) {
@@ -1010,13 +1030,10 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   float *through = reinterpret_cast<float *>(ws + w.through);
   const size_t sweeps = (w.per ? w.segs : (size_t)p.num_seqs) * p.H * (DV / kSlice);
   if (sweeps > 0x3FFFFFFFull || items * 2 * DK > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  constexpr int fwd_smem = SweepSmem<DK, false>::END, rev_smem = SweepSmem<DK, true>::END, grad_smem = GradSmem<DK, DV>::END;
-  cudaError_t e = lin::allow_smem<sweep_kernel<DK, DV, false>>(fwd_smem);
-  if (e == cudaSuccess) e = lin::allow_smem<sweep_kernel<DK, DV, true>>(rev_smem);
-  if (e == cudaSuccess) e = lin::allow_smem<grad_kernel<DK, DV>>(grad_smem);
+  constexpr int grad_smem = GradSmem<DK, DV>::END;
+  cudaError_t e = lin::allow_smem<grad_kernel<DK, DV>>(grad_smem);
   if (e != cudaSuccess) return e;
   Table *tables = reinterpret_cast<Table *>(ws + w.tables);
-  const unsigned sweep_grid = (unsigned)(sweeps < (size_t)sm_count() ? sweeps : (size_t)sm_count());
   const int *segments = nullptr;
   const float *part = nullptr, *rpart = nullptr;
   if (w.per) {
@@ -1028,11 +1045,8 @@ cudaError_t launch_backward(const LinearParams &p, const SweepMaps &mf, const Sw
   }
   if (e == cudaSuccess && items > 0) e = launch_next(table_kernel, (unsigned)((items + 7) / 8), 256, 0, s, p, sbase, tables);
   if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, false>, sweep_grid, kSweepThreads, fwd_smem, s, p, mf, sbase, order, segments, part,
-                    tables, nullptr);
-  if (e == cudaSuccess)
-    e = launch_next(sweep_kernel<DK, DV, true>, sweep_grid, kSweepThreads, rev_smem, s, p, mr, sbase, order, segments, rpart,
-                    tables, through);
+    e = w.per ? launch_sweeps<DK, DV, true>(p, mf, mr, sbase, order, segments, part, rpart, tables, through, sweeps, s)
+              : launch_sweeps<DK, DV, false>(p, mf, mr, sbase, order, segments, part, rpart, tables, through, sweeps, s);
   if (e != cudaSuccess || p.N == 0) return e;
   const bool shared = p.H != p.Hk;
   float *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
