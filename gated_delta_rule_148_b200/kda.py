@@ -207,9 +207,9 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _raw_stream(stream, device: int) -> int:
-    """The stream's handle; the device's current stream without an object made for it."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _current_stream(device: int) -> int:
+    """The device's current stream's handle, without an object made for it."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _check_cuda(name: str, t: Optional[torch.Tensor], dtype=None, shape=None):
@@ -555,6 +555,10 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha:
     query/key head h // (H // Hk)); log_alpha fp32 [N,H] (per token) or [H] (a constant of
     the head); cu_seqlens [B+1] int32; pad_mask [N] uint8 or None; init_state [B,H,dk,dv]
     fp32 or None.  Outputs are allocated here when not given."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return linear_prefill(q, k, v, log_alpha, cu_seqlens, pad_mask, init_state, o, final_state, workspace,
+                                  want_final_state)
     a = LinearArgs()
     N, B = q.shape[0], cu_seqlens.numel() - 1
     H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, N,
@@ -574,7 +578,7 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha:
     a.cu_seqlens, a.pad_mask, a.init_state = _ptr(cu_seqlens), _ptr(pad_mask), _ptr(init_state)
     a.o, a.final_state = _ptr(o), _ptr(final_state)
     workspace = _workspace(a, "kda_linear_prefill", (a.dtype, B, N, H, Hk, dk, dv), workspace, q)
-    st = (_lib or load()).kda_linear_prefill(ctypes.byref(a), _raw_stream(stream, q.get_device()))
+    st = (_lib or load()).kda_linear_prefill(ctypes.byref(a), _current_stream(q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill")
     return o, final_state
@@ -596,6 +600,9 @@ def linear_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: 
                   o: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One linear-attention step for each row (kda_linear_decode); ``state`` [B,H,dk,dv] fp32
     is updated in place.  q, k [B,Hk,dk], v [B,H,dv], log_alpha [B,H] or [H], mask [B] uint8."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return linear_decode(q, k, v, log_alpha, state, mask, o)
     a = LinearDecodeArgs()
     B = q.shape[0]
     H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, B, (state, mask, o))
@@ -607,7 +614,7 @@ def linear_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: 
         _check_cuda("o", o, q.dtype, (B, H, dv))
     a.B = B
     a.mask, a.state, a.o = _ptr(mask), _ptr(state), _ptr(o)
-    st = (_lib or load()).kda_linear_decode(ctypes.byref(a), _raw_stream(stream, q.get_device()))
+    st = (_lib or load()).kda_linear_decode(ctypes.byref(a), _current_stream(q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_decode")
     return o
@@ -619,6 +626,10 @@ def linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_s
     of q; grad_final_state [B,H,dk,dv] is fp32 or None.  Returns a dict: dq, dk, dv in the type
     of q (summed over the value heads of a shared query/key head), dlog_alpha fp32 in
     log_alpha's layout, dS0 fp32 (None unless wanted)."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_state, pad_mask,
+                                           init_state, want_grad_init_state, workspace)
     a = LinearBackwardArgs()
     N, B = q.shape[0], cu_seqlens.numel() - 1
     H, Hk, dk, dv = _linear_common(a, q, k, v, log_alpha, N,
@@ -637,7 +648,7 @@ def linear_prefill_backward(q, k, v, log_alpha, cu_seqlens, grad_o, grad_final_s
     a.grad_q, a.grad_k, a.grad_v = _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"])
     a.grad_log_alpha, a.grad_init_state = _ptr(g["dlog_alpha"]), _ptr(g["dS0"])
     workspace = _workspace(a, "kda_linear_prefill_backward", (a.dtype, B, N, H, Hk, dk, dv, a.decay), workspace, q)
-    st = (_lib or load()).kda_linear_prefill_backward(ctypes.byref(a), _raw_stream(stream, q.get_device()))
+    st = (_lib or load()).kda_linear_prefill_backward(ctypes.byref(a), _current_stream(q.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill_backward")
     return g
@@ -650,7 +661,7 @@ def _norm_rows(x: torch.Tensor) -> Tuple[int, int]:
     return (x.numel() // D if D else 0), D
 
 
-def _rms_norm(x, rows, D, weight, residual, eps, out_dtype, group, y, scale, residual_out, stream):
+def _rms_norm(x, rows, D, weight, residual, eps, out_dtype, group, y, scale, residual_out):
     _check_cuda("x", x)
     _check_cuda("weight", weight, torch.float32, (D,))
     _check_cuda("residual", residual, x.dtype, x.shape)
@@ -663,7 +674,7 @@ def _rms_norm(x, rows, D, weight, residual, eps, out_dtype, group, y, scale, res
     _check_device(x, weight, residual, y, scale, residual_out)
     a = RmsNormArgs(_dtype_code(x), out_dtype, rows, D, x.data_ptr(), _ptr(residual), _ptr(weight), eps, group,
                     y.data_ptr(), _ptr(scale), _ptr(residual_out))
-    st = (_lib or load()).kda_rms_norm(ctypes.byref(a), _raw_stream(stream, x.get_device()))
+    st = (_lib or load()).kda_rms_norm(ctypes.byref(a), _current_stream(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm")
     return residual_out
@@ -676,12 +687,15 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     residual is given.  x [.., D] bf16 or fp32, D a multiple of 8 up to 16384; weight [D] fp32
     or None (ones).  Returns (y, r), r None without a residual; residual_out may be the
     residual itself."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return rms_norm(x, weight, residual, eps, y, residual_out)
     rows, D = _norm_rows(x)
     if y is None:
         y = torch.empty_like(x)
     else:
         _check_cuda("y", y, x.dtype, x.shape)
-    return y, _rms_norm(x, rows, D, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out, stream)
+    return y, _rms_norm(x, rows, D, weight, residual, eps, _dtype_code(x), 0, y, None, residual_out)
 
 
 _BYTE_TYPES = {"e4m3": (KDA_E4M3, torch.float8_e4m3fn), "int8": (KDA_I8, torch.int8)}
@@ -695,6 +709,9 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     """rms_norm with an 8-bit output: quant "e4m3" or "int8", one fp32 scale per group of 32,
     64 or 128 columns, or per row (group 0).  Returns (y8 [.., D], scale [.., ceil(D / group)],
     r); y is approximately y8 * scale."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return rms_norm_quant(x, weight, residual, eps, quant, group, y, scale, residual_out)
     if quant not in _BYTE_TYPES:
         raise ValueError(f"quant must be one of {sorted(_BYTE_TYPES)}, got {quant!r}")
     code, tdt = _BYTE_TYPES[quant]
@@ -710,7 +727,7 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         scale = x.new_empty((*x.shape[:-1], n), dtype=torch.float32)
     else:
         _check_cuda("scale", scale, torch.float32, (*x.shape[:-1], n))
-    r = _rms_norm(x, rows, D, weight, residual, eps, code, group, y, scale, residual_out, stream)
+    r = _rms_norm(x, rows, D, weight, residual, eps, code, group, y, scale, residual_out)
     return y, scale, r
 
 
@@ -723,6 +740,9 @@ def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: t
     a residual); grad_residual is the gradient that reaches r along the residual stream.
     Returns (grad_x, grad_weight): the gradient of r, which is that of x and of the residual, in
     the type of x (grad_x may be grad_residual itself), and of weight [D] fp32."""
+    if stream is not None:      # outputs and workspace belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            return rms_norm_backward(x, weight, grad_y, grad_residual, eps, grad_x, want_grad_weight, workspace)
     rows, D = _norm_rows(x)
     _check_cuda("x", x)
     _check_cuda("weight", weight, torch.float32, (D,))
@@ -740,7 +760,7 @@ def rms_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], grad_y: t
     a.grad_x, a.grad_weight = _ptr(grad_x), _ptr(grad_weight)
     if want_grad_weight:
         workspace = _workspace(a, "kda_rms_norm_backward", (a.dtype, rows, D), workspace, x)
-    st = (_lib or load()).kda_rms_norm_backward(ctypes.byref(a), _raw_stream(stream, x.get_device()))
+    st = (_lib or load()).kda_rms_norm_backward(ctypes.byref(a), _current_stream(x.get_device()))
     if st != KDA_OK:
         raise KdaError(st, "kda_rms_norm_backward")
     return grad_x, grad_weight

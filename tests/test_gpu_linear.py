@@ -370,6 +370,50 @@ def test_backward_of_few_long_heads_with_waits_that_run_out():
     _check_backward(c)
 
 
+def test_calls_on_another_stream(monkeypatch):
+    """With a stream given, a call's outputs and workspace are made on it, so that nobody else gets their memory while
+    it runs; the results are those of the current stream."""
+    c = lib.case(17, [300, 70], 4, 2, 128, 64, "bf16")
+    d = lib.to_cuda(c)
+    x = torch.randn(70, 256, generator=torch.Generator().manual_seed(17)).cuda()
+    w = torch.ones(256).cuda()
+    other, made = torch.cuda.Stream(), []
+
+    def noted(fn):
+        def call(*args, **kw):
+            made.append(torch.cuda.current_stream())
+            return fn(*args, **kw)
+        return call
+
+    def step(stream):
+        state = d["init_state"].clone()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out = [*kda.linear_prefill(d["q"], d["k"], d["v"], d["log_alpha"], d["cu_seqlens"],
+                                   init_state=d["init_state"], stream=stream)]
+        g = kda.linear_prefill_backward(d["q"], d["k"], d["v"], d["log_alpha"], d["cu_seqlens"], d["grad_o"],
+                                        grad_final_state=d["grad_final_state"], init_state=d["init_state"], stream=stream)
+        out += [g[n] for n in sorted(g)]
+        rows = [d[n][:2].contiguous() for n in ("q", "k", "v", "log_alpha")]
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out += [kda.linear_decode(*rows, state, stream=stream), state]
+        out += [kda.rms_norm(x, w, stream=stream)[0]]
+        y, scale, _ = kda.rms_norm_quant(x, w, quant="int8", group=64, stream=stream)
+        out += [y, scale, *kda.rms_norm_backward(x, w, x, stream=stream)]
+        torch.cuda.synchronize()
+        return out
+
+    want = step(None)
+    monkeypatch.setattr(kda, "_workspace", noted(kda._workspace))
+    monkeypatch.setattr(kda, "_check_device", noted(kda._check_device))
+    got = step(other)
+    assert len(made) == 9 and all(s == other for s in made)
+    assert torch.cuda.current_stream() != other
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert kda.get_device_status() == kda.KDA_OK
+
+
 def test_waits_that_run_out_are_reported():
     """A limit shorter than any load: the call returns, its status says so, and the next calls are whole."""
     c = lib.case(14, [500, 300], 4, 2, 128, 128, "bf16")
