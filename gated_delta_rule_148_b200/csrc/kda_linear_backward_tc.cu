@@ -602,7 +602,9 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
                      xk[2] = {desc_kmajor(sx, DK, 0, 0), desc_kmajor(sx + L::X1, DK, 0, 0)}, mk = desc_kmajor(smm, C, 0, 0), mm = desc_mnmajor(smm, C, 0, 0);
       for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++it) {
         const uint32_t T_V = tm + t_v(it), T_Q = tm + t_q(it);
-        ok = wait(full, it, SITE_GRAD + 6);
+        // A takes the place of the item before's P and of the row sums beside it, which the third warpgroup reads last
+        if (it > 0) ok = wait(tab_free, it - 1, SITE_GRAD + 16);
+        ok = ok && wait(full, it, SITE_GRAD + 6);
         if (!ok) break;
         fence_after_sync();
 #pragma unroll

@@ -1,0 +1,37 @@
+"""CPU checks of the order in which the linear-attention kernels touch what their warps share, read off the
+source: orders that hold by timing alone never show in a result."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gated_delta_rule_148_b200", "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def _in_order(text, *what):
+    """Every one of ``what`` is in ``text``, each (its first occurrence from there) behind the one before."""
+    at = 0
+    for w in what:
+        i = text.find(w, at)
+        if i < 0:
+            return False
+        at = i + len(w)
+    return True
+
+
+def test_a_next_items_product_waits_for_the_row_sums_in_its_place():
+    """Gradients in bf16: the row sums q.E and k.F pass through columns of A's accumulator.  Stored, read by the third
+    warpgroup, told by tab_free, which the next item's A = K Q^T waits for."""
+    src = _source("kda_linear_backward_tc.cu")
+    grad = src[src.index("grad_kernel(LinearParams p"):]
+    products = grad[grad.index("if (warp == 16) {", grad.index("if (warp == 17) {")):grad.index("if (warp == 18) {")]
+    groups = grad[grad.index("if (warp == 18) {"):grad.index("// ======") if "// ======" in grad else len(grad)]
+    assert _in_order(groups, "tmem_st1(tm + lanes + T_A + 16 + y", "tmem_st_wait();", "fence_before_sync();", "mbar_arrive(summed);")
+    assert _in_order(groups, "wait.warp(summed, it", "fence_after_sync();", "tmem_ld2(tm + lanes + T_A + 16", "fence_before_sync();",
+                     "mbar_arrive(tab_free);")
+    assert groups.count("mbar_arrive(tab_free);") == 1 and groups.count("tmem_ld2(") == 1
+    before = products[:products.index("mma_bf16(tm + T_A,")]
+    assert _in_order(before, "if (it > 0) ok = wait(tab_free, it - 1", "if (!ok) break;", "fence_after_sync();")
