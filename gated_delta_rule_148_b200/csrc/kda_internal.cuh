@@ -250,4 +250,9 @@ __device__ __forceinline__ bool device_error_latched(const unsigned *err) {
   return *reinterpret_cast<const volatile unsigned *>(err) != 0u;
 }
 
+// The same answer for every thread of the block, all of which ask.  The word can be set between two warps' looks at it
+// (by another block whose wait ran out, by a call on another stream), and a block of which only some warps leave runs on
+// without its barriers, its tensor memory or its tables.
+__device__ __forceinline__ bool block_leaves(const unsigned *err) { return __syncthreads_or(device_error_latched(err)); }
+
 }  // namespace kda

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
   if (tid <= kMaxPer) slot[tid] = 0;
   __syncthreads();
   let_next_start();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const bool cached = p.num_seqs <= kCached;
   int wrong = 0, top = 0;
   for (int i = tid; i <= p.num_seqs; i += 1024) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, con
   extern __shared__ float sm[];
   __shared__ Decays dec;
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
@@ -358,7 +358,7 @@ template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + k
 __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
                                                     const float *whole) {
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const bool back = blockIdx.z != 0;
   const size_t bh = blockIdx.x, per = (size_t)p.dk * p.dv;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(Linear
   __shared__ Decays dec;
   float *sq = sm, *sk = sq + C * LK, *sv = sk + C * LK, *sS = sv + C * LV, *sP = sS + DK * LV;
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   __shared__ Decays dec;
   __shared__ float r_part[4 * C], k_part[4 * C], pair_sum[C], red[kThreads / 32];
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
 template <bool BF16>
 __global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float *gq32, const float *gk32) {
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = p.dk / 4;
   if (i >= (size_t)p.N * p.Hk * per) return;
   const int G = p.H / p.Hk, c = (int)(i % per);
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float 
 __global__ void __launch_bounds__(1024) head_decay_kernel(LinearParams p, const float *gla) {
   __shared__ double s[32];
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int h = blockIdx.x;
   double a = 0.0;
   for (int i = threadIdx.x; i < p.N; i += 1024) a += (double)gla[(size_t)h * p.N + i];

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreads) linear_decode_kernel(LinearDecodePar
   const int b = bh / p.H, h = bh % p.H;
   const int tid = threadIdx.x, cg = tid % TPR, rg = tid / TPR;
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   if (p.mask != nullptr && p.mask[b] == 0) {
     for (int j = tid; j < DVS; j += kThreads) store_elem<BF16>(p.o, (size_t)bh * DV + c0 + j, 0.f);
     return;

@@ -63,7 +63,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   using L = PartsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
@@ -341,7 +341,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   using L = RowsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);

@@ -146,7 +146,7 @@ template <int TPR, int VPT, int U, bool BF16, int OUT>
 __global__ void __launch_bounds__(block_threads(TPR), blocks_per_sm(TPR, BF16)) norm_kernel(NormParams p) {
   constexpr int NT = block_threads(TPR), GROUPS = NT / TPR;
   __shared__ float red[U * 32];
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int nvec = p.D / 8;
   const long long row0 = (long long)blockIdx.x * (GROUPS * U) + grp;
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(block_threads(TPR), back_blocks_per_sm(TPR, BF
   __shared__ float red[2 * 32];
   __shared__ float sum[GROUPS > 1 ? GROUPS * TPR * VPT * 8 : 1];
   let_next_start();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int nvec = p.D / 8;
   float w[VPT][8], dw[VPT][8];
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int pa
                                                        const unsigned *err) {
   __shared__ float s[32][33];
   after_previous();
-  if (device_error_latched(err)) return;
+  if (block_leaves(err)) return;
   const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
   float a = 0.f;
   if (c < D)

@@ -35,3 +35,27 @@ def test_a_next_items_product_waits_for_the_row_sums_in_its_place():
     assert groups.count("mbar_arrive(tab_free);") == 1 and groups.count("tmem_ld2(") == 1
     before = products[:products.index("mma_bf16(tm + T_A,")]
     assert _in_order(before, "if (it > 0) ok = wait(tab_free, it - 1", "if (!ok) break;", "fence_after_sync();")
+
+
+KERNELS = ("kda_linear.cu", "kda_linear_tc.cu", "kda_linear_backward_tc.cu", "kda_linear_decode.cu", "kda_norm.cu")
+
+
+def _kernel_starts(src):
+    """(name, body up to the first return) of each kernel."""
+    for m in re.finditer(r"__global__ void[^;{]*?(\w+)\(([^{;]*)\)\s*\{", src):
+        body = src[m.end():]
+        yield m.group(1), body[:body.index("return;")]
+
+
+def test_a_block_leaves_with_all_its_threads_or_none():
+    """On a latched error a kernel's threads leave together: the word may change between two warps' looks at it."""
+    assert "return __syncthreads_or(device_error_latched(err));" in _source("kda_internal.cuh")
+    for name in KERNELS:
+        src = _source(name)
+        assert "device_error_latched(" not in src, name
+        kernels = list(_kernel_starts(src))
+        assert len(kernels) == src.count("__global__"), name
+        for kernel, start in kernels:
+            # its first return, before any of its threads goes a way of its own
+            assert re.search(r"if \(block_leaves\((p\.)?err\)\) $", start), (name, kernel)
+            assert not re.search(r"if \((warp|w|lane)\b", start), (name, kernel)
