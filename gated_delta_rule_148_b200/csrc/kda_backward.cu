@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) intra_kernel(BackwardParams p, co
   float *vv = gT + DK * LP;                  // [C][DV]
   float *Ps = vv + C * DV, *Ms = Ps + C * LP, *Ts = Ms + C * LP;   // [C][LP]
   float *bs = Ts + C * LP;                   // [C]
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int H = p.H, h = blockIdx.x % H, tid = threadIdx.x;
   ChunkPos cp;
   if (!locate(p, cbase, blockIdx.x / H, cp)) return;
@@ -414,7 +414,7 @@ states_kernel(BackwardParams p, const int *cbase, const float *items, float *sta
   float *buf[2] = {sm, sm + SMc::BUF};
   float *S = sm + 2 * SMc::BUF;               // [DK][SLP]
   float *U = S + DK * SLP;                    // [C][SLP]
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = DV / NS, sl = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int b = bh / p.H, h = bh % p.H, n0 = sl * NS, tid = threadIdx.x;
   const int nch = (p.cu[b + 1] - p.cu[b] + C - 1) / C, cb = cbase[b];
@@ -505,7 +505,7 @@ dstates_kernel(BackwardParams p, const int *cbase, const float *items, float *ds
   float *Kt = sm + 2 * SMc::BUF, *Mt = Kt + C * LD;     // [C][LD], [C][C]
   float *dS = Kt + SMc::ABUF;             // [DK][SLP]
   float *dU = dS + DK * SLP;              // [C][SLP]
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = DV / NS, sl = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int b = bh / p.H, h = bh % p.H, n0 = sl * NS, tid = threadIdx.x, H = p.H;
   const int cs = p.cu[b], nrow = p.cu[b + 1] - cs;
@@ -798,7 +798,7 @@ grad_kernel(BackwardParams p, const int *cbase, const float *items, const float 
   extern __shared__ __align__(16) float sm[];
   float *Ts = sm + G::T0;
   float *dgam = sm + G::DGAM, *dbeta = sm + G::DBETA;
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int H = p.H, h = blockIdx.x % H, tid = threadIdx.x;
   const size_t gidx = blockIdx.x;
   ChunkPos cp;

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_kernel(ConvParams p, int spa
   __shared__ int vpos[kMaxSpan];
   __shared__ int wcnt[kThreads / 32];
   __shared__ Hist hist_sh;
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = KW;
   const int D = p.D, B = p.num_seqs;

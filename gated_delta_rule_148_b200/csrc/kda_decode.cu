@@ -43,9 +43,9 @@ decode_kernel(DecodeParams p) {
   const int cg = tid % TPR;                 // column group: columns 4cg..4cg+3
   const int rg = tid / TPR;                 // row group: rows rg*RPT ...
 
-  if (device_error_latched(p.err)) return;
   const bool active = (p.mask == nullptr) || (p.mask[b] != 0);
   if (!active) {
+    if (block_leaves(p.err)) return;
     for (int j = tid; j < DV; j += kDecodeThreads) store_elem<BF16>(p.o, (size_t)bh * DV + j, 0.f);
     return;
   }
@@ -55,6 +55,7 @@ decode_kernel(DecodeParams p) {
   float4 s[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) s[i] = __ldcs(&S[(size_t)(rg * RPT + i) * TPR + cg]);
+  if (block_leaves(p.err)) return;      // the loads are on their way meanwhile: 153.8 us for 256 rows, 155.8 asked before them
 
   for (int c = tid; c < DK; c += kDecodeThreads) {
     s_k[c] = load_elem<BF16>(p.k, (size_t)bh * DK + c);

@@ -100,7 +100,7 @@ template <int C>
 __global__ void __launch_bounds__(1024) index_kernel(PrefillParams p, const SeqSpan *spans, int *cbase) {
   __shared__ int warp_tot[32];
   __shared__ int carry;
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid == 0) carry = 0;
   __syncthreads();
@@ -259,7 +259,7 @@ merge_kernel(PrefillParams p, const SeqSpan *spans, const int *cb_in, const int 
   __shared__ __align__(8) uint64_t load_bar, mma_bar;
   __shared__ __align__(16) float gam_a[kDK], gam_b[kDK];
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int H = p.H;
   const int gch = blockIdx.x / H, h = blockIdx.x % H;
   if (gch >= cb_out[p.num_seqs]) return;
@@ -556,7 +556,7 @@ state_kernel(PrefillParams p, const SeqSpan *spans, const int *cbase, const unsi
   __shared__ __align__(8) uint64_t full_bar[NSLOT], free_bar[NSLOT];
   __shared__ int err_sh;
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = p.dv / NS;
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % p.H;

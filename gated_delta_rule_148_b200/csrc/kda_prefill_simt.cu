@@ -69,7 +69,7 @@ prefill_simt_kernel(PrefillParams p) {
   float *Us = sm + L::kU, *Ss = sm + L::kS, *Bs = sm + L::kB, *Ge = sm + L::kGe;
   constexpr int KS = L::KS, CS = L::CS, VS = L::VS;
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = p.dv / kDvTile;
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % p.H;
@@ -256,7 +256,7 @@ prefill_prepass_kernel(PrefillParams p, SeqSpan *spans) {
   const int tid = threadIdx.x;
   if (tid == 0) { s_bad = 0; s_first = INT_MAX; s_last = -1; s_count = 0; }
   __syncthreads();
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   int bad = 0;
   for (int i = tid; i <= p.num_seqs; i += blockDim.x) {
     const int v = p.cu[i];

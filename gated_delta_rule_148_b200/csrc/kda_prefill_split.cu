@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(1024) chunk_index_kernel(PrefillParams p, cons
                                                            int *cbase) {
   __shared__ int warp_tot[32];
   __shared__ int carry;
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid == 0) carry = 0;
   __syncthreads();
@@ -183,7 +183,7 @@ intra_kernel(PrefillParams p, const __grid_constant__ IntraMaps maps, const SeqS
   __shared__ __align__(16) float beta_sh[kC];   // read 16 bytes at a time by pack_tb
   __shared__ __align__(16) float part_sh[8][kDK];   // per row group of the decay prep
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int H = p.H;
   const int nitems = cbase[p.num_seqs] * Hg;
   if ((int)blockIdx.x >= nitems) return;
@@ -562,7 +562,7 @@ state_kernel(PrefillParams p, const SeqSpan *spans, const int *cbase, const unsi
   __shared__ __align__(8) uint64_t free_bar[2];
   __shared__ int err_sh;
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = p.dv / NS;
   const int tile = blockIdx.x % tiles;
   const int h = h0 + (blockIdx.x / tiles) % Hg;

@@ -153,7 +153,7 @@ prefill_tc_kernel(PrefillParams p, const __grid_constant__ TmaMaps maps) {
   const int wg = tid >> 7;           // column half
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
 
-  if (device_error_latched(p.err)) return;
+  if (block_leaves(p.err)) return;
   const int tiles = p.dv / kNV;
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % p.H;

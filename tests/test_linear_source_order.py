@@ -59,3 +59,12 @@ def test_a_block_leaves_with_all_its_threads_or_none():
             # its first return, before any of its threads goes a way of its own
             assert re.search(r"if \(block_leaves\((p\.)?err\)\) $", start), (name, kernel)
             assert not re.search(r"if \((warp|w|lane)\b", start), (name, kernel)
+
+
+def test_the_delta_rule_s_kernels_leave_in_whole_blocks_too():
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".cu"):
+            assert "device_error_latched(" not in _source(name), name
+    # after the state's loads, before any store
+    src = _source("kda_decode.cu")
+    assert _in_order(src, "__ldcs(", "if (block_leaves(p.err)) return;", "__stcs(", "store_elem")
