@@ -178,7 +178,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
 cudaError_t launch_linear_decode(const LinearDecodeParams &p, bool bf16, cudaStream_t s);
 // cu_seqlens check and table of segments of lo .. hi chunks; states at segment starts (and gradients at their ends).
 cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int chunk, int lo, int hi, int sms, int *order,
-                               cudaStream_t s);
+                               int *earlier, cudaStream_t s);
 cudaError_t launch_linear_chain(const LinearParams &p, const int *sbase, float *part, float *rpart,
                                 const float *whole, cudaStream_t s);
 // out: 0 the type of x, 1 e4m3, 2 int8.

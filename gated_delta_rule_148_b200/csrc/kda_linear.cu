@@ -161,10 +161,11 @@ __device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
 // r x SMs, since one SM has r + 1 of the segments up to there.  Against the best of 1, 2, .. 64 chunks, measured one by
 // one, the count so taken costs 0 to 5 % more on nine batches of 2048 to 32768 tokens and on 131072 tokens.  The
 // lengths are known here only.  order (may be null): the sequences from the longest to the shortest (unsorted beyond
-// those whose tables fit in shared memory).
+// those whose tables fit in shared memory).  earlier (may be null): the table of the call's plan before this one; both are
+// refused or none.
 constexpr int kCached = 1024;      // sequences whose tables fit in shared memory
 __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, int chunk, int lo, int hi, int sms,
-                                                    int *order) {
+                                                    int *order, int *earlier) {
   __shared__ int tot[32], carry, bad, most, slot[kMaxPer + 1], s_cu[kCached + 1], s_base[kCached + 1];
   __shared__ int lengths[32][kMaxPer + 1];
   __shared__ unsigned best;
@@ -173,7 +174,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
   if (tid <= kMaxPer) slot[tid] = 0;
   __syncthreads();
   let_next_start();
-  if (block_leaves(p.err)) return;
+  const bool stop = earlier != nullptr && earlier[p.num_seqs] == kRefused;
+  if (__syncthreads_or(stop || device_error_latched(p.err))) {
+    if (tid == 0) {
+      sbase[p.num_seqs] = kRefused;
+      if (earlier != nullptr) earlier[p.num_seqs] = kRefused;
+    }
+    return;
+  }
   const bool cached = p.num_seqs <= kCached;
   int wrong = 0, top = 0;
   for (int i = tid; i <= p.num_seqs; i += 1024) {
@@ -187,7 +195,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
   if (lane == 0 && top > 0) atomicMax(&most, (top + chunk - 1) / chunk);
   __syncthreads();
   if (bad) {
-    if (tid == 0) atomicOr(p.err, ERR_BIT_CHECK);
+    if (tid == 0) {
+      atomicOr(p.err, ERR_BIT_CHECK);
+      sbase[p.num_seqs] = kRefused;
+    }
     return;
   }
   const int *cu = cached ? s_cu : p.cu, *base = cached ? s_base : sbase;
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, con
   extern __shared__ float sm[];
   __shared__ Decays dec;
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
@@ -358,7 +369,7 @@ template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + k
 __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
                                                     const float *whole) {
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const bool back = blockIdx.z != 0;
   const size_t bh = blockIdx.x, per = (size_t)p.dk * p.dv;
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(Linear
   __shared__ Decays dec;
   float *sq = sm, *sk = sq + C * LK, *sv = sk + C * LK, *sS = sv + C * LV, *sP = sS + DK * LV;
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const int slices = p.dv / kSlice;
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
   __shared__ Decays dec;
   __shared__ float r_part[4 * C], k_part[4 * C], pair_sum[C], red[kThreads / 32];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
@@ -621,9 +632,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(LinearParams p, const in
 // ------------------------------------------------------------------ sums over shared inputs
 // dq, dk of a key head: the value heads' fp32 gradients added in order.  Thread: 4 columns.
 template <bool BF16>
-__global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float *gq32, const float *gk32) {
+__global__ void __launch_bounds__(256) share_kernel(LinearParams p, const int *sbase, const float *gq32,
+                                                    const float *gk32) {
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = p.dk / 4;
   if (i >= (size_t)p.N * p.Hk * per) return;
   const int G = p.H / p.Hk, c = (int)(i % per);
@@ -643,10 +655,10 @@ __global__ void __launch_bounds__(256) share_kernel(LinearParams p, const float 
 }
 
 // The gradient of a head's constant log_alpha: the sum over the tokens, in 64 bits and a fixed order.
-__global__ void __launch_bounds__(1024) head_decay_kernel(LinearParams p, const float *gla) {
+__global__ void __launch_bounds__(1024) head_decay_kernel(LinearParams p, const int *sbase, const float *gla) {
   __shared__ double s[32];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (call_ended(p, sbase)) return;
   const int h = blockIdx.x;
   double a = 0.0;
   for (int i = threadIdx.x; i < p.N; i += 1024) a += (double)gla[(size_t)h * p.N + i];
@@ -721,8 +733,8 @@ cudaError_t launch_grad_dims(const LinearParams &p, const int *sbase, const floa
 }  // namespace lin
 
 cudaError_t launch_linear_plan(const LinearParams &p, int *sbase, int chunk, int lo, int hi, int sms, int *order,
-                               cudaStream_t s) {
-  lin::plan_kernel<<<1, 1024, 0, s>>>(p, sbase, chunk, lo, hi < lin::kMaxPer ? hi : lin::kMaxPer, sms, order);
+                               int *earlier, cudaStream_t s) {
+  lin::plan_kernel<<<1, 1024, 0, s>>>(p, sbase, chunk, lo, hi < lin::kMaxPer ? hi : lin::kMaxPer, sms, order, earlier);
   return cudaGetLastError();
 }
 
@@ -751,7 +763,7 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   int *sbase = reinterpret_cast<int *>(w);
   float *whole = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs));
   float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4));
-  cudaError_t e = launch_linear_plan(p, sbase, tokens, 1, 1, 1, nullptr, s);
+  cudaError_t e = launch_linear_plan(p, sbase, tokens, 1, 1, 1, nullptr, nullptr, s);
   if (e != cudaSuccess) return e;
   e = launch_parts_chain(p, sbase, part, nullptr, whole, segs, tokens, s);
   if (e != cudaSuccess || p.N == 0) return e;
@@ -773,6 +785,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
   if (p.num_seqs == 0) return p.decay_head ? cudaMemsetAsync(p.gla, 0, (size_t)p.H * 4, s) : cudaSuccess;
   const bool shared = p.H != p.Hk;
   float *gq32 = nullptr, *gk32 = nullptr, *gla = p.gla;      // per value head; per head and token
+  const int *plan = static_cast<const int *>(p.ws);          // first in both workspaces
   cudaError_t e;
   if (bf16) {
     e = launch_linear_backward_tc(p, &gq32, &gk32, &gla, s);
@@ -792,7 +805,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
       gk32 = take((size_t)p.N * p.H * p.dk * 4);
     }
     if (p.decay_head) gla = take((size_t)p.N * p.H * 4);
-    if ((e = launch_linear_plan(p, sbase, C, 1, 1, 1, nullptr, s)) != cudaSuccess) return e;
+    if ((e = launch_linear_plan(p, sbase, C, 1, 1, 1, nullptr, nullptr, s)) != cudaSuccess) return e;
     e = launch_parts_chain(p, sbase, part, rpart, whole, segs, C, s);
     if (e != cudaSuccess) return e;
     if (p.N > 0) e = launch_grad_dims(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
@@ -802,12 +815,12 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
     if (shared) {
       const size_t n = ((size_t)p.N * p.Hk * (p.dk / 4) + 255) / 256;
       if (n > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-      e = bf16 ? launch_next(share_kernel<true>, dim3((unsigned)n, 2), 256, 0, s, p, gq32, gk32)
-               : launch_next(share_kernel<false>, dim3((unsigned)n, 2), 256, 0, s, p, gq32, gk32);
+      e = bf16 ? launch_next(share_kernel<true>, dim3((unsigned)n, 2), 256, 0, s, p, plan, gq32, gk32)
+               : launch_next(share_kernel<false>, dim3((unsigned)n, 2), 256, 0, s, p, plan, gq32, gk32);
       if (e != cudaSuccess) return e;
     }
   }
-  return p.decay_head ? launch_next(head_decay_kernel, (unsigned)p.H, 1024, 0, s, p, gla) : cudaSuccess;
+  return p.decay_head ? launch_next(head_decay_kernel, (unsigned)p.H, 1024, 0, s, p, plan, gla) : cudaSuccess;
 }
 
 }  // namespace kda

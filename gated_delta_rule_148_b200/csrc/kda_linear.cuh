@@ -31,6 +31,14 @@ struct alignas(16) Segment {
 };
 // Chunks in a segment at most, where segments have more than one: the plan counts the lengths in shared memory.
 constexpr int kMaxPer = 64;
+// In place of the number of segments, sbase[num_seqs]: the plan found the call's cu_seqlens invalid, or an error latched.
+// The word is the call's own, where the library's error word can be read and cleared (by kda_get_device_status on another
+// stream) between the plan and the kernels that index by its tables.
+constexpr int kRefused = -1;
+// Asked by every thread of the block, with the same answer for all, first of all in the kernels behind a plan.
+__device__ __forceinline__ bool call_ended(const LinearParams &p, const int *sbase) {
+  return __syncthreads_or(device_error_latched(p.err) | (sbase[p.num_seqs] == kRefused));      // both on their way at once
+}
 inline size_t max_segments(int N, int B, int tokens) { return (size_t)N / tokens + (size_t)B; }
 inline size_t table_bytes(int B, size_t segs) { return align256((size_t)(B + 1) * 4) + align256(segs * sizeof(Segment)); }
 __device__ __forceinline__ const Segment *segment_table(const int *sbase, int num_seqs) {

@@ -44,7 +44,7 @@ struct Table {
 
 __global__ void __launch_bounds__(256) table_kernel(LinearParams p, const int *sbase, Table *tables) {
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (lin::call_ended(p, sbase)) return;
   const size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= (size_t)sbase[p.num_seqs] * p.H) return;
   const int lane = threadIdx.x & 31;
@@ -93,7 +93,7 @@ sweep_kernel(LinearParams p, const __grid_constant__ SweepMaps maps, const int *
   using L = SweepSmem<DK, REVERSE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (lin::call_ended(p, sbase)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int SL = DV / kSlice;
   // whole sequences from the longest, or (CUT) segments of them from the states in start
@@ -445,7 +445,7 @@ grad_kernel(LinearParams p, const __grid_constant__ GradMaps maps, const int *sb
   using L = GradSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (lin::call_ended(p, sbase)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
@@ -1072,9 +1072,10 @@ cudaError_t launch_linear_backward_tc(const LinearParams &p, float **gq32, float
   *gk32 = shared ? reinterpret_cast<float *>(ws + w.gk32) : nullptr;
   *gla = p.decay_head ? reinterpret_cast<float *>(ws + w.gla) : p.gla;
   cudaError_t e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.sbase), C, 1, 1, 1,
-                                     reinterpret_cast<int *>(ws + w.order), s);
+                                     reinterpret_cast<int *>(ws + w.order), nullptr, s);
   if (e == cudaSuccess && w.per)
-    e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.seg_base), C, w.per, w.per, 1, nullptr, s);
+    e = launch_linear_plan(p, reinterpret_cast<int *>(ws + w.seg_base), C, w.per, w.per, 1, nullptr,
+                           reinterpret_cast<int *>(ws + w.sbase), s);
   if (e != cudaSuccess) return e;
   GradMaps mg{};
   SweepMaps mf{}, mr{};

@@ -63,7 +63,7 @@ parts_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase
   using L = PartsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (lin::call_ended(p, sbase)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float *wgt = reinterpret_cast<float *>(sm + L::WGT);
   uint32_t *valid = reinterpret_cast<uint32_t *>(sm + L::VALID);
@@ -341,7 +341,7 @@ rows_kernel(LinearParams p, const __grid_constant__ Maps maps, const int *sbase,
   using L = RowsSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   after_previous();
-  if (block_leaves(p.err)) return;
+  if (lin::call_ended(p, sbase)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nitems = sbase[p.num_seqs] * p.H;
   float2 *hl = reinterpret_cast<float2 *>(sm + L::HL);
@@ -789,7 +789,7 @@ cudaError_t launch_linear_prefill_tc(const LinearParams &p, cudaStream_t s) {
   int *sbase = reinterpret_cast<int *>(w);
   float *whole = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs));
   float *part = reinterpret_cast<float *>(w + lin::table_bytes(p.num_seqs, segs) + lin::align256(segs * p.H * 4));
-  cudaError_t e = launch_linear_plan(p, sbase, C, per, 64, sm_count(), nullptr, s);
+  cudaError_t e = launch_linear_plan(p, sbase, C, per, 64, sm_count(), nullptr, nullptr, s);
   if (e != cudaSuccess) return e;
   Maps maps{};
   if (p.N > 0 && !(encode(&maps.q, p.q, p.dk, p.Hk, p.N) && encode(&maps.k, p.k, p.dk, p.Hk, p.N) &&

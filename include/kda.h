@@ -526,7 +526,12 @@ size_t kda_rms_norm_backward_workspace_size(const kda_rms_norm_backward_args *ar
 kda_status kda_rms_norm_backward(const kda_rms_norm_backward_args *args, void *stream);
 
 /* Synchronise `stream`, then return and clear the error latched on the
- * current device by earlier kernels (KDA_OK if none). */
+ * current device by earlier kernels (KDA_OK if none).  The word is the
+ * device's, so an error of a call on another stream is returned and cleared
+ * too.  A linear-attention call that was refused on the device stays refused
+ * then (it keeps a mark of its own in its workspace); for kda_prefill,
+ * kda_prefill_noalloc and kda_prefill_backward ask only once the calls on
+ * other streams have ended. */
 kda_status kda_get_device_status(void *stream);
 
 /*

@@ -42,29 +42,44 @@ KERNELS = ("kda_linear.cu", "kda_linear_tc.cu", "kda_linear_backward_tc.cu", "kd
 
 def _kernel_starts(src):
     """(name, body up to the first return) of each kernel."""
-    for m in re.finditer(r"__global__ void[^;{]*?(\w+)\(([^{;]*)\)\s*\{", src):
-        body = src[m.end():]
+    for m in re.finditer(r"__global__ void(?:\s+__launch_bounds__\((?:[^()]|\([^()]*\))*\))?\s+(\w+)\(", src):
+        body = src[src.index("{", m.end()) + 1:]
         yield m.group(1), body[:body.index("return;")]
 
 
 def test_a_block_leaves_with_all_its_threads_or_none():
     """On a latched error a kernel's threads leave together: the word may change between two warps' looks at it."""
     assert "return __syncthreads_or(device_error_latched(err));" in _source("kda_internal.cuh")
+    assert "return __syncthreads_or(device_error_latched(p.err) | " in _source("kda_linear.cuh")
     for name in KERNELS:
         src = _source(name)
-        assert "device_error_latched(" not in src, name
+        assert src.count("device_error_latched(") == src.count("__syncthreads_or(stop || device_error_latched("), name
         kernels = list(_kernel_starts(src))
         assert len(kernels) == src.count("__global__"), name
         for kernel, start in kernels:
             # its first return, before any of its threads goes a way of its own
-            assert re.search(r"if \(block_leaves\((p\.)?err\)\) $", start), (name, kernel)
+            assert re.search(r"if \((block_leaves\((p\.)?err\)|(lin::)?call_ended\(p, sbase\))\) $", start) or \
+                re.search(r"if \(__syncthreads_or\(\w+ \|\| device_error_latched\(p\.err\)\)\) \{[^}]*\}\s*$", start), (name, kernel)
             assert not re.search(r"if \((warp|w|lane)\b", start), (name, kernel)
 
 
 def test_the_delta_rule_s_kernels_leave_in_whole_blocks_too():
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith(".cu"):
+        if name.endswith(".cu") and name not in KERNELS:
             assert "device_error_latched(" not in _source(name), name
     # after the state's loads, before any store
     src = _source("kda_decode.cu")
     assert _in_order(src, "__ldcs(", "if (block_leaves(p.err)) return;", "__stcs(", "store_elem")
+
+
+def test_kernels_behind_a_plan_look_at_the_call_s_own_word():
+    """cu_seqlens that a plan refuses: its tables are not to be read, whoever clears the library's error word meanwhile."""
+    for name in KERNELS[:3]:
+        src = _source(name)
+        for kernel, start in _kernel_starts(src):
+            if kernel == "plan_kernel":
+                plan = src[src.index("plan_kernel(LinearParams p"):]
+                assert _in_order(plan, "device_error_latched(", "sbase[p.num_seqs] = kRefused;", "return;", "if (bad) {",
+                                 "sbase[p.num_seqs] = kRefused;", "return;")
+            else:
+                assert "call_ended(p, sbase)) " in start, (name, kernel)
