@@ -216,11 +216,11 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
   return __uint_as_float(((unsigned)h) << 16);
 }
 
+// To nearest even; NaN stays NaN.
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
-  // round to nearest even; inputs here are finite
-  unsigned u = __float_as_uint(f);
-  u += 0x7FFFu + ((u >> 16) & 1u);
-  return (uint16_t)(u >> 16);
+  uint16_t u;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(f));
+  return u;
 }
 
 template <bool BF16>
