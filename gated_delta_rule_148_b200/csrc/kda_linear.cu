@@ -138,7 +138,7 @@ __device__ __forceinline__ void chunk_decays(Decays &d, const LinearParams &p, i
     if (lane >= o) s += y;
   }
   const double total = shfl_f64(s, 31);
-  const double b[2] = {s - x[1], s};
+  const double before = shfl_up_f64(s, 1), b[2] = {(lane ? before : 0.0) + x[0], s};
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = 2 * lane + e;

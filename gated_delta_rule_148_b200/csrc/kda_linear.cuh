@@ -72,12 +72,17 @@ __device__ __forceinline__ double shfl_f64(double x, int lane) {
                           __shfl_sync(0xFFFFFFFFu, __double2loint(x), lane));
 }
 
+// log2 of a decay: a step below 2^-400 counts as 2^-400, NaN stays NaN (a maximum would drop it, and a broken gate pass
+// for a reset).
+__device__ __forceinline__ double log2_step(float log_alpha) {
+  const double x = (double)log_alpha * 1.4426950408889634074;
+  return x < -400.0 ? -400.0 : x;
+}
 // log2 of token `pos`'s decay for head h; 0 past the end and at pads.
 __device__ __forceinline__ double log2_decay(const float *la, int decay_head, const uint8_t *mask, int pos, int end,
                                              int h, int H) {
   if (pos >= end || (mask != nullptr && mask[pos] == 0)) return 0.0;
-  const float x = la[decay_head ? (size_t)h : (size_t)pos * H + h];
-  return fmax((double)x * 1.4426950408889634074, -400.0);
+  return log2_step(la[decay_head ? (size_t)h : (size_t)pos * H + h]);
 }
 
 }  // namespace lin

@@ -168,7 +168,7 @@ __device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], 
   double s = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if ((d.bits >> e) & 1) s += fmax((double)d.x[e] * 1.4426950408889634074, -400.0);
+    if ((d.bits >> e) & 1) s += lin::log2_step(d.x[e]);
     b[e] = s;
   }
   double x = s;
@@ -178,8 +178,9 @@ __device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], 
     if (lane >= o) x += y;
   }
   total = lin::shfl_f64(x, 31);
+  const double before = lin::shfl_up_f64(x, 1);      // (x - s would carry a NaN back to the lane's rows before it)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] += x - s;
+  for (int e = 0; e < 4; ++e) b[e] += lane ? before : 0.0;
   word = d.bits << (4 * (lane & 7));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);

@@ -336,8 +336,10 @@ kda_status kda_prefill_backward(const kda_backward_args *args, void *stream);
  *   q, k         [N, Hk, dk]; v, o [N, H, dv]; 16-byte aligned.
  *   log_alpha    decay = KDA_DECAY_TOKEN: [N, H], one decay per token and head;
  *                decay = KDA_DECAY_HEAD: [H], a constant of the head.  Natural
- *                log, finite and <= 0 (not checked; other values give unspecified
- *                results).  A step below 2^-400 counts as 2^-400.
+ *                log, <= 0 (not checked; positive values give unspecified results).
+ *                A step below 2^-400 counts as 2^-400.  A NaN reaches o from its token
+ *                on, the states behind it and the gradients, as far as later decays of the
+ *                same head are not 0 in fp32.
  *   cu_seqlens   [B+1] int32 as for kda_prefill (checked on the device).
  *   pad_mask     [N] uint8, 1 = valid; NULL = all valid.
  *   init_state   [B, H, dk, dv] fp32, 16-byte aligned; NULL = 0.
