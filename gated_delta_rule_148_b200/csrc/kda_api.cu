@@ -592,7 +592,7 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
 }
 
 size_t kda_rms_norm_backward_workspace_size(const kda_rms_norm_backward_args *a) {
-  if (!a || norm_sizes(a->dtype, a->rows, a->D, a->eps) != KDA_OK) return 0;
+  if (!a || norm_sizes(a->dtype, a->rows, a->D, 0.f) != KDA_OK) return 0;
   return norm_backward_workspace(a->rows, a->D);
 }
 

@@ -533,9 +533,10 @@ def _workspace(a, name: str, sizes, workspace, like):
         nbytes = _workspace_sizes.get((name, sizes))
         if nbytes is None:
             nbytes = int(getattr(_lib or load(), name + "_workspace_size")(ctypes.byref(a)))
-            if len(_workspace_sizes) >= 4096:
-                _workspace_sizes.clear()
-            _workspace_sizes[(name, sizes)] = nbytes
+            if nbytes:      # 0 where the library refuses the call: not kept
+                if len(_workspace_sizes) >= 4096:
+                    _workspace_sizes.clear()
+                _workspace_sizes[(name, sizes)] = nbytes
         workspace = like.new_empty(max(nbytes, 1), dtype=torch.uint8)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()

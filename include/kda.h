@@ -524,6 +524,7 @@ typedef struct {
   size_t workspace_bytes;
 } kda_rms_norm_backward_args;
 
+/* Bytes of workspace (reads dtype, rows and D).  0 if args is NULL or these are invalid. */
 size_t kda_rms_norm_backward_workspace_size(const kda_rms_norm_backward_args *args);
 kda_status kda_rms_norm_backward(const kda_rms_norm_backward_args *args, void *stream);
 
