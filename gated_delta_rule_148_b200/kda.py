@@ -538,6 +538,8 @@ def _workspace(a, name: str, sizes, workspace, like):
                     _workspace_sizes.clear()
                 _workspace_sizes[(name, sizes)] = nbytes
         workspace = like.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    elif not workspace.is_contiguous():      # its count of elements is taken for the bytes behind its address
+        raise ValueError("workspace must be contiguous")
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
