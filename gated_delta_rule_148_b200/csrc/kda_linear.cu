@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(LinearParams p, int *sbase, 
 // Block: segment x head x 64 columns of d_v.  REVERSE: q, do and the rows in reverse.
 template <int DK, bool REVERSE>
 __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment &sg, int seg, int h, int c0,
-                                            float *part, float *whole, float *sm, Decays &dec, int tokens) {
+                                            float *part, float *whole, float *sm, Decays &dec) {
   constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
   float *sk = sm, *sv = sm + C * LK;
   const int warp = threadIdx.x >> 5, m0 = (warp & 3) * 16 * MT, n0 = (warp >> 2) * 32;
@@ -349,7 +349,7 @@ __device__ __forceinline__ void parts_block(const LinearParams &p, const Segment
 
 template <int DK>
 __global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, const int *sbase, float *part, float *rpart,
-                                                         float *whole, int tokens) {
+                                                         float *whole) {
   extern __shared__ float sm[];
   __shared__ Decays dec;
   after_previous();
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kPartThreads) parts_kernel(LinearParams p, con
   const int seg = blockIdx.x / (p.H * slices), h = blockIdx.x / slices % p.H, c0 = (blockIdx.x % slices) * kSlice;
   if (seg >= sbase[p.num_seqs]) return;
   const Segment sg = locate(sbase, p.num_seqs, seg);
-  if (blockIdx.y == 0) parts_block<DK, false>(p, sg, seg, h, c0, part, whole, sm, dec, tokens);
-  else parts_block<DK, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec, tokens);
+  if (blockIdx.y == 0) parts_block<DK, false>(p, sg, seg, h, c0, part, whole, sm, dec);
+  else parts_block<DK, true>(p, sg, seg, h, c0, rpart, nullptr, sm, dec);
 }
 template <int DK> constexpr size_t parts_smem() { return (size_t)C * (DK + 4 + kSlice + 4) * 4; }
 
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(256) chain_kernel(LinearParams p, const int *s
 
 // ------------------------------------------------------------------ prefill rows
 template <int DK>
-__global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(LinearParams p, const int *sbase, const float *start, int tokens) {
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) rows_kernel(LinearParams p, const int *sbase, const float *start) {
   constexpr int LK = DK + 4, LV = kSlice + 4, MT = DK / 64;
   extern __shared__ float sm[];
   __shared__ Decays dec;
@@ -687,30 +687,30 @@ size_t state_bytes(const LinearParams &p, size_t segs) { return align256(segs * 
 
 template <int DK>
 cudaError_t launch_parts(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole, size_t segs,
-                         int tokens, cudaStream_t s) {
+                         cudaStream_t s) {
   const size_t blocks = segs * p.H * (p.dv / kSlice);
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<parts_kernel<DK>>(parts_smem<DK>());
   if (e != cudaSuccess) return e;
   if (blocks == 0) return cudaSuccess;
   return launch_next(parts_kernel<DK>, dim3((unsigned)blocks, rpart ? 2 : 1), kPartThreads, parts_smem<DK>(), s, p, sbase,
-                     part, rpart, whole, tokens);
+                     part, rpart, whole);
 }
 cudaError_t launch_parts_chain(const LinearParams &p, const int *sbase, float *part, float *rpart, float *whole,
-                               size_t segs, int tokens, cudaStream_t s) {
-  const cudaError_t e = p.dk == 128 ? launch_parts<128>(p, sbase, part, rpart, whole, segs, tokens, s)
-                                    : launch_parts<64>(p, sbase, part, rpart, whole, segs, tokens, s);
+                               size_t segs, cudaStream_t s) {
+  const cudaError_t e = p.dk == 128 ? launch_parts<128>(p, sbase, part, rpart, whole, segs, s)
+                                    : launch_parts<64>(p, sbase, part, rpart, whole, segs, s);
   if (e != cudaSuccess) return e;
   return launch_linear_chain(p, sbase, part, rpart, whole, s);
 }
 
 template <int DK>
-cudaError_t launch_rows(const LinearParams &p, const int *sbase, const float *start, size_t segs, int tokens,
+cudaError_t launch_rows(const LinearParams &p, const int *sbase, const float *start, size_t segs,
                         cudaStream_t s) {
   const cudaError_t e = allow_smem<rows_kernel<DK>>(rows_smem<DK>());
   if (e != cudaSuccess) return e;
   return launch_next(rows_kernel<DK>, (unsigned)(segs * p.H * (p.dv / kSlice)), kThreads, rows_smem<DK>(), s, p, sbase,
-                     start, tokens);
+                     start);
 }
 
 template <int DK, int DV>
@@ -765,9 +765,9 @@ cudaError_t launch_linear_prefill(const LinearParams &p, bool bf16, cudaStream_t
   float *part = reinterpret_cast<float *>(w + table_bytes(p.num_seqs, segs) + align256(segs * p.H * 4));
   cudaError_t e = launch_linear_plan(p, sbase, tokens, 1, 1, 1, nullptr, nullptr, s);
   if (e != cudaSuccess) return e;
-  e = launch_parts_chain(p, sbase, part, nullptr, whole, segs, tokens, s);
+  e = launch_parts_chain(p, sbase, part, nullptr, whole, segs, s);
   if (e != cudaSuccess || p.N == 0) return e;
-  return p.dk == 128 ? launch_rows<128>(p, sbase, part, segs, tokens, s) : launch_rows<64>(p, sbase, part, segs, tokens, s);
+  return p.dk == 128 ? launch_rows<128>(p, sbase, part, segs, s) : launch_rows<64>(p, sbase, part, segs, s);
 }
 
 size_t linear_backward_workspace(const LinearParams &p, bool bf16) {
@@ -806,7 +806,7 @@ cudaError_t launch_linear_backward(const LinearParams &p, bool bf16, cudaStream_
     }
     if (p.decay_head) gla = take((size_t)p.N * p.H * 4);
     if ((e = launch_linear_plan(p, sbase, C, 1, 1, 1, nullptr, nullptr, s)) != cudaSuccess) return e;
-    e = launch_parts_chain(p, sbase, part, rpart, whole, segs, C, s);
+    e = launch_parts_chain(p, sbase, part, rpart, whole, segs, s);
     if (e != cudaSuccess) return e;
     if (p.N > 0) e = launch_grad_dims(p, sbase, part, rpart, gq32, gk32, gla, segs, s);
     if (e != cudaSuccess) return e;

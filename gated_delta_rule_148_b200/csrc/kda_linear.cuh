@@ -17,8 +17,6 @@
 namespace kda {
 namespace lin {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Segment tables: sbase[b] = segments of the sequences before b (b <= num_seqs); behind them the segments in the order

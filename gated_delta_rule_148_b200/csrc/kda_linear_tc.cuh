@@ -162,8 +162,7 @@ __device__ __forceinline__ RawDecays load_decays(const LinearParams &p, int pos0
   return d;
 }
 // Inclusive sums b of log2 a, the total; word: lanes 0, 8, 16, 24 get the bits of rows 32 (lane / 8) .. + 31.
-// Returns whether all 128 rows are real tokens.
-__device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], double &total, uint32_t &word) {
+__device__ __forceinline__ void scan_decays(const RawDecays &d, double (&b)[4], double &total, uint32_t &word) {
   const int lane = threadIdx.x & 31;
   double s = 0.0;
 #pragma unroll
@@ -185,7 +184,6 @@ __device__ __forceinline__ bool scan_decays(const RawDecays &d, double (&b)[4], 
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  return __all_sync(0xFFFFFFFFu, d.bits == 0xFu);
 }
 
 // A block's n-th item of a list: there and back over the blocks, so that the blocks with the longest item of one

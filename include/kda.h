@@ -324,8 +324,11 @@ kda_status kda_prefill_backward(const kda_backward_args *args, void *stream);
  *   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_t = exp(log_alpha_t)
  * per sequence b and value head h, with the state S d_k x d_v in fp32.  The same
  * conventions as kda_prefill: packed variable-length batch, pads are identity
- * steps with o = 0 whatever they hold (nothing at a pad is read but its mask),
- * optional initial and final state.  Any result is independent of how the
+ * steps with o = 0 whatever they hold (their memory may be read, but nothing there
+ * has an effect), optional initial and final state.  An infinity or NaN in q, k or v of
+ * a token that is no pad may reach o and the gradients of any token of its chunk (128
+ * rows in bf16, 64 in fp32), earlier ones too: their weights are 0 there, not left
+ * out.  Any result is independent of how the
  * library cuts sequences beyond rounding, and the same call gives the same bits.
  *
  * Fields (device pointers, caller-owned):
