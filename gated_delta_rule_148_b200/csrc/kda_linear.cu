@@ -36,8 +36,8 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // The sums of 16 columns start from zero and are added by fp32 additions that round: chained into the accumulator, each
-// of 3 K / 8 products lost up to 2^-23 of the whole sum, as a truncated addition does.  Errors of the gradients against 64 bits
-// 0.6 - 1.6e-6 -> 1.4 - 2.1e-7 for 2 - 8 % of the time (4096 tokens, 16 heads of 128: prefill 369 -> 396 us, backward
+// of 3 K / 8 products lost up to 2^-23 of the whole sum, as a truncated addition does.  Errors against 64 bits
+// 0.6 - 1.6e-6 -> 0.6 - 3.2e-7 for 2 - 8 % of the time (4096 tokens, 16 heads of 128: prefill 369 -> 396 us, backward
 // 709 -> 768 us; sums of 8 columns 397 and 787 us, 1.3 - 2.0e-7).
 // acc[m][n] += A B for a warp's 16 MT x 8 NT tile over K; a(r, k) and b(k, n) read the operands.
 // Entry acc[m][n][e] is row 16 m + lane / 4 + 8 (e / 2), column 8 n + 2 (lane % 4) + e % 2.
@@ -157,7 +157,7 @@ __device__ __forceinline__ float pair_decay(const Decays &d, int t, int s) {
 // Checks cu_seqlens (nothing else runs if it is invalid), takes the number of chunks in a segment, lo .. hi, and fills
 // the segment table, longest segments first.  In the time of a chunk on one SM: a segment costs its chunks and about a half
 // more (its state in and out), and its share of the state half of up to six chunks (a share ends where the decays
-// are 0 in fp32).  The longest run over the SMs is no shorter than the mean, nor than r + 1 times the segment in place
+// are 0 in fp32; six fits a mean log of -0.18 a token, slower decays walk the whole segment).  The longest run over the SMs is no shorter than the mean, nor than r + 1 times the segment in place
 // r x SMs, since one SM has r + 1 of the segments up to there.  Against the best of 1, 2, .. 64 chunks, measured one by
 // one, the count so taken costs 0 to 5 % more on nine batches of 2048 to 32768 tokens and on 131072 tokens.  The
 // lengths are known here only.  order (may be null): the sequences from the longest to the shortest (unsorted beyond

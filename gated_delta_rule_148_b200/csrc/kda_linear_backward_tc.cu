@@ -18,8 +18,9 @@
 //           M lies in shared memory once and is read K-major (M Q) and MN-major (M^T K); P stays in
 //           TMEM over A.  E, F and U are scaled in TMEM, where the second products add to them; on
 //           the way the row sums q.E and k.F give the decays' gradients, in fp32.
-// 16384 tokens, 32 heads, d = 128: sweeps 128 and 147 us (0.54 and 0.81 GB; a step of a chunk takes 1 us, a chain of
-// load, weights, products and state), grad 310 us (1.44 GB, 220 us at the copy rate).
+// 16384 tokens, 32 heads, d = 128: sweeps 131 and 157 us (0.54 and 0.81 GB; a step of a chunk takes 1 us, a chain of
+// load, weights, products and state), grad 292 us (1.44 GB, 220 us at the copy rate).  Slow decays change nothing here
+// unless segments are swept (8192 tokens, 4 heads: 116 -> 131 us).
 // The grad kernel is a persistent block per SM: a load/store warp, an MMA thread, a warp that
 // prepares decays, and four warpgroups, whose loops over 32 columns are not unrolled: 96 registers a thread hold one
 // round, and the addresses of all rounds spilled (636 -> 608 us for the whole pass over 16384 tokens, 32 heads).

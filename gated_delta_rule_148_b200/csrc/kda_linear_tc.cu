@@ -15,9 +15,10 @@
 // next sequence are cleared or masked by their own threads.  Off the diagonal a warp's 32 rows share a reference row R
 // before them, 2^{b_t - b_s} = 2^{b_t - R} 2^{R - b_s}, both factors <= 1: one exponential per row and column
 // instead of one per pair.
-// 131072 tokens, 32 heads, d = 128: shares 75 us (the decays end a share after five chunks), chain 13 us, rows 1.04 ms
-// (4.3 GB).  Rows is bound by turns of products and warpgroups (1.04 ms without any load or store, 0.67 ms for these
-// alone) and by power: SM clocks fall to 1.7 - 1.85 GHz.  Chunks of 128: a state's way through TMEM and shared memory
+// 131072 tokens, 32 heads, d = 128: shares 78 us where the decays end a share after about five chunks (a mean log of
+// -0.18 a token), 560 us where they walk whole segments (-2^-8 a token: keys and values are read twice, 2.1 GB more);
+// chain 16 us, rows 1.02 ms (4.3 GB).  Rows is bound by turns of products and warpgroups (the tensor pipe is busy a third
+// of the time; 1.04 ms without any load or store, 0.67 ms for these alone), then by power: SM clocks fall to 1.7 - 1.85 GHz.  Chunks of 128: a state's way through TMEM and shared memory
 // costs the same for any chunk, the pairs inside grow with it, and 128 rows are the products' own height.
 #include <cmath>
 
