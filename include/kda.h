@@ -481,7 +481,8 @@ kda_status kda_linear_prefill_backward(const kda_linear_backward_args *args, voi
  *                y / scale (as y times the reciprocal of scale, both in fp32) rounded to nearest
  *                even.  A NaN in a group makes its scale NaN.
  *   residual_out [rows, D] r, or NULL; needs residual; may be the same pointer as residual.
- * The mean is taken in fp32: a row whose squares sum to more than 3.4e38 gives y = 0.
+ * The mean is taken in fp32: a row whose squares sum to more than 3.4e38 gives y = 0, and
+ * with eps = 0 one whose squares sum to less than 1.2e-38 loses digits, down to y infinite.
  * Outputs may not otherwise overlap an input or each other.  Allocates nothing.
  */
 typedef struct {
