@@ -1,8 +1,9 @@
 """Relative 2-norms of whole outputs against the 64-bit recurrence: the accuracy that the header states, near enough that a
-part left out of a product shows (bounds derived in linear_testlib)."""
+part left out of a product shows (bounds derived in linear_accuracy_lib)."""
 import pytest
 import torch
 
+import linear_accuracy_lib as bounds
 import linear_testlib as lib
 from gated_delta_rule_148_b200 import kda
 
@@ -18,11 +19,11 @@ def _check(c):
                                     grad_final_state=d["grad_final_state"], pad_mask=d["pad_mask"], init_state=d["init_state"])
     assert kda.get_device_status() == kda.KDA_OK
     (ro, rs), rg = lib.prefill(c), lib.backward(c)
-    wide = lib.BF16_NORM if bf16 else lib.FP32_NORM
-    off = {"o": (lib.relative(o, ro), wide), "final_state": (lib.relative(s, rs), lib.FP32_NORM),
-           "dS0": (lib.relative(g["dS0"], rg["dS0"]), lib.FP32_NORM),
-           "dlog_alpha": (lib.relative(g["dlog_alpha"], rg["dlog_alpha"]), lib.TWO_PART_NORM if bf16 else lib.FP32_NORM)}
-    off.update({n: (lib.relative(g[n], rg[n]), wide) for n in ("dq", "dk", "dv")})
+    wide = bounds.BF16_NORM if bf16 else bounds.FP32_NORM
+    off = {"o": (bounds.relative(o, ro), wide), "final_state": (bounds.relative(s, rs), bounds.FP32_NORM),
+           "dS0": (bounds.relative(g["dS0"], rg["dS0"]), bounds.FP32_NORM),
+           "dlog_alpha": (bounds.relative(g["dlog_alpha"], rg["dlog_alpha"]), bounds.TWO_PART_NORM if bf16 else bounds.FP32_NORM)}
+    off.update({n: (bounds.relative(g[n], rg[n]), wide) for n in ("dq", "dk", "dv")})
     print({n: f"{x:.2e}" for n, (x, _) in off.items()})
     assert all(x <= bound for x, bound in off.values()), off
 
@@ -51,9 +52,9 @@ def test_decode(dtype, rows):
     d = lib.to_cuda(c)
     o = kda.linear_decode(d["q"], d["k"], d["v"], d["log_alpha"], d["init_state"])
     ro, rs = lib.prefill(c)
-    assert lib.relative(d["init_state"], rs) <= lib.FP32_NORM
+    assert bounds.relative(d["init_state"], rs) <= bounds.FP32_NORM
     # no operand is rounded: the output alone
-    assert lib.relative(o, ro) <= (3.0 ** -0.5 * lib.HALF_BF16 if dtype == "bf16" else lib.FP32_NORM)
+    assert bounds.relative(o, ro) <= (3.0 ** -0.5 * lib.HALF_BF16 if dtype == "bf16" else bounds.FP32_NORM)
 
 
 def test_captured_calls_write_every_output_on_every_replay():
@@ -108,4 +109,4 @@ def test_norm_weight_gradient_of_many_wide_rows(dtype, rows, D):
     steps = rows / 148 + 1 + 296 / 32 + 32
     assert ((dw.double() - terms.sum(0)).abs() <= (2.0 ** -19 + steps * 2.0 ** -24) * terms.abs().sum(0)).all()
     # in the 2-norm the steps' errors are independent, half a step at most each, of sums that grow with the root of the rows
-    assert lib.relative(dw, terms.sum(0).cpu()) <= steps ** 0.5 * 2.0 ** -24 + 2.0 ** -22
+    assert bounds.relative(dw, terms.sum(0).cpu()) <= steps ** 0.5 * 2.0 ** -24 + 2.0 ** -22

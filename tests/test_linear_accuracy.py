@@ -3,6 +3,7 @@ one part fewer would: the mistake is planted in the oracle."""
 import pytest
 import torch
 
+import linear_accuracy_lib as bounds
 import linear_testlib as lib
 
 
@@ -28,8 +29,8 @@ def _state(c, parts):
 def test_states_need_three_parts(la_scale):
     c = lib.case(100, [128], 4, 4, 128, 128, "bf16", la_scale=la_scale)
     ref = _state(c, None)
-    assert lib.relative(_state(c, 3), ref) < lib.FP32_NORM / 8
-    assert lib.relative(_state(c, 2), ref) > 2 * lib.FP32_NORM
+    assert bounds.relative(_state(c, 3), ref) < bounds.FP32_NORM / 8
+    assert bounds.relative(_state(c, 2), ref) > 2 * bounds.FP32_NORM
 
 
 def test_decay_gradients_need_two_parts():
@@ -37,8 +38,8 @@ def test_decay_gradients_need_two_parts():
     g = torch.Generator().manual_seed(101)
     S, D = (torch.randn(64, 128, 128, generator=g, dtype=torch.float64) for _ in range(2))
     ref = (S * D).sum((1, 2))
-    assert lib.relative((_parts(S, 2) * _parts(D, 2)).sum((1, 2)), ref) < lib.TWO_PART_NORM
-    assert lib.relative((_parts(S, 1) * _parts(D, 2)).sum((1, 2)), ref) > 8 * lib.TWO_PART_NORM
+    assert bounds.relative((_parts(S, 2) * _parts(D, 2)).sum((1, 2)), ref) < bounds.TWO_PART_NORM
+    assert bounds.relative((_parts(S, 1) * _parts(D, 2)).sum((1, 2)), ref) > 8 * bounds.TWO_PART_NORM
 
 
 def test_bf16_outputs_allow_one_rounded_operand():
@@ -47,5 +48,5 @@ def test_bf16_outputs_allow_one_rounded_operand():
     P, V = (torch.randn(64, 128, 128, generator=g, dtype=torch.float64) for _ in range(2))
     V = V.bfloat16().double()
     ref = P @ V
-    assert lib.relative((_parts(P, 1) @ V).bfloat16(), ref) < lib.BF16_NORM
-    assert lib.relative((_parts(P, 1) @ V.to(torch.float8_e4m3fn).double()).bfloat16(), ref) > 4 * lib.BF16_NORM
+    assert bounds.relative((_parts(P, 1) @ V).bfloat16(), ref) < bounds.BF16_NORM
+    assert bounds.relative((_parts(P, 1) @ V.to(torch.float8_e4m3fn).double()).bfloat16(), ref) > 4 * bounds.BF16_NORM
